@@ -193,7 +193,7 @@ def _codes(x):
 
 def _quantise(x):
     c, e = _codes(x)
-    return c[:, 0::2] | (c[:, 1::2] << 4), (e + 127).to(torch.uint8)
+    return (c[:, 0::2] | (c[:, 1::2] << 4)).to(torch.uint8), (e + 127).to(torch.uint8)
 
 
 def _values(codes, e, dtype):
