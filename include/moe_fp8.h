@@ -64,6 +64,15 @@ typedef enum {
                                 out FP32 [M_total, N] */
 } moe_epilogue;
 
+/* What the MXFP4 grouped GEMM writes (grouped_gemm_mxfp4). */
+typedef enum {
+    MOE_MX_STORE_F32 = 0,    /* out = C, FP32 [M_total, N] */
+    MOE_MX_STORE_BF16 = 1,   /* out = C, bf16 [M_total, N] */
+    MOE_MX_SWIGLU_BF16 = 2,  /* out = h = SiLU(C_gate) * C_up, bf16 [M_total, N/2] */
+    MOE_MX_SWIGLU_QUANT = 3  /* the same h, quantised as by mxfp4_quant_1x32 into
+                                out_q [M_total, N/4 bytes] + out_scale [M_total, N/64] */
+} moe_mx_epilogue;
+
 const char* moe_status_string(int status);
 const char* moe_last_error(void);
 /* Library version: major*10000 + minor*100 + patch. */
@@ -468,6 +477,94 @@ int moe_wgrad(const int32_t* kb_start, int G, int n_kb, int d, int I, const uint
               const uint8_t* hT_q, const float* hT_scale, const uint8_t* dzT_q, const float* dzT_scale,
               const uint8_t* xT_q, const float* xT_scale, float* dw13, float* dw2, void* ws, size_t ws_bytes,
               moe_stream_t stream);
+
+/* ------------------------------------------------------------------ residual + RMS norm
+ * moe_add_rmsnorm -- what comes before the layer: per row t of d values
+ *   h    = x + residual                      (FP32; h = x when residual is NULL)
+ *   rstd = 1 / sqrt(mean(h^2) + eps)         (FP32, of the unrounded h)
+ *   y    = bf16(h * rstd * weight)
+ *   q, scale = fp8_quant_1x128(y), bit for bit
+ * x [T,d] of x_dt, residual [T,d] of res_dt, weight [d] of w_dt (MOE_BF16 or
+ * MOE_F32 each).  Outputs, each NULL when not asked for: h_out [T,d] of res_dt
+ * (the stream handed on; needs a residual; rounded once if bf16), y bf16 [T,d],
+ * q E4M3 [T,d] with scale FP32 [T,d/128] (both or neither), rstd FP32 [T] (what
+ * the backward takes).  h_out may be residual itself, or x itself where x_dt ==
+ * res_dt; y may be x or residual itself where that is bf16 (and then is not
+ * h_out); no other overlap.  A row of zeros with eps = 0 gives NaN.
+ * Limits: 1 <= d <= 16384, d % 128 == 0 with q, eps >= 0.
+ */
+int moe_add_rmsnorm(const void* x, int x_dt, const void* residual, int res_dt, const void* weight, int w_dt,
+                    int64_t T, int d, float eps, void* h_out, void* y_bf16, uint8_t* q, float* scale, float* rstd,
+                    moe_stream_t stream);
+
+/* moe_add_rmsnorm_backward -- from dy = dL/dy and, where h goes on as a
+ * residual stream, dh = dL/dh_out (NULL: none):
+ *   xh = h * rstd,  g = dy * weight,  c = mean(g * xh)
+ *   dx = rstd * (g - xh * c) + dh            (the gradient of x and of residual)
+ *   dw = sum over the rows of dy * xh        (the gradient of weight)
+ * in FP32, dx rounded once.  dy [T,d] of dy_dt, h [T,d] of h_dt (h_out, or x
+ * where there was no residual), weight [d] of w_dt, rstd FP32 [T]; dh and dx
+ * [T,d] of dx_dt (dx may be dh itself, or dy or h of the same type); dw FP32
+ * [d].  The rows are added up in an order that depends on T and d alone.  T = 0
+ * writes zeros to dw.  ws: scratch of moe_add_rmsnorm_backward_workspace_bytes(T,
+ * d) bytes (no setup needed; may be NULL when T = 0).
+ * Limits: 1 <= d <= 16384.
+ */
+/* 0 outside the call's limits (T < 1, d outside [1, 16384]). */
+size_t moe_add_rmsnorm_backward_workspace_bytes(int64_t T, int d);
+int moe_add_rmsnorm_backward(const void* dy, int dy_dt, const void* h, int h_dt, const void* weight, int w_dt,
+                             const float* rstd, const void* dh, int64_t T, int d, void* dx, int dx_dt, float* dw,
+                             void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------ MXFP4
+ * OCP microscaling with E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives): 32 consecutive values of a row share one E8M0 scale byte s, which
+ * stands for 2^(s - 127); s = 255 makes all 32 values NaN.  Two codes to a byte,
+ * the value with the even index in the low four bits.
+ *
+ * mxfp4_quant_1x32: x [rows, cols] (bf16 or FP32) -> q [rows, cols/2] bytes,
+ *   scale [rows, cols/32] bytes.  Per block amax = max|x|:
+ *     a NaN or an infinity in the block: scale 255, codes 0;
+ *     else e = floor(log2(amax)) - 2, held at -127 from below (amax = 0
+ *     included), scale = e + 127, code = E2M1(x / 2^e), round to nearest, ties
+ *     to even, magnitudes above 6 saturating, the sign of a zero kept.
+ * mxfp4_dequant_1x32: the values of q and scale, exact in bf16 and FP32 (4 and 6
+ *   times 2^127, which the quantiser never writes, are infinite).
+ * fp8_dequant_1x128: E4M3(q) * scale, the values of fp8_quant_1x128's outputs,
+ *   in FP32 and rounded once for bf16.
+ * Limits: rows >= 0, cols a positive multiple of 32 (128 for FP8).
+ */
+int mxfp4_quant_1x32(const void* x, int in_dt, int64_t rows, int cols, uint8_t* q, uint8_t* scale,
+                     moe_stream_t stream);
+int mxfp4_dequant_1x32(const uint8_t* q, const uint8_t* scale, int64_t rows, int cols, void* out, int out_dt,
+                       moe_stream_t stream);
+int fp8_dequant_1x128(const uint8_t* q, const float* scale, int64_t rows, int cols, void* out, int out_dt,
+                      moe_stream_t stream);
+
+/* grouped_gemm_mxfp4 -- the expert products on MXFP4 operands:
+ *   C[m,n] = sum_k A[am,k] * B[g,n,k]         (FP32 accumulation)
+ * for row m of group g, group_offset[g] <= m < group_offset[g+1], with
+ * am = a_row_index[m] (NULL: am = m).
+ *   a_q [a_rows, K/2 bytes], a_scale [a_rows, K/32]: mxfp4_quant_1x32's rows;
+ *        an index outside [0, a_rows) reads as a row of zeros
+ *   group_offset int32 [G+1] (device), non-decreasing, from 0 to M_total; groups
+ *        may be empty.  Values outside [0, M_total] are held inside it.
+ *   b_q [G, N, K/2 bytes], b_scale [G, N, K/32]: each group's weights, quantised
+ *        along K
+ *   epi  a moe_mx_epilogue.  SwiGLU takes B's rows interleaved as
+ *        grouped_gemm_fp8_blockscaled does: rows [256j, 256j+128) are the gate
+ *        projection's rows [128j, 128j+128), the next 128 the up projection's.
+ *        out is NULL for MOE_MX_SWIGLU_QUANT; out_q and out_scale are NULL for
+ *        the others.
+ * One launch and no workspace.  Limits: 1 <= G <= 1024, 0 <= M_total <= 2^31 - 2^16,
+ * N >= 1 (N % 256 == 0 for SwiGLU), K a positive multiple of 32, a_rows * K / 2
+ * and N * K / 2 at most 4294901760 (32-bit offsets inside A and inside one
+ * group's B), M_total <= a_rows without a_row_index.
+ */
+int grouped_gemm_mxfp4(const uint8_t* a_q, const uint8_t* a_scale, int64_t a_rows, const int32_t* a_row_index,
+                       const int32_t* group_offset, int G, int64_t M_total, const uint8_t* b_q,
+                       const uint8_t* b_scale, int N, int K, int epi, void* out, uint8_t* out_q,
+                       uint8_t* out_scale, moe_stream_t stream);
 
 /* moe_layer_forward -- the whole layer, [LINEAGE] "The notation":
  *   h'[t] = u[t] + FFN_shared(u[t]) + sum_k g[t,k] FFN_{idx[t,k]}(u[t])

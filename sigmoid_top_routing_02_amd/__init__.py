@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from collections import namedtuple
 
 import numpy as np
 
@@ -20,7 +21,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoefp8.so")
 
 MOE_BF16, MOE_F32 = 0, 1
+_DTYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
 MOE_EPI_STORE_F32, MOE_EPI_SWIGLU_F32, MOE_EPI_SWIGLU_QUANT, MOE_EPI_SWIGLU_QUANT_Z = 0, 1, 2, 3
+MOE_MX_STORE_F32, MOE_MX_STORE_BF16, MOE_MX_SWIGLU_BF16, MOE_MX_SWIGLU_QUANT = 0, 1, 2, 3
 
 # every symbol the header declares (kept in step with include/moe_fp8.h)
 EXPORTS = (
@@ -35,6 +38,8 @@ EXPORTS = (
     "moe_layer_workspace_bytes", "moe_layer_forward",
     "moe_prepare_backward_weights", "moe_gate_backward", "moe_swiglu_backward", "moe_router_backward",
     "moe_wgrad_block_starts", "moe_wgrad_operands", "moe_wgrad_workspace_bytes", "moe_wgrad",
+    "moe_add_rmsnorm", "moe_add_rmsnorm_backward_workspace_bytes", "moe_add_rmsnorm_backward",
+    "mxfp4_quant_1x32", "mxfp4_dequant_1x32", "fp8_dequant_1x128", "grouped_gemm_mxfp4",
 )
 
 
@@ -86,6 +91,13 @@ def load_library(path: str = LIB_PATH):
         "moe_wgrad_operands": ([P, P, P, P, P, P, P, P, P, I32, I32, I64, I32, I32, I32, I64,
                                 P, P, P, P, P, P, P, P, P], I32),
         "moe_wgrad_workspace_bytes": ([I32, I32, I32], SZ),
+        "moe_add_rmsnorm": ([P, I32, P, I32, P, I32, I64, I32, F32, P, P, P, P, P, P], I32),
+        "moe_add_rmsnorm_backward_workspace_bytes": ([I64, I32], SZ),
+        "moe_add_rmsnorm_backward": ([P, I32, P, I32, P, I32, P, P, I64, I32, P, I32, P, P, SZ, P], I32),
+        "mxfp4_quant_1x32": ([P, I32, I64, I32, P, P, P], I32),
+        "mxfp4_dequant_1x32": ([P, P, I64, I32, P, I32, P], I32),
+        "fp8_dequant_1x128": ([P, P, I64, I32, P, I32, P], I32),
+        "grouped_gemm_mxfp4": ([P, P, I64, P, P, I32, I64, P, P, I32, I32, I32, P, P, P, P], I32),
         "moe_wgrad": ([P, I32, I32, I32, I32, P, P, P, P, P, P, P, P, P, P, P, SZ, P], I32),
     }
     for name, (args, res) in sig.items():
@@ -557,3 +569,171 @@ def moe_wgrad(dh, topk_gate, slot_row, row_token, z, dh_row, u, group_offset, sh
                        *(_ptr(bufs[k]) for k in ("dyT_q", "dyT_s", "hT_q", "hT_s", "dzT_q", "dzT_s", "xT_q", "xT_s")),
                        _ptr(dw13), _ptr(dw2), _ptr(ws), ws.numel(), _stream()), "moe_wgrad")
     return dw13, dw2, bufs, kbs
+
+
+# ---------------------------------------------------------------- residual + RMS norm
+RMSNorm = namedtuple("RMSNorm", "y h rstd q scale")
+
+
+def _dt(t, name):
+    if t.dtype not in _DTYPES:
+        raise MoEError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
+    return _DTYPES[t.dtype]
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise MoEError(f"{name}: shape {tuple(t.shape)}, expected two dimensions")
+    return tuple(t.shape)
+
+
+def _on(t, *others):
+    """The tensors lie on the device whose current stream the call is put on."""
+    here = torch.device("cuda", torch.cuda.current_device()) if t.is_cuda else None
+    for o in (t, *others):
+        if o is not None and (not o.is_cuda or o.device != here):
+            raise MoEError(f"tensor on {o.device}, expected the current GPU ({here})")
+
+
+def moe_add_rmsnorm(x, weight, eps, residual=None, quant=False, h_out=None, y=None, q=None, scale=None, rstd=None):
+    """h = x + residual, y = bf16(h / sqrt(mean(h^2) + eps) * weight) and, with quant, the FP8 1x128
+    codes and scales of y.  x, residual bf16/f32 [T,d], weight bf16/f32 [d]
+    -> RMSNorm(y bf16 [T,d], h of residual's type [T,d] or None, rstd f32 [T], q uint8 [T,d] or None,
+    scale f32 [T,d/128] or None).  h_out may be residual, or x of the same type."""
+    T, d = _matrix(x, "x")
+    xd, wd = _dt(x, "x"), _dt(weight, "weight")
+    _want(weight, weight.dtype, (d,), "weight")
+    rd = MOE_F32
+    if residual is not None:
+        rd = _dt(residual, "residual")
+        _want(residual, residual.dtype, (T, d), "residual")
+        h_out = _new((T, d), residual.dtype, x) if h_out is None else h_out
+        _want(h_out, residual.dtype, (T, d), "h_out")
+    elif h_out is not None:
+        raise MoEError("moe_add_rmsnorm: h_out without a residual")
+    y = _new((T, d), torch.bfloat16, x) if y is None else y
+    rstd = _new((T,), torch.float32, x) if rstd is None else rstd
+    _want(y, torch.bfloat16, (T, d), "y")
+    _want(rstd, torch.float32, (T,), "rstd")
+    if quant:
+        q = _new((T, d), torch.uint8, x) if q is None else q
+        scale = _new((T, d // 128), torch.float32, x) if scale is None else scale
+        _want(q, torch.uint8, (T, d), "q")
+        _want(scale, torch.float32, (T, d // 128), "scale")
+    elif q is not None or scale is not None:
+        raise MoEError("moe_add_rmsnorm: q or scale without quant")
+    _on(x, weight, residual, h_out, y, q, scale, rstd)
+    L = load_library()
+    _check(L.moe_add_rmsnorm(_ptr(x), xd, _ptr(residual), rd, _ptr(weight), wd, T, d, eps, _ptr(h_out), _ptr(y),
+                             _ptr(q), _ptr(scale), _ptr(rstd), _stream()), "moe_add_rmsnorm")
+    return RMSNorm(y, h_out, rstd, q, scale)
+
+
+def moe_add_rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, dw=None, dx_dtype=None, ws=None):
+    """dy, h bf16/f32 [T,d], weight bf16/f32 [d], rstd f32 [T], dh (the gradient of h_out) or None
+    -> (dx [T,d] of dh's type, else dx_dtype, else dy's; dw f32 [d]).  dx is the gradient of x and of
+    residual alike."""
+    T, d = _matrix(dy, "dy")
+    yd, hd, wd = _dt(dy, "dy"), _dt(h, "h"), _dt(weight, "weight")
+    _want(h, h.dtype, (T, d), "h")
+    _want(weight, weight.dtype, (d,), "weight")
+    _want(rstd, torch.float32, (T,), "rstd")
+    if dx_dtype is None:
+        dx_dtype = dh.dtype if dh is not None else dx.dtype if dx is not None else dy.dtype
+    dx = _new((T, d), dx_dtype, dy) if dx is None else dx
+    dw = _new((d,), torch.float32, dy) if dw is None else dw
+    _want(dx, dx_dtype, (T, d), "dx")
+    _want(dw, torch.float32, (d,), "dw")
+    if dh is not None:
+        _want(dh, dx_dtype, (T, d), "dh")
+    L = load_library()
+    if ws is None:
+        ws = _new((max(L.moe_add_rmsnorm_backward_workspace_bytes(T, d), 256),), torch.uint8, dy)
+    _on(dy, h, weight, rstd, dh, dx, dw, ws)
+    _check(L.moe_add_rmsnorm_backward(_ptr(dy), yd, _ptr(h), hd, _ptr(weight), wd, _ptr(rstd), _ptr(dh), T, d,
+                                      _ptr(dx), _dt(dx, "dx"), _ptr(dw), _ptr(ws), ws.numel() * ws.element_size(),
+                                      _stream()), "moe_add_rmsnorm_backward")
+    return dx, dw
+
+
+# ---------------------------------------------------------------- MXFP4
+def mxfp4_quant_1x32(x, q=None, scale=None):
+    """x bf16/f32 [rows, cols] -> (q uint8 [rows, cols/2], two E2M1 codes to a byte, the even column in
+    the low half; scale uint8 [rows, cols/32], E8M0)."""
+    rows, cols = _matrix(x, "x")
+    dt = _dt(x, "x")
+    q = _new((rows, cols // 2), torch.uint8, x) if q is None else q
+    scale = _new((rows, cols // 32), torch.uint8, x) if scale is None else scale
+    _want(q, torch.uint8, (rows, cols // 2), "q")
+    _want(scale, torch.uint8, (rows, cols // 32), "scale")
+    _on(x, q, scale)
+    L = load_library()
+    _check(L.mxfp4_quant_1x32(_ptr(x), dt, rows, cols, _ptr(q), _ptr(scale), _stream()), "mxfp4_quant_1x32")
+    return q, scale
+
+
+def mxfp4_dequant_1x32(q, scale, dtype=torch.bfloat16, out=None):
+    """The values of mxfp4_quant_1x32's outputs, bf16 or f32 [rows, cols]."""
+    rows, half = _matrix(q, "q")
+    cols = half * 2
+    _want(q, torch.uint8, (rows, half), "q")
+    _want(scale, torch.uint8, (rows, cols // 32), "scale")
+    out = _new((rows, cols), dtype, q) if out is None else out
+    _want(out, dtype, (rows, cols), "out")
+    _on(q, scale, out)
+    L = load_library()
+    _check(L.mxfp4_dequant_1x32(_ptr(q), _ptr(scale), rows, cols, _ptr(out), _dt(out, "out"), _stream()),
+           "mxfp4_dequant_1x32")
+    return out
+
+
+def fp8_dequant_1x128(q, scale, dtype=torch.float32, out=None):
+    """The values of fp8_quant_1x128's outputs, bf16 or f32 [rows, cols]."""
+    rows, cols = _matrix(q, "q")
+    _want(q, torch.uint8, (rows, cols), "q")
+    _want(scale, torch.float32, (rows, cols // 128), "scale")
+    out = _new((rows, cols), dtype, q) if out is None else out
+    _want(out, dtype, (rows, cols), "out")
+    _on(q, scale, out)
+    L = load_library()
+    _check(L.fp8_dequant_1x128(_ptr(q), _ptr(scale), rows, cols, _ptr(out), _dt(out, "out"), _stream()),
+           "fp8_dequant_1x128")
+    return out
+
+
+def grouped_gemm_mxfp4(a_q, a_scale, group_offset, M_total, b_q, b_scale, epi=MOE_MX_STORE_F32, a_row_index=None,
+                       out=None, out_q=None, out_scale=None):
+    """a_q uint8 [*,K/2], a_scale uint8 [*,K/32], group_offset i32 [G+1] (device), b_q uint8 [G,N,K/2],
+    b_scale uint8 [G,N,K/32] -> out f32 or bf16 [M_total,N], h bf16 [M_total,N/2] (MOE_MX_SWIGLU_BF16), or
+    (out_q uint8 [M_total,N/4], out_scale uint8 [M_total,N/64]) (MOE_MX_SWIGLU_QUANT)."""
+    if b_q.dim() != 3:
+        raise MoEError(f"b_q: shape {tuple(b_q.shape)}, expected [G, N, K/2]")
+    G, N, half = b_q.shape
+    K = half * 2
+    _want(b_q, torch.uint8, (G, N, half), "b_q")
+    _want(b_scale, torch.uint8, (G, N, K // 32), "b_scale")
+    if a_q.dim() != 2 or a_q.dtype != torch.uint8 or a_q.shape[1] != half:
+        raise MoEError(f"a_q: {a_q.dtype} {tuple(a_q.shape)}, expected torch.uint8 [*, {half}]")
+    rows = a_q.shape[0]
+    _want(a_scale, torch.uint8, (rows, K // 32), "a_scale")
+    if group_offset.dtype != torch.int32 or group_offset.numel() < G + 1:
+        raise MoEError("group_offset must be int32 with G+1 entries")
+    if a_row_index is not None and (a_row_index.dtype != torch.int32 or a_row_index.numel() < M_total):
+        raise MoEError(f"a_row_index: {a_row_index.dtype} with {a_row_index.numel()} entries, "
+                       f"expected int32 with at least M_total = {M_total}")
+    if epi == MOE_MX_SWIGLU_QUANT:
+        out_q = _new((M_total, N // 4), torch.uint8, a_q) if out_q is None else out_q
+        out_scale = _new((M_total, N // 64), torch.uint8, a_q) if out_scale is None else out_scale
+        _want(out_q, torch.uint8, (M_total, N // 4), "out_q")
+        _want(out_scale, torch.uint8, (M_total, N // 64), "out_scale")
+    else:
+        want = torch.float32 if epi == MOE_MX_STORE_F32 else torch.bfloat16
+        cols = N // 2 if epi == MOE_MX_SWIGLU_BF16 else N
+        out = _new((M_total, cols), want, a_q) if out is None else out
+        _want(out, want, (M_total, cols), "out")
+    _on(a_q, a_scale, a_row_index, group_offset, b_q, b_scale, out, out_q, out_scale)
+    L = load_library()
+    _check(L.grouped_gemm_mxfp4(_ptr(a_q), _ptr(a_scale), rows, _ptr(a_row_index), _ptr(group_offset), G, M_total,
+                                _ptr(b_q), _ptr(b_scale), N, K, epi, _ptr(out), _ptr(out_q), _ptr(out_scale),
+                                _stream()), "grouped_gemm_mxfp4")
+    return (out_q, out_scale) if epi == MOE_MX_SWIGLU_QUANT else out

@@ -573,6 +573,157 @@ int moe_wgrad(const int32_t* kb_start, int G, int n_kb, int d, int I, const uint
                       "wgrad GEMM launch");
 }
 
+// ---------------------------------------------------------------- residual + RMS norm, MXFP4
+namespace {
+bool is_dtype(int dt) { return dt == MOE_BF16 || dt == MOE_F32; }
+}  // namespace
+
+int moe_add_rmsnorm(const void* x, int x_dt, const void* residual, int res_dt, const void* weight, int w_dt, int64_t T,
+                    int d, float eps, void* h_out, void* y_bf16, uint8_t* q, float* scale, float* rstd,
+                    moe_stream_t stream) {
+    REQUIRE(T >= 0, MOE_ERR_SHAPE, "moe_add_rmsnorm: T < 0");
+    REQUIRE(d >= 1, MOE_ERR_SHAPE, "moe_add_rmsnorm: d=%d not positive", d);
+    REQUIRE(d <= 16384, MOE_ERR_UNSUPPORTED, "moe_add_rmsnorm: d=%d above 16384", d);
+    REQUIRE(is_dtype(x_dt) && is_dtype(w_dt) && (!residual || is_dtype(res_dt)), MOE_ERR_UNSUPPORTED,
+            "moe_add_rmsnorm: dtypes %d, %d, %d", x_dt, res_dt, w_dt);
+    REQUIRE(eps >= 0.0f, MOE_ERR_UNSUPPORTED, "moe_add_rmsnorm: eps=%g is negative or NaN", (double)eps);
+    REQUIRE((q == nullptr) == (scale == nullptr), MOE_ERR_NULLPTR,
+            "moe_add_rmsnorm: q and scale must both be given or both be NULL");
+    REQUIRE(!q || d % 128 == 0, MOE_ERR_SHAPE, "moe_add_rmsnorm: d=%d not a multiple of 128, as q needs", d);
+    REQUIRE(!h_out || residual || T == 0, MOE_ERR_NULLPTR, "moe_add_rmsnorm: h_out without a residual");
+    if (T == 0) return MOE_OK;
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(weight);
+    if (residual) REQUIRE_PTR(residual);
+    if (h_out) REQUIRE_PTR(h_out);
+    if (y_bf16) REQUIRE_PTR(y_bf16);
+    if (q) REQUIRE_PTR(q);
+    if (scale) REQUIRE_PTR(scale);
+    if (rstd) REQUIRE_PTR(rstd);
+    moe::AddRmsnormArgs a{};
+    a.x = x; a.x_f32 = x_dt == MOE_F32;
+    a.res = residual; a.res_f32 = res_dt == MOE_F32;
+    a.w = weight; a.w_f32 = w_dt == MOE_F32;
+    a.T = T; a.d = d; a.eps = eps;
+    a.h = h_out; a.y = y_bf16; a.q = q; a.scale = scale; a.rstd = rstd;
+    return hip_status(moe::launch_add_rmsnorm(a, S(stream)), "add rmsnorm launch");
+}
+
+size_t moe_add_rmsnorm_backward_workspace_bytes(int64_t T, int d) {
+    return T >= 1 && d >= 1 && d <= 16384 ? moe::add_rmsnorm_backward_ws_bytes(T, d) : 0;
+}
+
+int moe_add_rmsnorm_backward(const void* dy, int dy_dt, const void* h, int h_dt, const void* weight, int w_dt,
+                             const float* rstd, const void* dh, int64_t T, int d, void* dx, int dx_dt, float* dw,
+                             void* ws, size_t ws_bytes, moe_stream_t stream) {
+    REQUIRE(T >= 0, MOE_ERR_SHAPE, "moe_add_rmsnorm_backward: T < 0");
+    REQUIRE(d >= 1, MOE_ERR_SHAPE, "moe_add_rmsnorm_backward: d=%d not positive", d);
+    REQUIRE(d <= 16384, MOE_ERR_UNSUPPORTED, "moe_add_rmsnorm_backward: d=%d above 16384", d);
+    REQUIRE(is_dtype(dy_dt) && is_dtype(h_dt) && is_dtype(w_dt) && is_dtype(dx_dt), MOE_ERR_UNSUPPORTED,
+            "moe_add_rmsnorm_backward: dtypes %d, %d, %d, %d", dy_dt, h_dt, w_dt, dx_dt);
+    REQUIRE_PTR(dw);
+    if (T > 0) {
+        REQUIRE_PTR(dy);
+        REQUIRE_PTR(h);
+        REQUIRE_PTR(weight);
+        REQUIRE_PTR(rstd);
+        REQUIRE_PTR(dx);
+        REQUIRE_PTR(ws);
+        if (dh) REQUIRE_PTR(dh);
+        REQUIRE(ws_bytes >= moe::add_rmsnorm_backward_ws_bytes(T, d), MOE_ERR_WORKSPACE,
+                "moe_add_rmsnorm_backward: workspace %zu < %zu bytes", ws_bytes,
+                moe::add_rmsnorm_backward_ws_bytes(T, d));
+    }
+    moe::AddRmsnormBackwardArgs a{};
+    a.dy = dy; a.dy_f32 = dy_dt == MOE_F32;
+    a.h = h; a.h_f32 = h_dt == MOE_F32;
+    a.w = weight; a.w_f32 = w_dt == MOE_F32;
+    a.rstd = rstd; a.dh = dh; a.T = T; a.d = d;
+    a.dx = dx; a.dx_f32 = dx_dt == MOE_F32;
+    a.part = static_cast<float*>(ws);
+    return hip_status(moe::launch_add_rmsnorm_backward(a, dw, S(stream)), "add rmsnorm backward launch");
+}
+
+int mxfp4_quant_1x32(const void* x, int in_dt, int64_t rows, int cols, uint8_t* q, uint8_t* scale,
+                     moe_stream_t stream) {
+    REQUIRE(rows >= 0, MOE_ERR_SHAPE, "mxfp4_quant_1x32: rows < 0");
+    REQUIRE(cols > 0 && cols % 32 == 0, MOE_ERR_SHAPE, "mxfp4_quant_1x32: cols=%d not a positive multiple of 32", cols);
+    REQUIRE(is_dtype(in_dt), MOE_ERR_UNSUPPORTED, "mxfp4_quant_1x32: dtype %d", in_dt);
+    REQUIRE(rows < (int64_t)1 << 32, MOE_ERR_UNSUPPORTED, "mxfp4_quant_1x32: too many rows");
+    if (rows == 0) return MOE_OK;
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(scale);
+    return hip_status(moe::launch_mxfp4_quant(x, in_dt == MOE_F32, rows * (cols / 32), q, scale, S(stream)),
+                      "mxfp4 quant launch");
+}
+
+int mxfp4_dequant_1x32(const uint8_t* q, const uint8_t* scale, int64_t rows, int cols, void* out, int out_dt,
+                       moe_stream_t stream) {
+    REQUIRE(rows >= 0, MOE_ERR_SHAPE, "mxfp4_dequant_1x32: rows < 0");
+    REQUIRE(cols > 0 && cols % 32 == 0, MOE_ERR_SHAPE, "mxfp4_dequant_1x32: cols=%d not a positive multiple of 32", cols);
+    REQUIRE(is_dtype(out_dt), MOE_ERR_UNSUPPORTED, "mxfp4_dequant_1x32: dtype %d", out_dt);
+    REQUIRE(rows < (int64_t)1 << 32, MOE_ERR_UNSUPPORTED, "mxfp4_dequant_1x32: too many rows");
+    if (rows == 0) return MOE_OK;
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(scale);
+    REQUIRE_PTR(out);
+    return hip_status(moe::launch_mxfp4_dequant(q, scale, rows * (cols / 32), out_dt == MOE_F32, out, S(stream)),
+                      "mxfp4 dequant launch");
+}
+
+int fp8_dequant_1x128(const uint8_t* q, const float* scale, int64_t rows, int cols, void* out, int out_dt,
+                      moe_stream_t stream) {
+    REQUIRE(rows >= 0, MOE_ERR_SHAPE, "fp8_dequant_1x128: rows < 0");
+    REQUIRE(cols > 0 && cols % 128 == 0, MOE_ERR_SHAPE, "fp8_dequant_1x128: cols=%d not a positive multiple of 128", cols);
+    REQUIRE(is_dtype(out_dt), MOE_ERR_UNSUPPORTED, "fp8_dequant_1x128: dtype %d", out_dt);
+    REQUIRE(rows < (int64_t)1 << 32, MOE_ERR_UNSUPPORTED, "fp8_dequant_1x128: too many rows");
+    if (rows == 0) return MOE_OK;
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(scale);
+    REQUIRE_PTR(out);
+    return hip_status(moe::launch_fp8_dequant_1x128(q, scale, rows * (cols / 128), out_dt == MOE_F32, out, S(stream)),
+                      "fp8 dequant launch");
+}
+
+int grouped_gemm_mxfp4(const uint8_t* a_q, const uint8_t* a_scale, int64_t a_rows, const int32_t* a_row_index,
+                       const int32_t* group_offset, int G, int64_t M_total, const uint8_t* b_q, const uint8_t* b_scale,
+                       int N, int K, int epi, void* out, uint8_t* out_q, uint8_t* out_scale, moe_stream_t stream) {
+    constexpr int64_t MOST = 0xFFFF0000ll;
+    REQUIRE(G >= 1 && G <= 1024, MOE_ERR_UNSUPPORTED, "grouped_gemm_mxfp4: G=%d outside [1, 1024]", G);
+    REQUIRE(M_total >= 0 && M_total <= ((int64_t)1 << 31) - 65536, MOE_ERR_UNSUPPORTED, "grouped_gemm_mxfp4: M_total out of range");
+    REQUIRE(K > 0 && K % 32 == 0, MOE_ERR_SHAPE, "grouped_gemm_mxfp4: K=%d not a positive multiple of 32", K);
+    REQUIRE(epi >= MOE_MX_STORE_F32 && epi <= MOE_MX_SWIGLU_QUANT, MOE_ERR_UNSUPPORTED, "grouped_gemm_mxfp4: epilogue %d", epi);
+    REQUIRE(N >= 1, MOE_ERR_SHAPE, "grouped_gemm_mxfp4: N=%d not positive", N);
+    REQUIRE(epi < MOE_MX_SWIGLU_BF16 || N % 256 == 0, MOE_ERR_SHAPE, "grouped_gemm_mxfp4: SwiGLU needs N=%d a multiple of 256", N);
+    REQUIRE((int64_t)N * (K / 2) <= MOST, MOE_ERR_UNSUPPORTED, "grouped_gemm_mxfp4: one group's B exceeds 32-bit offsets");
+    REQUIRE(a_rows >= 0 && a_rows < ((int64_t)1 << 31) && a_rows * (K / 2) <= MOST, MOE_ERR_UNSUPPORTED,
+            "grouped_gemm_mxfp4: A of %lld rows exceeds 32-bit offsets", (long long)a_rows);
+    REQUIRE(a_row_index || M_total <= a_rows, MOE_ERR_SHAPE, "grouped_gemm_mxfp4: A has %lld rows, fewer than M_total=%lld",
+            (long long)a_rows, (long long)M_total);
+    if (M_total == 0) return MOE_OK;
+    REQUIRE_PTR(a_q);
+    REQUIRE_PTR(a_scale);
+    if (a_row_index) REQUIRE_PTR(a_row_index);
+    REQUIRE_PTR(group_offset);
+    REQUIRE_PTR(b_q);
+    REQUIRE_PTR(b_scale);
+    if (epi == MOE_MX_SWIGLU_QUANT) {
+        REQUIRE(!out, MOE_ERR_UNSUPPORTED, "grouped_gemm_mxfp4: this epilogue writes out_q and out_scale, not out");
+        REQUIRE_PTR(out_q);
+        REQUIRE_PTR(out_scale);
+    } else {
+        REQUIRE(!out_q && !out_scale, MOE_ERR_UNSUPPORTED, "grouped_gemm_mxfp4: this epilogue writes out, not out_q or out_scale");
+        REQUIRE_PTR(out);
+    }
+    moe::MxGemmArgs a{};
+    a.a_q = a_q; a.a_s = a_scale; a.a_rows = a_rows; a.a_row_index = a_row_index;
+    a.group_offset = group_offset; a.G = G; a.M_total = M_total;
+    a.b_q = b_q; a.b_s = b_scale; a.N = N; a.K = K;
+    a.out = out; a.out_q = out_q; a.out_s = out_scale;
+    return hip_status(moe::launch_grouped_gemm_mxfp4(a, epi, S(stream)), "grouped_gemm_mxfp4 launch");
+}
+
 // ---------------------------------------------------------------- whole layer
 namespace {
 struct LayerWs {

@@ -96,6 +96,63 @@ hipError_t launch_seq_balance_loss(const float* s, const int32_t* idx, int64_t n
 hipError_t launch_accum_probe(const uint8_t* a_q, const uint8_t* b_q, int M, int N, int K,
                               int chained, float* out, hipStream_t st);
 
+// norm.hip.  *_f32: the type of the tensor (else bf16); null pointers: not asked for.
+struct AddRmsnormArgs {
+    const void* x; bool x_f32;
+    const void* res; bool res_f32;      // h has its type
+    const void* w; bool w_f32;
+    int64_t T;
+    int d;
+    float eps;
+    void* h;
+    void* y;                            // bf16
+    uint8_t* q;
+    float* scale;
+    float* rstd;
+};
+hipError_t launch_add_rmsnorm(const AddRmsnormArgs& a, hipStream_t st);
+struct AddRmsnormBackwardArgs {
+    const void* dy; bool dy_f32;
+    const void* h; bool h_f32;
+    const void* w; bool w_f32;
+    const float* rstd;
+    const void* dh;                     // of dx's type
+    int64_t T;
+    int d;
+    void* dx; bool dx_f32;
+    float* part;                        // add_rmsnorm_backward_ws_bytes: partial rows of dw
+};
+size_t add_rmsnorm_backward_ws_bytes(int64_t T, int d);
+hipError_t launch_add_rmsnorm_backward(const AddRmsnormBackwardArgs& a, float* dw, hipStream_t st);
+
+// mxfp4.hip: n_blocks blocks of 32 consecutive values
+hipError_t launch_mxfp4_quant(const void* x, int in_is_f32, int64_t n_blocks, uint8_t* q, uint8_t* scale,
+                              hipStream_t st);
+hipError_t launch_mxfp4_dequant(const uint8_t* q, const uint8_t* scale, int64_t n_blocks, int out_is_f32, void* out,
+                                hipStream_t st);
+// n_tiles tiles of 128 consecutive values
+hipError_t launch_fp8_dequant_1x128(const uint8_t* q, const float* scale, int64_t n_tiles, int out_is_f32, void* out,
+                                    hipStream_t st);
+
+// mxgemm.hip
+struct MxGemmArgs {
+    const uint8_t* a_q;
+    const uint8_t* a_s;
+    int64_t a_rows;
+    const int32_t* a_row_index;
+    const int32_t* group_offset;
+    int G;
+    int64_t M_total;
+    const uint8_t* b_q;
+    const uint8_t* b_s;
+    int N;
+    int K;
+    void* out;
+    uint8_t* out_q;
+    uint8_t* out_s;
+};
+hipError_t launch_grouped_gemm_mxfp4(const MxGemmArgs& a, int epi, hipStream_t st);
+
 // combine.hip
 hipError_t launch_combine(const uint16_t* u, const void* y, int y_is_f32, int64_t shared_row0,
                           const float* gate, const int32_t* slot_row, int64_t T, int K, int d,

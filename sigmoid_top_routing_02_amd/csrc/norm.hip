@@ -1,0 +1,336 @@
+// Residual addition, RMS norm and FP8 copy in one pass, and the backward.
+//
+// Forward, per row of d values:
+//   h = x + residual (h = x without one),  rstd = 1 / sqrt(mean(h^2) + eps),
+//   y = bf16(h * rstd * w),  (q, scale) = the 1x128 E4M3 tiles of y.
+// h is held in FP32 from its addition to the last use: the statistic and y are
+// taken of the unrounded sum, the stored copy of h is rounded once.  q is taken
+// of the rounded y, so that it equals fp8_quant_1x128(y) bit for bit and the
+// router (which reads y) and the experts (which read q) see one input.
+//
+// Backward, with xh = h * rstd, g = dy * w, c = mean(g * xh):
+//   dx = rstd * (g - xh * c) + dh,   dw = sum over the rows of dy * xh.
+//
+// Both are bound by HBM: a row is read once, kept in registers between its
+// reduction and its use, and written once.
+#include "device_math.h"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    const v2bf v = {(__bf16)a, (__bf16)b};          // round to nearest even, NaN stays NaN
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// How a row of d values lies in the NV * 8 registers of each of its TPR threads.
+// VEC (d % 8 == 0, rows then 16-byte aligned): thread t holds 8 consecutive
+// values at ((v * TPR) + t) * 8.  Otherwise value j of step v is at
+// (v * 8 + j) * TPR + t, one element per access, neighbours on neighbouring
+// threads.
+template <bool VEC>
+__device__ __forceinline__ int col_of(int v, int j, int t, int tpr) {
+    return VEC ? (v * tpr + t) * 8 + j : (v * 8 + j) * tpr + t;
+}
+
+// 8 values of a row (zero past its end).  f32 is uniform over the launch.
+template <bool VEC>
+__device__ __forceinline__ void load8(const void* p, bool f32, int64_t row_off, int v, int t, int tpr, int d,
+                                      float (&x)[8]) {
+    if constexpr (VEC) {
+        const int c = col_of<VEC>(v, 0, t, tpr);
+        if (c < d) {
+            if (f32) {
+                const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + row_off + c);
+                const float4 a = q[0], b = q[1];
+                x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+                x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+            } else {
+                const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + row_off + c);
+                x[0] = bf16_lo(a.x); x[1] = bf16_hi(a.x); x[2] = bf16_lo(a.y); x[3] = bf16_hi(a.y);
+                x[4] = bf16_lo(a.z); x[5] = bf16_hi(a.z); x[6] = bf16_lo(a.w); x[7] = bf16_hi(a.w);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = col_of<VEC>(v, j, t, tpr);
+            x[j] = c >= d ? 0.0f
+                   : f32  ? static_cast<const float*>(p)[row_off + c]
+                          : bf16_to_f32(static_cast<const uint16_t*>(p)[row_off + c]);
+        }
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(void* p, bool f32, int64_t row_off, int v, int t, int tpr, int d,
+                                       const float (&x)[8]) {
+    if constexpr (VEC) {
+        const int c = col_of<VEC>(v, 0, t, tpr);
+        if (c >= d) return;
+        if (f32) {
+            float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + row_off + c);
+            q[0] = make_float4(x[0], x[1], x[2], x[3]);
+            q[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + row_off + c) =
+                make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = col_of<VEC>(v, j, t, tpr);
+            if (c >= d) continue;
+            if (f32) static_cast<float*>(p)[row_off + c] = x[j];
+            else static_cast<uint16_t*>(p)[row_off + c] = (uint16_t)pack_bf16(x[j], 0.0f);
+        }
+    }
+}
+
+// Sum over the threads of one row: the wave by shuffles, the waves through LDS
+// (two buffers in turn, so one barrier per row is enough).  Same order on every
+// run.
+template <bool WAVE_ROW>
+__device__ __forceinline__ float row_sum(float s, float (*part)[16], int flip) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
+    if constexpr (WAVE_ROW) return s;
+    const int nw = (int)blockDim.x >> 6;
+    if ((threadIdx.x & 63) == 0) part[flip][threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = part[flip][0];
+    for (int i = 1; i < nw; ++i) s += part[flip][i];
+    return s;
+}
+
+// A block is one row at a time (WAVE_ROW: each of its four waves is one).
+template <int NV, bool VEC, bool WAVE_ROW>
+__global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddRmsnormArgs a) {
+    __shared__ float part[2][16];
+    const int t = WAVE_ROW ? (int)threadIdx.x & 63 : (int)threadIdx.x;
+    const int tpr = WAVE_ROW ? 64 : (int)blockDim.x;
+    const int64_t step = WAVE_ROW ? (int64_t)gridDim.x * 4 : gridDim.x;
+    const int64_t first = WAVE_ROW ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    const int d = a.d;
+    float w[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) load8<VEC>(a.w, a.w_f32, 0, v, t, tpr, d, w[v]);
+    int flip = 0;
+    for (int64_t row = first; row < a.T; row += step, flip ^= 1) {
+        const int64_t off = row * d;
+        float h[NV][8];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) load8<VEC>(a.x, a.x_f32, off, v, t, tpr, d, h[v]);
+        if (a.res) {
+            float r[NV][8];
+#pragma unroll
+            for (int v = 0; v < NV; ++v) load8<VEC>(a.res, a.res_f32, off, v, t, tpr, d, r[v]);
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[v][j] += r[v][j];
+            if (a.h) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v) store8<VEC>(a.h, a.res_f32, off, v, t, tpr, d, h[v]);
+            }
+        }
+        float s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s = __builtin_fmaf(h[v][j], h[v][j], s);
+        s = row_sum<WAVE_ROW>(s, part, flip);
+        const float rstd = 1.0f / __builtin_sqrtf(s / (float)d + a.eps);
+        if (a.rstd && t == 0) a.rstd[row] = rstd;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = h[v][j] * rstd * w[v][j];
+            if (a.y) store8<VEC>(a.y, false, off, v, t, tpr, d, y);
+            if constexpr (VEC) {
+                if (a.q) {                            // d % 128 == 0: 16 lanes are one tile, all in the row or none
+                    const int c = col_of<VEC>(v, 0, t, tpr);
+                    float amax = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        const uint32_t b = pack_bf16(y[j], y[j + 1]);
+                        y[j] = bf16_lo(b);
+                        y[j + 1] = bf16_hi(b);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float m = __builtin_fabsf(y[j]);
+                        amax = m > amax ? m : amax;
+                    }
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1) {
+                        const float m = __shfl_xor(amax, o, 64);
+                        amax = m > amax ? m : amax;
+                    }
+                    float inv, sc;
+                    tile_scale(amax, inv, sc);
+                    if (c < d) {
+                        *reinterpret_cast<uint2*>(a.q + off + c) =
+                            make_uint2(e4m3_encode4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                                       e4m3_encode4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+                        if ((t & 15) == 0) a.scale[row * (d / 128) + c / 128] = sc;
+                    }
+                }
+            }
+        }
+    }
+}
+
+// As the forward; each row's block (WAVE_ROW: wave) keeps the sum of dy * xh of
+// its rows in registers and leaves it as one row of `part` at the end.
+template <int NV, bool VEC, bool WAVE_ROW>
+__global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_backward_kernel(AddRmsnormBackwardArgs a) {
+    __shared__ float part[2][16];
+    const int t = WAVE_ROW ? (int)threadIdx.x & 63 : (int)threadIdx.x;
+    const int tpr = WAVE_ROW ? 64 : (int)blockDim.x;
+    const int64_t step = WAVE_ROW ? (int64_t)gridDim.x * 4 : gridDim.x;
+    const int64_t first = WAVE_ROW ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    const int d = a.d;
+    float w[NV][8], dw[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        load8<VEC>(a.w, a.w_f32, 0, v, t, tpr, d, w[v]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[v][j] = 0.0f;
+    }
+    int flip = 0;
+    for (int64_t row = first; row < a.T; row += step, flip ^= 1) {
+        const int64_t off = row * d;
+        const float rstd = a.rstd[row];
+        float g[NV][8], xh[NV][8];
+        float s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) load8<VEC>(a.dy, a.dy_f32, off, v, t, tpr, d, g[v]);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) load8<VEC>(a.h, a.h_f32, off, v, t, tpr, d, xh[v]);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                xh[v][j] *= rstd;
+                dw[v][j] = __builtin_fmaf(g[v][j], xh[v][j], dw[v][j]);
+                g[v][j] *= w[v][j];
+                s = __builtin_fmaf(g[v][j], xh[v][j], s);
+            }
+        const float c = row_sum<WAVE_ROW>(s, part, flip) / (float)d;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = (g[v][j] - xh[v][j] * c) * rstd;
+            if (a.dh) {
+                float r[8];
+                load8<VEC>(a.dh, a.dx_f32, off, v, t, tpr, d, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] += r[j];
+            }
+            store8<VEC>(a.dx, a.dx_f32, off, v, t, tpr, d, o);
+        }
+    }
+    const int64_t prow = WAVE_ROW ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) store8<VEC>(a.part, true, prow * d, v, t, tpr, d, dw[v]);
+}
+
+// dw[c] = sum of the partial rows: 16 threads take every 16th row of a column,
+// then their sums are added in order.
+__global__ __launch_bounds__(256) void dw_reduce_kernel(const float* __restrict__ part, int rows, int d,
+                                                        float* __restrict__ dw) {
+    __shared__ float sum[16][17];
+    const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4;
+    const int c = blockIdx.x * 16 + cl;
+    float s = 0.0f;
+    if (c < d)
+        for (int r = rl; r < rows; r += 16) s += part[(int64_t)r * d + c];
+    sum[rl][cl] = s;
+    __syncthreads();
+    if (rl == 0 && c < d) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += sum[i][cl];
+        dw[c] = s;
+    }
+}
+
+// Rows up to 1024 wide are one wave each, four to a block; a wider one is a
+// block of as many waves as hold it at 16 values a thread.
+bool wave_row(int d) { return d <= 1024; }
+
+template <typename Launch>
+void dispatch_shape(int d, Launch&& go) {
+    const bool vec = d % 8 == 0;
+    if (wave_row(d)) {
+        if (d <= 512) vec ? go.template operator()<1, true, true>() : go.template operator()<1, false, true>();
+        else vec ? go.template operator()<2, true, true>() : go.template operator()<2, false, true>();
+    } else {
+        vec ? go.template operator()<2, true, false>() : go.template operator()<2, false, false>();
+    }
+}
+
+int row_threads(int d) { return wave_row(d) ? 256 : (d + 1023) / 1024 * 64; }
+
+// Blocks of the backward: a few per CU, so that the partial rows stay small
+// beside the data; a function of the sizes alone, so dw's bits are too.
+int backward_blocks(int64_t T, int d) {
+    const int64_t per = wave_row(d) ? 4 : 1;
+    const int64_t b = (T + per - 1) / per;
+    return (int)(b < 512 ? b : 512);
+}
+
+struct ForwardLaunch {
+    const AddRmsnormArgs& a;
+    hipStream_t st;
+    template <int NV, bool VEC, bool WAVE_ROW>
+    void operator()() const {
+        const int64_t per = WAVE_ROW ? 4 : 1;
+        int64_t blocks = (a.T + per - 1) / per;
+        if (blocks > 2048) blocks = 2048;
+        hipLaunchKernelGGL((add_rmsnorm_kernel<NV, VEC, WAVE_ROW>), dim3((unsigned)blocks), dim3(row_threads(a.d)), 0,
+                           st, a);
+    }
+};
+
+struct BackwardLaunch {
+    const AddRmsnormBackwardArgs& a;
+    hipStream_t st;
+    template <int NV, bool VEC, bool WAVE_ROW>
+    void operator()() const {
+        hipLaunchKernelGGL((add_rmsnorm_backward_kernel<NV, VEC, WAVE_ROW>), dim3(backward_blocks(a.T, a.d)),
+                           dim3(row_threads(a.d)), 0, st, a);
+    }
+};
+
+}  // namespace
+
+hipError_t launch_add_rmsnorm(const AddRmsnormArgs& a, hipStream_t st) {
+    dispatch_shape(a.d, ForwardLaunch{a, st});
+    return hipGetLastError();
+}
+
+size_t add_rmsnorm_backward_ws_bytes(int64_t T, int d) {
+    return (size_t)backward_blocks(T, d) * (wave_row(d) ? 4 : 1) * d * sizeof(float);
+}
+
+hipError_t launch_add_rmsnorm_backward(const AddRmsnormBackwardArgs& a, float* dw, hipStream_t st) {
+    int rows = 0;                                   // no rows: the reduction alone, which writes zeros
+    if (a.T > 0) {
+        dispatch_shape(a.d, BackwardLaunch{a, st});
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        rows = backward_blocks(a.T, a.d) * (wave_row(a.d) ? 4 : 1);
+    }
+    hipLaunchKernelGGL(dw_reduce_kernel, dim3((a.d + 15) / 16), dim3(256), 0, st, a.part, rows, a.d, dw);
+    return hipGetLastError();
+}
+
+}  // namespace moe
