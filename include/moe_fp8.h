@@ -557,9 +557,10 @@ int fp8_dequant_1x128(const uint8_t* q, const float* scale, int64_t rows, int co
  *        out is NULL for MOE_MX_SWIGLU_QUANT; out_q and out_scale are NULL for
  *        the others.
  * One launch and no workspace.  Limits: 1 <= G <= 1024, 0 <= M_total <= 2^31 - 2^16,
- * N >= 1 (N % 256 == 0 for SwiGLU), K a positive multiple of 32, a_rows * K / 2
- * and N * K / 2 at most 4294901760 (32-bit offsets inside A and inside one
- * group's B), M_total <= a_rows without a_row_index.
+ * N >= 1 (N % 256 == 0 for SwiGLU), K a multiple of 32 up to 65536, a_rows * K / 2
+ * and (N + 256) * K / 2 at most 4294901760 (32-bit offsets inside A and inside
+ * one group's B), (ceil(M_total / 128) + G) * ceil(N / 256) < 2^31, M_total <=
+ * a_rows without a_row_index.
  */
 int grouped_gemm_mxfp4(const uint8_t* a_q, const uint8_t* a_scale, int64_t a_rows, const int32_t* a_row_index,
                        const int32_t* group_offset, int G, int64_t M_total, const uint8_t* b_q,

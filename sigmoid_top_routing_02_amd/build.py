@@ -5,6 +5,8 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -31,20 +33,47 @@ FLAGS = [
     "-mllvm", "-amdgpu-atomic-optimizer-strategy=None",
 ]
 
+# Sources that take other flags than FLAGS.  The MXFP4 product chains its
+# accumulators through the matrix instruction and fills the accumulation
+# registers with them, so it leaves the VGPR form to the others.
+WITHOUT = {"mxgemm.hip": ("-mllvm", "-amdgpu-mfma-vgpr-form")}
+
+
+def flags_of(source):
+    """FLAGS without what WITHOUT names for this source."""
+    drop = WITHOUT.get(os.path.basename(source))
+    if not drop:
+        return list(FLAGS)
+    at = next(i for i in range(len(FLAGS)) if tuple(FLAGS[i:i + len(drop)]) == drop)
+    return FLAGS[:at] + FLAGS[at + len(drop):]
+
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *sources()]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("hipcc failed to build libmoefp8.so")
+
+
+def build(verbose: bool = False) -> str:
+    """Compiles every source to an object, a few at a time, and links them."""
+    tmp = LIB + ".tmp"
+    with tempfile.TemporaryDirectory() as obj:
+        def compile_one(src):
+            out = os.path.join(obj, os.path.basename(src) + ".o")
+            flags = [f for f in flags_of(src) if f != "-shared"]
+            _run([HIPCC, *flags, "-I", os.path.join(ROOT, "include"), "-c", "-o", out, src], verbose)
+            return out
+
+        with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+            objects = list(ex.map(compile_one, sources()))
+        _run([HIPCC, "--offload-arch=gfx950", "-fPIC", "-shared", "-o", tmp, *objects], verbose)
     os.replace(tmp, LIB)
     return LIB
 

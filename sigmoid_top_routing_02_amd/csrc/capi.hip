@@ -693,10 +693,13 @@ int grouped_gemm_mxfp4(const uint8_t* a_q, const uint8_t* a_scale, int64_t a_row
     REQUIRE(G >= 1 && G <= 1024, MOE_ERR_UNSUPPORTED, "grouped_gemm_mxfp4: G=%d outside [1, 1024]", G);
     REQUIRE(M_total >= 0 && M_total <= ((int64_t)1 << 31) - 65536, MOE_ERR_UNSUPPORTED, "grouped_gemm_mxfp4: M_total out of range");
     REQUIRE(K > 0 && K % 32 == 0, MOE_ERR_SHAPE, "grouped_gemm_mxfp4: K=%d not a positive multiple of 32", K);
+    REQUIRE(K <= 65536, MOE_ERR_UNSUPPORTED, "grouped_gemm_mxfp4: K=%d above 65536", K);
     REQUIRE(epi >= MOE_MX_STORE_F32 && epi <= MOE_MX_SWIGLU_QUANT, MOE_ERR_UNSUPPORTED, "grouped_gemm_mxfp4: epilogue %d", epi);
     REQUIRE(N >= 1, MOE_ERR_SHAPE, "grouped_gemm_mxfp4: N=%d not positive", N);
     REQUIRE(epi < MOE_MX_SWIGLU_BF16 || N % 256 == 0, MOE_ERR_SHAPE, "grouped_gemm_mxfp4: SwiGLU needs N=%d a multiple of 256", N);
-    REQUIRE((int64_t)N * (K / 2) <= MOST, MOE_ERR_UNSUPPORTED, "grouped_gemm_mxfp4: one group's B exceeds 32-bit offsets");
+    REQUIRE(((int64_t)N + 256) * (K / 2) <= MOST, MOE_ERR_UNSUPPORTED, "grouped_gemm_mxfp4: one group's B exceeds 32-bit offsets");
+    REQUIRE(((M_total + 127) / 128 + G) * (((int64_t)N + 255) / 256) < (int64_t)1 << 31, MOE_ERR_UNSUPPORTED,
+            "grouped_gemm_mxfp4: too many tiles");
     REQUIRE(a_rows >= 0 && a_rows < ((int64_t)1 << 31) && a_rows * (K / 2) <= MOST, MOE_ERR_UNSUPPORTED,
             "grouped_gemm_mxfp4: A of %lld rows exceeds 32-bit offsets", (long long)a_rows);
     REQUIRE(a_row_index || M_total <= a_rows, MOE_ERR_SHAPE, "grouped_gemm_mxfp4: A has %lld rows, fewer than M_total=%lld",

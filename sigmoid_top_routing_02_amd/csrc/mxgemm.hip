@@ -32,6 +32,9 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 // reads there return 0 and touch no memory.
 constexpr uint32_t OUT = 0xFFFF0000u;
 
+template <int V>
+struct IC { static constexpr int value = V; };
+
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
 }
@@ -142,6 +145,43 @@ __device__ __forceinline__ void store_mx_block(uint8_t* out_q, uint8_t* out_s, i
         uint16_t* o = reinterpret_cast<uint16_t*>(out_q + block * 16);
         o[kb] = (uint16_t)w;
         o[4 + kb] = (uint16_t)(w >> 16);
+        if (kb == 0) out_s[block] = (uint8_t)byte;
+    }
+}
+
+// 32 columns of h as one MXFP4 block, lane l having columns 8 q + 4 (l / 32) + e
+// of row l % 32 in h[q][e]: the two lanes of a row exchange half their codes and
+// store 8 bytes each.
+__device__ __forceinline__ void store_mx_row(uint8_t* out_q, uint8_t* out_s, int64_t block, int kb, bool live,
+                                             const v4f (&h)[4]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t a = __float_as_uint(h[q][e]) << 1;
+            m = a > m ? a : m;
+        }
+    const uint32_t o = (uint32_t)__shfl_xor((int)m, 32, 64);
+    m = (o > m ? o : m) >> 24;
+    const uint32_t byte = m == 255u ? 255u : m > 2u ? m - 2u : 0u;
+    const float s = byte == 255u ? 1.0f : __uint_as_float(byte ? byte << 23 : 0x00400000u);
+    uint32_t w[2];                                       // 16 bits of codes for each q
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, h[2 * i][0], h[2 * i][1], s, 0);
+        w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], h[2 * i][2], h[2 * i][3], s, 1);
+        w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], h[2 * i + 1][0], h[2 * i + 1][1], s, 2);
+        w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[i], h[2 * i + 1][2], h[2 * i + 1][3], s, 3);
+        if (byte == 255u) w[i] = 0;
+    }
+    // bytes of the block: q = 0 lanes' 2, their partners' 2, q = 1, ...; lane 0 of
+    // a row keeps q = 0 and 1, its partner q = 2 and 3
+    const uint32_t mine = kb ? w[1] : w[0], got = (uint32_t)__shfl_xor((int)(kb ? w[0] : w[1]), 32, 64);
+    const uint32_t lo = kb ? got : mine, hi = kb ? mine : got;
+    if (live) {
+        *reinterpret_cast<uint2*>(out_q + block * 16 + kb * 8) =
+            make_uint2((lo & 0xFFFFu) | (hi << 16), (lo >> 16) | (hi & 0xFFFF0000u));
         if (kb == 0) out_s[block] = (uint8_t)byte;
     }
 }
@@ -279,23 +319,353 @@ void launch_rows(const MxGemmArgs& a, hipStream_t st) {
         hipLaunchKernelGGL((mxgemm_rows_kernel<EPI, MI, NT, false>), grid, dim3(256), 0, st, a);
 }
 
+
+// ---------------------------------------------------------------- many rows to a group
+//
+// Block tile BM (256 or 128) x 256, one block of four waves to a CU, a wave has
+// BM/2 x 128 of it in 32 x 32 tiles (32x32x64 scaled instructions, which reach
+// a higher rate than 16x16x128 on this card's power: 6.7 against 6.3 PFLOP/s
+// from registers with random codes).  The accumulators fill the 256
+// accumulation registers of a wave, so one operand byte read from LDS serves
+// 128 multiplications and LDS is read at half its rate.
+//
+// Stages of 256 values of K (128-byte rows) go from memory to LDS by DMA, two
+// in turn.  Lane l's four operands of a stage are blocks 4 (l / 32) .. + 3 of the
+// stage's eight and its four scale bytes one word, as above.
+constexpr int TN = 256;
+constexpr int STAGE_BYTES = 128;                         // of a row
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+// One LDS object per stage and operand, named at compile time at every access:
+// the compiler then sees that a read of one does not touch the DMA into another.
+__shared__ __attribute__((aligned(1024))) char g_a0[256 * STAGE_BYTES];
+__shared__ __attribute__((aligned(1024))) char g_a1[256 * STAGE_BYTES];
+__shared__ __attribute__((aligned(1024))) char g_b0[TN * STAGE_BYTES];
+__shared__ __attribute__((aligned(1024))) char g_b1[TN * STAGE_BYTES];
+template <int ST> __device__ __forceinline__ char* a_buf() { return ST ? g_a1 : g_a0; }
+template <int ST> __device__ __forceinline__ char* b_buf() { return ST ? g_b1 : g_b0; }
+
+// global -> LDS: lane l's 16 bytes, from voff + soff, land at lds + 16 l.
+__device__ __forceinline__ void lds_dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, char* lds) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, voff, soff, 0, 0);
+}
+
+// The 16-byte chunk c of row r lies in slot c ^ swz(r) of its 128 bytes: 8
+// neighbouring rows read one chunk from 8 slots, 16 rows from all 64 banks.
+__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+#define FENCE() __builtin_amdgcn_sched_barrier(0)
+
+template <int J>
+__device__ __forceinline__ v16f mfma32(v4u a, v4u b, v16f c, uint32_t sa, uint32_t sb) {
+    const v8i x = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+    const v8i y = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, J, (int)sa, J, (int)sb);
+}
+
+// Scale bytes blk .. blk + 3 of a row of nblk (zero past its end), the first of
+// them at row + at; row may be OUT.
+template <bool KA>
+__device__ __forceinline__ uint32_t scale_word(__amdgpu_buffer_rsrc_t d, uint32_t row, int at, int blk, int nblk) {
+    if constexpr (KA) {
+        return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(d, blk < nblk ? row : OUT, at, 0);
+    } else {
+        uint32_t w = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
+                     d, blk + j < nblk && row != OUT ? row + (uint32_t)j : OUT, at, 0) << (8 * j);
+        return w;
+    }
+}
+
+// First B row, inside the block's 256, of the wave's column tile t (of 4).
+template <bool SWIGLU>
+__device__ __forceinline__ int tile_row(int wn, int t) {
+    return SWIGLU ? wn * 64 + (t & 1) * 32 + (t >> 1) * 128 : wn * 128 + t * 32;
+}
+
+template <int EPI, int BM, bool KA>
+__global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
+    constexpr bool SWIGLU = EPI == MOE_MX_SWIGLU_BF16 || EPI == MOE_MX_SWIGLU_QUANT;
+    constexpr int MT = BM / 64;                          // 32-row tiles of a wave
+    constexpr int A_DMA = BM / 32, B_DMA = TN / 32;      // 1 KiB (8 rows) DMAs of a wave per stage
+    constexpr int CHUNK_M = 2048 / BM;                   // row tiles that go through the columns together
+    __shared__ int start[1025];                          // first row tile of each group
+    __shared__ int found;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
+    const int lr = lane & 31, kb = lane >> 5;
+    const int total = (int)p.M_total;
+    const int nblk = p.K / 32, ns = (nblk + 15) / 16 * 2;      // stages, an even number: those past K are zeros
+    const uint32_t rb = (uint32_t)p.K / 2;
+
+    // Row tiles before each group: four groups a thread, then a scan of the threads.
+    {
+        int n[4], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int g = tid * 4 + i;
+            n[i] = 0;
+            if (g < p.G) {
+                const int lo = min(max(p.group_offset[g], 0), total), hi = min(p.group_offset[g + 1], total);
+                n[i] = hi > lo ? (hi - lo + BM - 1) / BM : 0;
+            }
+            sum += n[i];
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(incl, o, 64);
+            if (lane >= o) incl += v;
+        }
+        int* wsum = reinterpret_cast<int*>(g_a0);
+        if (lane == 63) wsum[wave] = incl;
+        __syncthreads();
+        int at = incl - sum;
+        for (int w = 0; w < wave; ++w) at += wsum[w];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            start[tid * 4 + i] = at;
+            at += n[i];
+        }
+        if (tid == 255) start[1024] = at;
+        __syncthreads();
+    }
+    const int n_tiles = (p.N + TN - 1) / TN;
+    const int tiles = start[p.G] * n_tiles;              // the C ABI keeps it under 2^31
+    // Blocks go to the eight XCDs in turn; each XCD has one stretch of the tiles
+    // and its blocks take neighbouring ones, which share operands in its L2.
+    const int share = (tiles + 7) / 8, xcd = (int)blockIdx.x & 7, t_step = (int)gridDim.x >> 3;
+    const int t_end = min(tiles, (xcd + 1) * share);
+    int t = xcd * share + ((int)blockIdx.x >> 3);
+
+    const auto aq = make_rsrc(p.a_q, (uint32_t)(p.a_rows * rb)), as = make_rsrc(p.a_s, (uint32_t)(p.a_rows * nblk));
+    auto bq = aq, bs = as;
+    struct Tile { int g, m0, hi, n0; } T, U;
+    uint32_t aro[A_DMA], bro[2], aso[MT], bso[4];
+    uint32_t sa[2][MT], sb[2][4];
+    v16f acc[4][MT];
+    v4u fa[2][MT], fb[2][4];
+
+    auto locate = [&](int at) {                          // every thread of the block
+        __syncthreads();
+        const int rt = at / n_tiles;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int g = tid * 4 + i;
+            if (start[g] <= rt && rt < start[g + 1]) found = g;
+        }
+        __syncthreads();
+        Tile v;
+        v.g = __builtin_amdgcn_readfirstlane(found);
+        const int first = __builtin_amdgcn_readfirstlane(start[v.g]);
+        const int n = __builtin_amdgcn_readfirstlane(start[v.g + 1]) - first;    // the group's row tiles
+        const int inside = at - first * n_tiles;
+        const int chunk = inside / (CHUNK_M * n_tiles), left = inside - chunk * CHUNK_M * n_tiles;
+        const int cm = min(CHUNK_M, n - chunk * CHUNK_M);
+        const int lo = min(max(__builtin_amdgcn_readfirstlane(p.group_offset[v.g]), 0), total);
+        v.hi = min(__builtin_amdgcn_readfirstlane(p.group_offset[v.g + 1]), total);
+        v.m0 = lo + (chunk * CHUNK_M + left % cm) * BM;
+        v.n0 = left / cm * TN;
+        return v;
+    };
+    // A 1 KiB DMA fills eight rows: lane l brings slot l % 8 of row l / 8, which
+    // is chunk slot ^ swz(row), and swz takes the parity of the eight in its
+    // fourth bit.
+    const int chunk_of[2] = {(lane & 7) ^ swz(lane >> 3), (lane & 7) ^ swz((lane >> 3) + 8)};
+    auto setup = [&](const Tile& v) {
+        bq = make_rsrc(p.b_q + (int64_t)v.g * p.N * rb, (uint32_t)p.N * rb);
+        bs = make_rsrc(p.b_s + (int64_t)v.g * p.N * nblk, (uint32_t)p.N * (uint32_t)nblk);
+        // the row of A behind row m of the product; OUT where there is none
+        auto a_row = [&](int m) {
+            const uint32_t r = m < v.hi ? (p.a_row_index ? (uint32_t)p.a_row_index[m] : (uint32_t)m) : 0xFFFFFFFFu;
+            return r < (uint32_t)p.a_rows ? r : OUT;
+        };
+#pragma unroll
+        for (int i = 0; i < A_DMA; ++i) {
+            const uint32_t r = a_row(v.m0 + (wave * A_DMA + i) * 8 + (lane >> 3));
+            aro[i] = r == OUT ? OUT : r * rb + (uint32_t)chunk_of[i & 1] * 16u;
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const uint32_t r = a_row(v.m0 + wm * (BM / 2) + i * 32 + lr);
+            aso[i] = r == OUT ? OUT : r * (uint32_t)nblk + (uint32_t)kb * 4u;
+        }
+        // rows past N lie past the end of B's descriptors
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            bro[i] = (uint32_t)(v.n0 + (wave * B_DMA + i) * 8 + (lane >> 3)) * rb + (uint32_t)chunk_of[i] * 16u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            bso[i] = (uint32_t)(v.n0 + tile_row<SWIGLU>(wn, i) + lr) * (uint32_t)nblk + (uint32_t)kb * 4u;
+    };
+    // Stage s of K into LDS stage ST.  Chunks past the end of K read zero.
+    auto send = [&](auto stc, int s) {
+        constexpr int ST = decltype(stc)::value;
+        const bool in[2] = {s * 8 + chunk_of[0] < nblk, s * 8 + chunk_of[1] < nblk};
+#pragma unroll
+        for (int i = 0; i < A_DMA; ++i)
+            lds_dma16(aq, in[i & 1] ? aro[i] : OUT, s * STAGE_BYTES, a_buf<ST>() + (wave * A_DMA + i) * 1024);
+#pragma unroll
+        for (int i = 0; i < B_DMA; ++i)
+            lds_dma16(bq, in[i & 1] ? bro[i & 1] + (uint32_t)(i & ~1) * 8u * rb : OUT, s * STAGE_BYTES,
+                      b_buf<ST>() + (wave * B_DMA + i) * 1024);
+    };
+    // The scales of stage s into register set ST.
+    auto scales = [&](auto stc, int s) {
+        constexpr int ST = decltype(stc)::value;
+        const int blk = s * 8 + kb * 4;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) sa[ST][i] = scale_word<KA>(as, aso[i], s * 8, blk, nblk);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sb[ST][i] = scale_word<KA>(bs, bso[i], s * 8, blk, nblk);
+    };
+    uint32_t slot[4];                                    // the lane's chunk of step j in its row
+#pragma unroll
+    for (int j = 0; j < 4; ++j) slot[j] = (uint32_t)lr * STAGE_BYTES + (uint32_t)(((kb * 4 + j) ^ swz(lr)) * 16);
+    auto read = [&](auto stc, auto jc, auto fc) {
+        constexpr int ST = decltype(stc)::value, J = decltype(jc)::value, F = decltype(fc)::value;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            fb[F][i] = *reinterpret_cast<const v4u*>(b_buf<ST>() + tile_row<SWIGLU>(wn, i) * STAGE_BYTES + slot[J]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            fa[F][i] = *reinterpret_cast<const v4u*>(a_buf<ST>() + (wm * (BM / 2) + i * 32) * STAGE_BYTES + slot[J]);
+    };
+    auto multiply = [&](auto stc, auto jc, auto fc) {
+        constexpr int ST = decltype(stc)::value, J = decltype(jc)::value, F = decltype(fc)::value;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) acc[n][i] = mfma32<J>(fb[F][n], fa[F][i], acc[n][i], sb[ST][n], sa[ST][i]);
+    };
+    constexpr IC<0> c0{};
+    constexpr IC<1> c1{};
+    constexpr IC<2> c2{};
+    constexpr IC<3> c3{};
+    // Lane l has columns 8 q + 4 (l / 32) + e of row l % 32 of each 32 x 32 tile in
+    // element 4 q + e.
+    auto store = [&](const Tile& v) {
+                auto quad = [](const v16f& v, int q) { return v4f{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]}; };
+        #pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const int m = v.m0 + wm * (BM / 2) + i * 32 + lr;
+                    const bool live = m < v.hi;
+                    if constexpr (SWIGLU) {
+        #pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const int col = v.n0 / 2 + wn * 64 + n * 32;
+                            v4f h[4];
+        #pragma unroll
+                            for (int q = 0; q < 4; ++q) h[q] = swiglu(quad(acc[n][i], q), quad(acc[n + 2][i], q));
+                            if constexpr (EPI == MOE_MX_SWIGLU_BF16) {
+        #pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    if (live) store4<false>(p.out, m, col + 8 * q + 4 * kb, p.N / 2, h[q]);
+                            } else {
+                                store_mx_row(p.out_q, p.out_s, (int64_t)m * (p.N / 64) + col / 32, kb, live, h);
+                            }
+                        }
+                    } else {
+        #pragma unroll
+                        for (int n = 0; n < 4; ++n)
+        #pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (live)
+                                    store4<EPI == MOE_MX_STORE_F32>(p.out, m, v.n0 + tile_row<false>(wn, n) + 8 * q + 4 * kb,
+                                                                    p.N, quad(acc[n][i], q));
+                    }
+                }
+    };
+    // Every DMA and scale sent for has arrived, and every wave has read what it asked of LDS.
+    auto landed = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+    // Stage s from LDS stage ST.  The operands of a step are read while the one
+    // before is multiplied.  Before the last step every wave has read all of the
+    // stage, and stage s + 1 has landed; stage s + 2 is then sent for into the
+    // place of stage s.  Past the last stage the same instructions read zeros and
+    // stale operands that nothing uses, so that the loop has no branches.
+    auto stage = [&](auto stc, auto other, int s) {
+        FENCE();
+        read(stc, c1, c1);
+        multiply(stc, c0, c0);
+        FENCE();
+        read(stc, c2, c0);
+        multiply(stc, c1, c1);
+        FENCE();
+        read(stc, c3, c1);
+        multiply(stc, c2, c0);
+        FENCE();
+        landed();
+        read(other, c0, c0);
+        send(stc, s + 2);
+        multiply(stc, c3, c1);
+        scales(stc, s + 2);
+        FENCE();
+    };
+    for (bool before = false;; before = true) {
+        const bool more = t < t_end;
+        if (more) {                                      // the first two stages travel during the last tile's stores
+            T = locate(t);
+            setup(T);
+            send(c0, 0);
+            scales(c0, 0);
+            send(c1, 1);
+            scales(c1, 1);
+        }
+        if (before) store(U);
+        if (!more) break;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[n][i][e] = 0.0f;
+        landed();
+        read(c0, c0, c0);
+        for (int s = 0; s < ns; s += 2) {
+            stage(c0, c1, s);
+            stage(c1, c0, s + 1);
+        }
+        landed();                                        // the zeros of the stages past the last
+        U = T;
+        t += t_step;
+    }
+}
+template <int EPI, int BM>
+hipError_t launch_tiles(const MxGemmArgs& a, hipStream_t st) {
+    int dev = 0, cus = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e != hipSuccess) return e;
+    const int64_t most = ((a.M_total + BM - 1) / BM + a.G) * ((a.N + TN - 1) / TN);
+    const int64_t want = most < cus ? most : cus;
+    const dim3 grid((unsigned)((want + 7) / 8 * 8));      // the same count on every XCD
+    if (a.K % 128 == 0) hipLaunchKernelGGL((mxgemm_tile_kernel<EPI, BM, true>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((mxgemm_tile_kernel<EPI, BM, false>), grid, dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
 template <int EPI>
-void launch_epi(const MxGemmArgs& a, hipStream_t st) {
+hipError_t launch_epi(const MxGemmArgs& a, hipStream_t st) {
     const int64_t rows = (a.M_total + a.G - 1) / a.G;    // rows of a group, on the average
     if (rows <= 16) launch_rows<EPI, 1>(a, st);
-    else launch_rows<EPI, 4>(a, st);
+    else if (rows <= 48) launch_rows<EPI, 4>(a, st);
+    else if (rows <= 192) return launch_tiles<EPI, 128>(a, st);
+    else return launch_tiles<EPI, 256>(a, st);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_grouped_gemm_mxfp4(const MxGemmArgs& a, int epi, hipStream_t st) {
     switch (epi) {
-        case MOE_MX_STORE_F32: launch_epi<MOE_MX_STORE_F32>(a, st); break;
-        case MOE_MX_STORE_BF16: launch_epi<MOE_MX_STORE_BF16>(a, st); break;
-        case MOE_MX_SWIGLU_BF16: launch_epi<MOE_MX_SWIGLU_BF16>(a, st); break;
-        default: launch_epi<MOE_MX_SWIGLU_QUANT>(a, st); break;
+        case MOE_MX_STORE_F32: return launch_epi<MOE_MX_STORE_F32>(a, st);
+        case MOE_MX_STORE_BF16: return launch_epi<MOE_MX_STORE_BF16>(a, st);
+        case MOE_MX_SWIGLU_BF16: return launch_epi<MOE_MX_SWIGLU_BF16>(a, st);
+        default: return launch_epi<MOE_MX_SWIGLU_QUANT>(a, st);
     }
-    return hipGetLastError();
 }
 
 }  // namespace moe
