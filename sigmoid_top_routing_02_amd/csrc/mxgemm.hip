@@ -16,6 +16,8 @@
 //
 // The weights are the instruction's first operand: a lane then holds four
 // neighbouring columns of one output row.
+#include <utility>
+
 #include "device_math.h"
 #include "kernels.h"
 #include "moe_fp8.h"
@@ -111,6 +113,23 @@ __device__ __forceinline__ void store4(void* out, int64_t m, int n, int ld, v4f 
             if (n + i < ld) {
                 if constexpr (F32) static_cast<float*>(out)[at + i] = v[i];
                 else static_cast<uint16_t*>(out)[at + i] = (uint16_t)((i & 2 ? w.y : w.x) >> (16 * (i & 1)));
+            }
+    }
+}
+
+// 16 bytes of row m of an [*, ld] output from column n on, FP32 or bf16, cut at ld.
+template <bool F32>
+__device__ __forceinline__ void store16(void* out, int64_t m, int n, int ld, v4u x) {
+    constexpr int PER = F32 ? 4 : 8;
+    const int64_t at = m * ld + n;
+    if (ld % PER == 0) {                                  // rows start on 16 bytes; n is a multiple of PER
+        if (n < ld) *reinterpret_cast<v4u*>(static_cast<char*>(out) + at * (16 / PER)) = x;
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (n + i < ld) {
+                if constexpr (F32) static_cast<uint32_t*>(out)[at + i] = x[i];
+                else static_cast<uint16_t*>(out)[at + i] = (uint16_t)(x[i / 2] >> (16 * (i & 1)));
             }
     }
 }
@@ -329,33 +348,76 @@ void launch_rows(const MxGemmArgs& a, hipStream_t st) {
 // accumulation registers of a wave, so one operand byte read from LDS serves
 // 128 multiplications and LDS is read at half its rate.
 //
-// Stages of 256 values of K (128-byte rows) go from memory to LDS by DMA, two
-// in turn.  Lane l's four operands of a stage are blocks 4 (l / 32) .. + 3 of the
-// stage's eight and its four scale bytes one word, as above.
+// Stages of 128 values of K (64-byte rows) go from memory to LDS by DMA through a
+// ring of four, sent for three stages ahead.  The scales of a chunk of four stages
+// (16 bytes a row) pass through registers into one of two buffers a chunk ahead,
+// one row a thread, so that a line of scales is touched once per chunk and not by
+// every wave in every stage.  Lane l's two operands of a stage are blocks
+// 2 (l / 32) and + 1 of its four: a row's 16 bytes are put into LDS as the 8 of
+// lanes 0-31, stage by stage, then the 8 of lanes 32-63.
 constexpr int TN = 256;
-constexpr int STAGE_BYTES = 128;                         // of a row
+constexpr int STAGE_BYTES = 64;                          // of a row
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
 
-// One LDS object per stage and operand, named at compile time at every access:
-// the compiler then sees that a read of one does not touch the DMA into another.
-__shared__ __attribute__((aligned(1024))) char g_a0[256 * STAGE_BYTES];
-__shared__ __attribute__((aligned(1024))) char g_a1[256 * STAGE_BYTES];
-__shared__ __attribute__((aligned(1024))) char g_b0[TN * STAGE_BYTES];
-__shared__ __attribute__((aligned(1024))) char g_b1[TN * STAGE_BYTES];
-template <int ST> __device__ __forceinline__ char* a_buf() { return ST ? g_a1 : g_a0; }
-template <int ST> __device__ __forceinline__ char* b_buf() { return ST ? g_b1 : g_b0; }
+// One LDS object per stage (A's rows, B's rows), named at compile time at every
+// access, so that the compiler sees that a read of one does not touch the DMA into
+// another.  The scales of an even and of an odd chunk (512 rows of 16 bytes each)
+// lie behind the first stage, whose DMA has landed wherever they are read: the
+// compiler waits for every DMA before a read that it knows to touch none.
+constexpr int B_AT = 256 * STAGE_BYTES, SCALE_AT = 2 * B_AT, SCALE_BYTES = 512 * 16;
+__shared__ __attribute__((aligned(1024))) char g_s0[SCALE_AT + 2 * SCALE_BYTES];
+__shared__ __attribute__((aligned(1024))) char g_s1[2 * B_AT];
+__shared__ __attribute__((aligned(1024))) char g_s2[2 * B_AT];
+__shared__ __attribute__((aligned(1024))) char g_s3[2 * B_AT];
+template <int ST> __device__ __forceinline__ char* stage_buf() {
+    if constexpr (ST == 0) return g_s0;
+    else if constexpr (ST == 1) return g_s1;
+    else if constexpr (ST == 2) return g_s2;
+    else return g_s3;
+}
 
 // global -> LDS: lane l's 16 bytes, from voff + soff, land at lds + 16 l.
 __device__ __forceinline__ void lds_dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, char* lds) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, voff, soff, 0, 0);
 }
+// Writes 16 bytes to LDS, unseen by the compiler, which would first wait for every
+// DMA under way into the object; the barrier that readers pass waits for it.
+__device__ __forceinline__ void lds_put(char* lds, v4u v) {
+    asm volatile("ds_write_b128 %0, %1" ::"v"((uint32_t)(uintptr_t)(lds_void*)lds), "v"(v) : "memory");
+}
 
-// The 16-byte chunk c of row r lies in slot c ^ swz(r) of its 128 bytes: 8
-// neighbouring rows read one chunk from 8 slots, 16 rows from all 64 banks.
-__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+// A row's scale bytes 0 .. 15 in the order in which lanes read them.
+__device__ __forceinline__ v4u deal_scales(v4u v) {
+    const uint32_t LO = 0x05040100u, HI = 0x07060302u;   // bytes 0, 1 (2, 3) of the second word, then of the first
+    return v4u{__builtin_amdgcn_perm(v[1], v[0], LO), __builtin_amdgcn_perm(v[3], v[2], LO),
+               __builtin_amdgcn_perm(v[1], v[0], HI), __builtin_amdgcn_perm(v[3], v[2], HI)};
+}
+
+// The 16-byte chunk c of row r lies in slot c ^ swz(r) of its 64 bytes: 8
+// neighbouring rows read one chunk from 8 slots of 128 bytes, 16 rows from all
+// 64 banks.
+__device__ __forceinline__ int swz(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
 
 #define FENCE() __builtin_amdgcn_sched_barrier(0)
+#define SCHED(KIND, N) __builtin_amdgcn_sched_group_barrier(KIND, N, 0)
+constexpr int MFMA = 0x8, VMEM = 0x20, DS_READ = 0x100;
+
+template <int READS, int LOADS, int... I>
+__device__ __forceinline__ void interleave_slots(std::integer_sequence<int, I...>) {
+    constexpr int S = sizeof...(I);
+    // slot I's share of n things dealt to S slots, the first ones first
+#define SHARE(n) (((I + 1) * (n) + S - 1) / S - (I * (n) + S - 1) / S)
+    ((SHARE(READS) ? SCHED(DS_READ, SHARE(READS)) : void(), SCHED(MFMA, 1),
+      SHARE(LOADS) ? SCHED(VMEM, SHARE(LOADS)) : void()), ...);
+#undef SHARE
+}
+
+// Deals the LDS reads and vector loads of a step out among its matrix instructions.
+template <int MATRIX, int READS, int LOADS>
+__device__ __forceinline__ void interleave() {
+    interleave_slots<READS, LOADS>(std::make_integer_sequence<int, MATRIX>{});
+}
 
 template <int J>
 __device__ __forceinline__ v16f mfma32(v4u a, v4u b, v16f c, uint32_t sa, uint32_t sb) {
@@ -364,21 +426,39 @@ __device__ __forceinline__ v16f mfma32(v4u a, v4u b, v16f c, uint32_t sa, uint32
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, J, (int)sa, J, (int)sb);
 }
 
-// Scale bytes blk .. blk + 3 of a row of nblk (zero past its end), the first of
-// them at row + at; row may be OUT.
+// 16 scale bytes of a row, blocks 16 c .. + 15; those past the row's nblk blocks
+// are zero, whatever lies there.  KA: the row starts on a word.  Otherwise the
+// five words around the bytes are read (the last row's may hold up to three bytes
+// past the tensor's end, in the word of its last byte) and shifted.
 template <bool KA>
-__device__ __forceinline__ uint32_t scale_word(__amdgpu_buffer_rsrc_t d, uint32_t row, int at, int blk, int nblk) {
-    if constexpr (KA) {
-        return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(d, blk < nblk ? row : OUT, at, 0);
-    } else {
-        uint32_t w = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
-                     d, blk + j < nblk && row != OUT ? row + (uint32_t)j : OUT, at, 0) << (8 * j);
-        return w;
+struct Scales {
+    v4u w;
+    uint32_t more;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t d, uint32_t row, int c) {
+        if constexpr (KA) {
+            w = __builtin_amdgcn_raw_buffer_load_b128(d, row, c * 16, 0);
+        } else {
+            w = __builtin_amdgcn_raw_buffer_load_b128(d, row & ~3u, c * 16, 0);
+            more = __builtin_amdgcn_raw_buffer_load_b32(d, (row & ~3u) + 16u, c * 16, 0);
+        }
     }
-}
+    __device__ __forceinline__ v4u bytes(uint32_t row, int c, int nblk) const {
+        v4u v = w;
+        if constexpr (!KA) {
+            const uint32_t sh = (row & 3u) * 8u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = (uint32_t)((((uint64_t)(j < 3 ? w[j + 1] : more) << 32) | w[j]) >> sh);
+        }
+        const int left = nblk - c * 16;                  // of the row's blocks
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = left - 4 * j;
+            v[j] = n >= 4 ? v[j] : n <= 0 ? 0u : KA ? v[j] : v[j] & ((1u << (8 * n)) - 1u);
+        }
+        return v;
+    }
+};
 
 // First B row, inside the block's 256, of the wave's column tile t (of 4).
 template <bool SWIGLU>
@@ -390,7 +470,8 @@ template <int EPI, int BM, bool KA>
 __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
     constexpr bool SWIGLU = EPI == MOE_MX_SWIGLU_BF16 || EPI == MOE_MX_SWIGLU_QUANT;
     constexpr int MT = BM / 64;                          // 32-row tiles of a wave
-    constexpr int A_DMA = BM / 32, B_DMA = TN / 32;      // 1 KiB (8 rows) DMAs of a wave per stage
+    constexpr int A_DMA = BM / 64, B_DMA = TN / 64;      // 1 KiB (16 rows) DMAs of a wave per stage
+    constexpr int ND = A_DMA + B_DMA, NSC = KA ? 2 : 4;  // vector loads of a stage, and of a chunk's scales
     constexpr int CHUNK_M = 2048 / BM;                   // row tiles that go through the columns together
     __shared__ int start[1025];                          // first row tile of each group
     __shared__ int found;
@@ -398,7 +479,7 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
     const int lr = lane & 31, kb = lane >> 5;
     const int total = (int)p.M_total;
-    const int nblk = p.K / 32, ns = (nblk + 15) / 16 * 2;      // stages, an even number: those past K are zeros
+    const int nblk = p.K / 32, nchunk = (nblk + 15) / 16;
     const uint32_t rb = (uint32_t)p.K / 2;
 
     // Row tiles before each group: four groups a thread, then a scan of the threads.
@@ -420,7 +501,7 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
             const int v = __shfl_up(incl, o, 64);
             if (lane >= o) incl += v;
         }
-        int* wsum = reinterpret_cast<int*>(g_a0);
+        int* wsum = reinterpret_cast<int*>(g_s0);
         if (lane == 63) wsum[wave] = incl;
         __syncthreads();
         int at = incl - sum;
@@ -441,11 +522,15 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
     const int t_end = min(tiles, (xcd + 1) * share);
     int t = xcd * share + ((int)blockIdx.x >> 3);
 
-    const auto aq = make_rsrc(p.a_q, (uint32_t)(p.a_rows * rb)), as = make_rsrc(p.a_s, (uint32_t)(p.a_rows * nblk));
+    // Scale descriptors end on a word.  A group's scales may start off one: the
+    // descriptor then starts at the word before and the offsets begin at the rest.
+    const auto aq = make_rsrc(p.a_q, (uint32_t)(p.a_rows * rb));
+    const auto as = make_rsrc(p.a_s, ((uint32_t)(p.a_rows * nblk) + 3u) & ~3u);
     auto bq = aq, bs = as;
     struct Tile { int g, m0, hi, n0; } T, U;
-    uint32_t aro[A_DMA], bro[2], aso[MT], bso[4];
+    uint32_t aro[A_DMA], bro[B_DMA], aso, bso;
     uint32_t sa[2][MT], sb[2][4];
+    Scales<KA> ca, cb;
     v16f acc[4][MT];
     v4u fa[2][MT], fb[2][4];
 
@@ -471,13 +556,13 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
         v.n0 = left / cm * TN;
         return v;
     };
-    // A 1 KiB DMA fills eight rows: lane l brings slot l % 8 of row l / 8, which
-    // is chunk slot ^ swz(row), and swz takes the parity of the eight in its
-    // fourth bit.
-    const int chunk_of[2] = {(lane & 7) ^ swz(lane >> 3), (lane & 7) ^ swz((lane >> 3) + 8)};
+    // A 1 KiB DMA fills 16 rows: lane l brings slot l % 4 of row l / 4.
+    const int chunk_of = (lane & 3) ^ swz(lane >> 2);
     auto setup = [&](const Tile& v) {
         bq = make_rsrc(p.b_q + (int64_t)v.g * p.N * rb, (uint32_t)p.N * rb);
-        bs = make_rsrc(p.b_s + (int64_t)v.g * p.N * nblk, (uint32_t)p.N * (uint32_t)nblk);
+        const int64_t sg = (int64_t)v.g * p.N * nblk;
+        const uint32_t off = KA ? 0u : (uint32_t)sg & 3u;
+        bs = make_rsrc(p.b_s + (sg - off), ((uint32_t)p.N * (uint32_t)nblk + off + 3u) & ~3u);
         // the row of A behind row m of the product; OUT where there is none
         auto a_row = [&](int m) {
             const uint32_t r = m < v.hi ? (p.a_row_index ? (uint32_t)p.a_row_index[m] : (uint32_t)m) : 0xFFFFFFFFu;
@@ -485,154 +570,215 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
         };
 #pragma unroll
         for (int i = 0; i < A_DMA; ++i) {
-            const uint32_t r = a_row(v.m0 + (wave * A_DMA + i) * 8 + (lane >> 3));
-            aro[i] = r == OUT ? OUT : r * rb + (uint32_t)chunk_of[i & 1] * 16u;
+            const uint32_t r = a_row(v.m0 + (wave * A_DMA + i) * 16 + (lane >> 2));
+            aro[i] = r == OUT ? OUT : r * rb + (uint32_t)chunk_of * 16u;
         }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const uint32_t r = a_row(v.m0 + wm * (BM / 2) + i * 32 + lr);
-            aso[i] = r == OUT ? OUT : r * (uint32_t)nblk + (uint32_t)kb * 4u;
-        }
+        const uint32_t r = tid < BM ? a_row(v.m0 + tid) : OUT;
+        aso = r == OUT ? OUT : r * (uint32_t)nblk;
         // rows past N lie past the end of B's descriptors
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            bro[i] = (uint32_t)(v.n0 + (wave * B_DMA + i) * 8 + (lane >> 3)) * rb + (uint32_t)chunk_of[i] * 16u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            bso[i] = (uint32_t)(v.n0 + tile_row<SWIGLU>(wn, i) + lr) * (uint32_t)nblk + (uint32_t)kb * 4u;
+        for (int i = 0; i < B_DMA; ++i)
+            bro[i] = (uint32_t)(v.n0 + (wave * B_DMA + i) * 16 + (lane >> 2)) * rb + (uint32_t)chunk_of * 16u;
+        bso = (uint32_t)(v.n0 + tid) * (uint32_t)nblk + off;
     };
-    // Stage s of K into LDS stage ST.  Chunks past the end of K read zero.
-    auto send = [&](auto stc, int s) {
+    // Stage s of K into LDS stage ST, A and B.  Blocks past the end of K read zero.
+    auto send_a = [&](auto stc, int s) {
         constexpr int ST = decltype(stc)::value;
-        const bool in[2] = {s * 8 + chunk_of[0] < nblk, s * 8 + chunk_of[1] < nblk};
+        const bool in = s * 4 + chunk_of < nblk;
 #pragma unroll
         for (int i = 0; i < A_DMA; ++i)
-            lds_dma16(aq, in[i & 1] ? aro[i] : OUT, s * STAGE_BYTES, a_buf<ST>() + (wave * A_DMA + i) * 1024);
+            lds_dma16(aq, in ? aro[i] : OUT, s * STAGE_BYTES, stage_buf<ST>() + (wave * A_DMA + i) * 1024);
+    };
+    auto send_b = [&](auto stc, int s) {
+        constexpr int ST = decltype(stc)::value;
+        const bool in = s * 4 + chunk_of < nblk;
 #pragma unroll
         for (int i = 0; i < B_DMA; ++i)
-            lds_dma16(bq, in[i & 1] ? bro[i & 1] + (uint32_t)(i & ~1) * 8u * rb : OUT, s * STAGE_BYTES,
-                      b_buf<ST>() + (wave * B_DMA + i) * 1024);
+            lds_dma16(bq, in ? bro[i] : OUT, s * STAGE_BYTES, stage_buf<ST>() + B_AT + (wave * B_DMA + i) * 1024);
     };
-    // The scales of stage s into register set ST.
-    auto scales = [&](auto stc, int s) {
-        constexpr int ST = decltype(stc)::value;
-        const int blk = s * 8 + kb * 4;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) sa[ST][i] = scale_word<KA>(as, aso[i], s * 8, blk, nblk);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sb[ST][i] = scale_word<KA>(bs, bso[i], s * 8, blk, nblk);
+    auto load_scales = [&](int c) {
+        ca.load(as, aso, c);
+        cb.load(bs, bso, c);
     };
-    uint32_t slot[4];                                    // the lane's chunk of step j in its row
+    auto write_scales = [&](int c) {
+        char* to = g_s0 + SCALE_AT + (c & 1) * SCALE_BYTES + tid * 16;
+        const v4u a = deal_scales(ca.bytes(aso, c, nblk)), b = deal_scales(cb.bytes(bso, c, nblk));
+        if (BM == 256 || tid < BM) lds_put(to, a);
+        lds_put(to + 256 * 16, b);
+    };
+    uint32_t slot[2];                                    // the lane's chunk of step j in its row
 #pragma unroll
-    for (int j = 0; j < 4; ++j) slot[j] = (uint32_t)lr * STAGE_BYTES + (uint32_t)(((kb * 4 + j) ^ swz(lr)) * 16);
-    auto read = [&](auto stc, auto jc, auto fc) {
-        constexpr int ST = decltype(stc)::value, J = decltype(jc)::value, F = decltype(fc)::value;
+    for (int j = 0; j < 2; ++j) slot[j] = (uint32_t)(lr * STAGE_BYTES + ((kb * 2 + j) ^ swz(lr)) * 16);
+    auto read = [&](auto stc, auto jc) {                 // the operands of step J of stage ST, into set J
+        constexpr int ST = decltype(stc)::value, J = decltype(jc)::value;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            fb[F][i] = *reinterpret_cast<const v4u*>(b_buf<ST>() + tile_row<SWIGLU>(wn, i) * STAGE_BYTES + slot[J]);
+            fb[J][i] = *reinterpret_cast<const v4u*>(stage_buf<ST>() + B_AT + tile_row<SWIGLU>(wn, i) * STAGE_BYTES + slot[J]);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-            fa[F][i] = *reinterpret_cast<const v4u*>(a_buf<ST>() + (wm * (BM / 2) + i * 32) * STAGE_BYTES + slot[J]);
+            fa[J][i] = *reinterpret_cast<const v4u*>(stage_buf<ST>() + (wm * (BM / 2) + i * 32) * STAGE_BYTES + slot[J]);
     };
-    auto multiply = [&](auto stc, auto jc, auto fc) {
-        constexpr int ST = decltype(stc)::value, J = decltype(jc)::value, F = decltype(fc)::value;
+    // Word H of the lane's scales of chunk c: stages 2 H and 2 H + 1, bytes 0 and 1
+    // those of the first's steps 0 and 1, bytes 2 and 3 of the second's.
+    auto read_scales = [&](auto hc, int c) {
+        constexpr int H = decltype(hc)::value;
+        int off = SCALE_AT + (c & 1) * SCALE_BYTES + lr * 16 + kb * 8 + H * 4;
+        asm volatile("" : "+v"(off));                    // opaque: a read that may touch the stage's DMA
+        const char* at = g_s0 + off;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            sb[H][i] = *reinterpret_cast<const uint32_t*>(at + (256 + tile_row<SWIGLU>(wn, i)) * 16);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            sa[H][i] = *reinterpret_cast<const uint32_t*>(at + (wm * (BM / 2) + i * 32) * 16);
+    };
+    auto multiply = [&](auto stc, auto jc) {
+        constexpr int ST = decltype(stc)::value, J = decltype(jc)::value;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int n = 0; n < 4; ++n) acc[n][i] = mfma32<J>(fb[F][n], fa[F][i], acc[n][i], sb[ST][n], sa[ST][i]);
+            for (int n = 0; n < 4; ++n)
+                acc[n][i] = mfma32<(ST & 1) * 2 + J>(fb[J][n], fa[J][i], acc[n][i], sb[ST / 2][n], sa[ST / 2][i]);
     };
     constexpr IC<0> c0{};
     constexpr IC<1> c1{};
     constexpr IC<2> c2{};
     constexpr IC<3> c3{};
     // Lane l has columns 8 q + 4 (l / 32) + e of row l % 32 of each 32 x 32 tile in
-    // element 4 q + e.
+    // element 4 q + e.  FP32 and bf16 leave through LDS, 32 rows of 128 bytes at a
+    // time (the wave's own 4 KiB of the last stage's B rows, which the next tile's
+    // first three stages leave alone), so that eight lanes store one whole line;
+    // chunk c of a row lies in slot c ^ row % 8.
     auto store = [&](const Tile& v) {
-                auto quad = [](const v16f& v, int q) { return v4f{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]}; };
-        #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const int m = v.m0 + wm * (BM / 2) + i * 32 + lr;
-                    const bool live = m < v.hi;
-                    if constexpr (SWIGLU) {
-        #pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            const int col = v.n0 / 2 + wn * 64 + n * 32;
-                            v4f h[4];
-        #pragma unroll
-                            for (int q = 0; q < 4; ++q) h[q] = swiglu(quad(acc[n][i], q), quad(acc[n + 2][i], q));
-                            if constexpr (EPI == MOE_MX_SWIGLU_BF16) {
-        #pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    if (live) store4<false>(p.out, m, col + 8 * q + 4 * kb, p.N / 2, h[q]);
-                            } else {
-                                store_mx_row(p.out_q, p.out_s, (int64_t)m * (p.N / 64) + col / 32, kb, live, h);
-                            }
-                        }
+        auto quad = [](const v16f& x, int q) { return v4f{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]}; };
+        char* mine = g_s3 + B_AT + wave * 4096;
+        auto put16 = [&](int chunk, v4f x) { *reinterpret_cast<v4f*>(mine + lr * 128 + ((chunk ^ (lr & 7)) << 4)) = x; };
+        auto put8 = [&](int chunk, v4f x) {
+            *reinterpret_cast<uint2*>(mine + lr * 128 + ((chunk ^ (lr & 7)) << 4) + kb * 8) = pack4(x);
+        };
+        auto flush = [&](int m0, int col, int ld) {      // 32 rows from m0, 128 bytes from column col
+            constexpr bool F32 = EPI == MOE_MX_STORE_F32;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = i * 8 + (lane >> 3);
+                const v4u x = *reinterpret_cast<const v4u*>(mine + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                if (m0 + r < v.hi) store16<F32>(p.out, m0 + r, col + (lane & 7) * (F32 ? 4 : 8), ld, x);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int m0 = v.m0 + wm * (BM / 2) + i * 32;
+            if constexpr (EPI == MOE_MX_STORE_F32) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) put16(2 * q + kb, quad(acc[n][i], q));
+                    flush(m0, v.n0 + tile_row<false>(wn, n), p.N);
+                }
+            } else if constexpr (EPI == MOE_MX_STORE_BF16) {
+#pragma unroll
+                for (int n = 0; n < 4; n += 2) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        put8(q, quad(acc[n][i], q));
+                        put8(4 + q, quad(acc[n + 1][i], q));
+                    }
+                    flush(m0, v.n0 + tile_row<false>(wn, n), p.N);
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    v4f h[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) h[q] = swiglu(quad(acc[n][i], q), quad(acc[n + 2][i], q));
+                    if constexpr (EPI == MOE_MX_SWIGLU_BF16) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) put8(4 * n + q, h[q]);
                     } else {
-        #pragma unroll
-                        for (int n = 0; n < 4; ++n)
-        #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (live)
-                                    store4<EPI == MOE_MX_STORE_F32>(p.out, m, v.n0 + tile_row<false>(wn, n) + 8 * q + 4 * kb,
-                                                                    p.N, quad(acc[n][i], q));
+                        const int m = m0 + lr, col = v.n0 / 2 + wn * 64 + n * 32;
+                        store_mx_row(p.out_q, p.out_s, (int64_t)m * (p.N / 64) + col / 32, kb, m < v.hi, h);
                     }
                 }
+                if constexpr (EPI == MOE_MX_SWIGLU_BF16) flush(m0, v.n0 / 2 + wn * 64, p.N / 2);
+            }
+        }
     };
-    // Every DMA and scale sent for has arrived, and every wave has read what it asked of LDS.
-    auto landed = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
-    // Stage s from LDS stage ST.  The operands of a step are read while the one
-    // before is multiplied.  Before the last step every wave has read all of the
-    // stage, and stage s + 1 has landed; stage s + 2 is then sent for into the
-    // place of stage s.  Past the last stage the same instructions read zeros and
-    // stale operands that nothing uses, so that the loop has no branches.
-    auto stage = [&](auto stc, auto other, int s) {
+    // Waits until all but the last N of this wave's vector memory operations are
+    // done and every wave has come here with its LDS reads and writes done.
+    auto landed = [](auto nc) {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(nc)::value) : "memory");
+    };
+    // Stage ST of chunk c, stage s = 4 c + ST of K.  Step 0 sends for B of stage
+    // s + 3 and step 1 for A of stage s + 4, into the places of stages s - 1 and s,
+    // which every wave had read before the last barrier.  Step 1 begins when stage
+    // s + 1 has landed (stages s + 2 and s + 3, and the scales on their way, may be
+    // out) and reads its first operands; the next chunk's scales are loaded in step
+    // 1 of the chunk's first stage and written in step 1 of its third; each half of
+    // them is read when the last stage that used its registers is under way.  Past
+    // the end of K the same instructions move zeros, so that the loop has no
+    // branches.
+    auto stage = [&](auto stc, auto nextc, auto sentc, int c) {
+        constexpr int ST = decltype(stc)::value;
         FENCE();
-        read(stc, c1, c1);
-        multiply(stc, c0, c0);
+        read(stc, c1);
+        send_b(sentc, c * 4 + ST + 3);
+        if constexpr (ST == 0) read_scales(c1, c);
+        multiply(stc, c0);
+        interleave<4 * MT, MT + 4 + (ST == 0 ? (MT + 4) / 2 : 0), B_DMA>();
         FENCE();
-        read(stc, c2, c0);
-        multiply(stc, c1, c1);
+        landed(IC<2 * ND + (ST == 1 || ST == 2 ? NSC : 0)>{});
         FENCE();
-        read(stc, c3, c1);
-        multiply(stc, c2, c0);
-        FENCE();
-        landed();
-        read(other, c0, c0);
-        send(stc, s + 2);
-        multiply(stc, c3, c1);
-        scales(stc, s + 2);
+        read(nextc, c0);
+        send_a(stc, c * 4 + ST + 4);
+        if constexpr (ST == 0) load_scales(c + 1);
+        if constexpr (ST == 2) write_scales(c + 1);
+        if constexpr (ST == 3) read_scales(c0, c + 1);
+        multiply(stc, c1);
+        interleave<4 * MT, MT + 4 + (ST == 3 ? (MT + 4) / 2 : 0), A_DMA + (ST == 0 ? NSC : 0)>();
         FENCE();
     };
     for (bool before = false;; before = true) {
         const bool more = t < t_end;
-        if (more) {                                      // the first two stages travel during the last tile's stores
+        if (more) {                                      // the first three stages travel during the last tile's stores
             T = locate(t);
             setup(T);
-            send(c0, 0);
-            scales(c0, 0);
-            send(c1, 1);
-            scales(c1, 1);
+            load_scales(0);
+            FENCE();
+            send_a(c0, 0);
+            send_b(c0, 0);
+            FENCE();
+            send_a(c1, 1);
+            send_b(c1, 1);
+            FENCE();
+            send_a(c2, 2);
+            send_b(c2, 2);
+            FENCE();
         }
         if (before) store(U);
         if (!more) break;
+        send_a(c3, 3);
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[n][i][e] = 0.0f;
-        landed();
-        read(c0, c0, c0);
-        for (int s = 0; s < ns; s += 2) {
-            stage(c0, c1, s);
-            stage(c1, c0, s + 1);
+        write_scales(0);
+        landed(IC<2 * ND + A_DMA>{});
+        read(c0, c0);
+        read_scales(c0, 0);
+        for (int c = 0; c < nchunk; ++c) {
+            stage(c0, c1, c3, c);
+            stage(c1, c2, c0, c);
+            stage(c2, c3, c1, c);
+            stage(c3, c0, c2, c);
         }
-        landed();                                        // the zeros of the stages past the last
+        landed(IC<0>{});                                 // the zeros past the end of K
         U = T;
         t += t_step;
     }
 }
+
 template <int EPI, int BM>
 hipError_t launch_tiles(const MxGemmArgs& a, hipStream_t st) {
     int dev = 0, cus = 0;
