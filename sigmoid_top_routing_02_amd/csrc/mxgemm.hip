@@ -403,6 +403,19 @@ __device__ __forceinline__ int swz(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 
 #define SCHED(KIND, N) __builtin_amdgcn_sched_group_barrier(KIND, N, 0)
 constexpr int MFMA = 0x8, VMEM = 0x20, DS_READ = 0x100;
 
+// Elements 4 q .. 4 q + 3 of an accumulator, read where this stands.  (Left to the
+// compiler, all 256 copies are made at the end of the loop over K, and spill.)
+__device__ __forceinline__ v4f quad(const v16f& x, int q) {
+    v4f v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float f;
+        asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(f) : "a"(x[4 * q + e]));
+        v[e] = f;
+    }
+    return v;
+}
+
 template <int READS, int LOADS, int... I>
 __device__ __forceinline__ void interleave_slots(std::integer_sequence<int, I...>) {
     constexpr int S = sizeof...(I);
@@ -473,7 +486,7 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
     constexpr int A_DMA = BM / 64, B_DMA = TN / 64;      // 1 KiB (16 rows) DMAs of a wave per stage
     constexpr int ND = A_DMA + B_DMA, NSC = KA ? 2 : 4;  // vector loads of a stage, and of a chunk's scales
     constexpr int CHUNK_M = 2048 / BM;                   // row tiles that go through the columns together
-    __shared__ int start[1025];                          // first row tile of each group
+    __shared__ int start[1025], rows[1025];              // first row tile and first row of each group
     __shared__ int found;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
@@ -490,8 +503,10 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
             const int g = tid * 4 + i;
             n[i] = 0;
             if (g < p.G) {
-                const int lo = min(max(p.group_offset[g], 0), total), hi = min(p.group_offset[g + 1], total);
+                const int lo = min(max(p.group_offset[g], 0), total), hi = min(max(p.group_offset[g + 1], 0), total);
                 n[i] = hi > lo ? (hi - lo + BM - 1) / BM : 0;
+                rows[g] = lo;
+                if (g == p.G - 1) rows[p.G] = hi;
             }
             sum += n[i];
         }
@@ -527,22 +542,24 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
     const auto aq = make_rsrc(p.a_q, (uint32_t)(p.a_rows * rb));
     const auto as = make_rsrc(p.a_s, ((uint32_t)(p.a_rows * nblk) + 3u) & ~3u);
     auto bq = aq, bs = as;
-    struct Tile { int g, m0, hi, n0; } T, U;
+    struct Tile { int g, m0, hi, n0; } T{}, U{}, V{};   // the tile at work, the one before, the next
     uint32_t aro[A_DMA], bro[B_DMA], aso, bso;
     uint32_t sa[2][MT], sb[2][4];
     Scales<KA> ca, cb;
     v16f acc[4][MT];
     v4u fa[2][MT], fb[2][4];
 
+    // A barrier for LDS alone, which leaves stores and loads under way.
+    auto lds_barrier = [] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
     auto locate = [&](int at) {                          // every thread of the block
-        __syncthreads();
+        lds_barrier();
         const int rt = at / n_tiles;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int g = tid * 4 + i;
             if (start[g] <= rt && rt < start[g + 1]) found = g;
         }
-        __syncthreads();
+        lds_barrier();
         Tile v;
         v.g = __builtin_amdgcn_readfirstlane(found);
         const int first = __builtin_amdgcn_readfirstlane(start[v.g]);
@@ -550,31 +567,35 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
         const int inside = at - first * n_tiles;
         const int chunk = inside / (CHUNK_M * n_tiles), left = inside - chunk * CHUNK_M * n_tiles;
         const int cm = min(CHUNK_M, n - chunk * CHUNK_M);
-        const int lo = min(max(__builtin_amdgcn_readfirstlane(p.group_offset[v.g]), 0), total);
-        v.hi = min(__builtin_amdgcn_readfirstlane(p.group_offset[v.g + 1]), total);
-        v.m0 = lo + (chunk * CHUNK_M + left % cm) * BM;
+        v.hi = __builtin_amdgcn_readfirstlane(rows[v.g + 1]);
+        v.m0 = __builtin_amdgcn_readfirstlane(rows[v.g]) + (chunk * CHUNK_M + left % cm) * BM;
         v.n0 = left / cm * TN;
         return v;
     };
     // A 1 KiB DMA fills 16 rows: lane l brings slot l % 4 of row l / 4.
     const int chunk_of = (lane & 3) ^ swz(lane >> 2);
+    // Entry i (of A_DMA + 1) of the rows of A that this thread's DMAs and scales need
+    // of a tile; find_rows loads them and nothing uses them before the next setup.
+    uint32_t am[A_DMA + 1];
+    auto row_of = [&](int i) { return i < A_DMA ? (wave * A_DMA + i) * 16 + (lane >> 2) : tid; };
+    auto find_rows = [&](const Tile& v) {
+#pragma unroll
+        for (int i = 0; i <= A_DMA; ++i) {
+            const int m = min(v.m0 + row_of(i), v.hi - 1);
+            am[i] = p.a_row_index ? (uint32_t)p.a_row_index[m] : (uint32_t)m;
+        }
+    };
     auto setup = [&](const Tile& v) {
         bq = make_rsrc(p.b_q + (int64_t)v.g * p.N * rb, (uint32_t)p.N * rb);
         const int64_t sg = (int64_t)v.g * p.N * nblk;
         const uint32_t off = KA ? 0u : (uint32_t)sg & 3u;
         bs = make_rsrc(p.b_s + (sg - off), ((uint32_t)p.N * (uint32_t)nblk + off + 3u) & ~3u);
-        // the row of A behind row m of the product; OUT where there is none
-        auto a_row = [&](int m) {
-            const uint32_t r = m < v.hi ? (p.a_row_index ? (uint32_t)p.a_row_index[m] : (uint32_t)m) : 0xFFFFFFFFu;
-            return r < (uint32_t)p.a_rows ? r : OUT;
+        auto has = [&](int i) {                          // a row of the tile, and of A
+            return row_of(i) < BM && v.m0 + row_of(i) < v.hi && am[i] < (uint32_t)p.a_rows;
         };
 #pragma unroll
-        for (int i = 0; i < A_DMA; ++i) {
-            const uint32_t r = a_row(v.m0 + (wave * A_DMA + i) * 16 + (lane >> 2));
-            aro[i] = r == OUT ? OUT : r * rb + (uint32_t)chunk_of * 16u;
-        }
-        const uint32_t r = tid < BM ? a_row(v.m0 + tid) : OUT;
-        aso = r == OUT ? OUT : r * (uint32_t)nblk;
+        for (int i = 0; i < A_DMA; ++i) aro[i] = has(i) ? am[i] * rb + (uint32_t)chunk_of * 16u : OUT;
+        aso = has(A_DMA) ? am[A_DMA] * (uint32_t)nblk : OUT;
         // rows past N lie past the end of B's descriptors
 #pragma unroll
         for (int i = 0; i < B_DMA; ++i)
@@ -646,44 +667,47 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
     constexpr IC<3> c3{};
     // Lane l has columns 8 q + 4 (l / 32) + e of row l % 32 of each 32 x 32 tile in
     // element 4 q + e.  FP32 and bf16 leave through LDS, 32 rows of 128 bytes at a
-    // time (the wave's own 4 KiB of the last stage's B rows, which the next tile's
-    // first three stages leave alone), so that eight lanes store one whole line;
-    // chunk c of a row lies in slot c ^ row % 8.
+    // time (two places in turn, the wave's own in the last stage, which the next
+    // tile's first three stages leave alone), so that eight lanes store one whole
+    // line; chunk c of a row lies in slot c ^ row % 8.
     auto store = [&](const Tile& v) {
-        auto quad = [](const v16f& x, int q) { return v4f{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]}; };
-        char* mine = g_s3 + B_AT + wave * 4096;
-        auto put16 = [&](int chunk, v4f x) { *reinterpret_cast<v4f*>(mine + lr * 128 + ((chunk ^ (lr & 7)) << 4)) = x; };
-        auto put8 = [&](int chunk, v4f x) {
-            *reinterpret_cast<uint2*>(mine + lr * 128 + ((chunk ^ (lr & 7)) << 4) + kb * 8) = pack4(x);
+        // the reads of quad() are hidden from the compiler, which counts the wait
+        // from the last matrix instruction to a read of its result (at most 19)
+        asm volatile("s_nop 15\n\ts_nop 15");
+        char* mine = g_s3 + wave * 8192;
+        auto put16 = [&](int place, int chunk, v4f x) { *reinterpret_cast<v4f*>(mine + place * 4096 + lr * 128 + ((chunk ^ (lr & 7)) << 4)) = x; };
+        auto put8 = [&](int place, int chunk, v4f x) {
+            *reinterpret_cast<uint2*>(mine + place * 4096 + lr * 128 + ((chunk ^ (lr & 7)) << 4) + kb * 8) = pack4(x);
         };
-        auto flush = [&](int m0, int col, int ld) {      // 32 rows from m0, 128 bytes from column col
+        auto flush = [&](int place, int m0, int col, int ld) {      // 32 rows from m0, 128 bytes from column col
             constexpr bool F32 = EPI == MOE_MX_STORE_F32;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = i * 8 + (lane >> 3);
-                const v4u x = *reinterpret_cast<const v4u*>(mine + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                const v4u x = *reinterpret_cast<const v4u*>(mine + place * 4096 + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
                 if (m0 + r < v.hi) store16<F32>(p.out, m0 + r, col + (lane & 7) * (F32 ? 4 : 8), ld, x);
             }
         };
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             const int m0 = v.m0 + wm * (BM / 2) + i * 32;
+            FENCE();                                     // one row of tiles at a time out of the accumulators
             if constexpr (EPI == MOE_MX_STORE_F32) {
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) put16(2 * q + kb, quad(acc[n][i], q));
-                    flush(m0, v.n0 + tile_row<false>(wn, n), p.N);
+                    for (int q = 0; q < 4; ++q) put16(n & 1, 2 * q + kb, quad(acc[n][i], q));
+                    flush(n & 1, m0, v.n0 + tile_row<false>(wn, n), p.N);
                 }
             } else if constexpr (EPI == MOE_MX_STORE_BF16) {
 #pragma unroll
                 for (int n = 0; n < 4; n += 2) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        put8(q, quad(acc[n][i], q));
-                        put8(4 + q, quad(acc[n + 1][i], q));
+                        put8(n / 2, q, quad(acc[n][i], q));
+                        put8(n / 2, 4 + q, quad(acc[n + 1][i], q));
                     }
-                    flush(m0, v.n0 + tile_row<false>(wn, n), p.N);
+                    flush(n / 2, m0, v.n0 + tile_row<false>(wn, n), p.N);
                 }
             } else {
 #pragma unroll
@@ -693,13 +717,13 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
                     for (int q = 0; q < 4; ++q) h[q] = swiglu(quad(acc[n][i], q), quad(acc[n + 2][i], q));
                     if constexpr (EPI == MOE_MX_SWIGLU_BF16) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) put8(4 * n + q, h[q]);
+                        for (int q = 0; q < 4; ++q) put8(i & 1, 4 * n + q, h[q]);
                     } else {
                         const int m = m0 + lr, col = v.n0 / 2 + wn * 64 + n * 32;
                         store_mx_row(p.out_q, p.out_s, (int64_t)m * (p.N / 64) + col / 32, kb, m < v.hi, h);
                     }
                 }
-                if constexpr (EPI == MOE_MX_SWIGLU_BF16) flush(m0, v.n0 / 2 + wn * 64, p.N / 2);
+                if constexpr (EPI == MOE_MX_SWIGLU_BF16) flush(i & 1, m0, v.n0 / 2 + wn * 64, p.N / 2);
             }
         }
     };
@@ -737,10 +761,15 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
         interleave<4 * MT, MT + 4 + (ST == 3 ? (MT + 4) / 2 : 0), A_DMA + (ST == 0 ? NSC : 0)>();
         FENCE();
     };
+    // Each tile's place and rows of A are looked up before the tile ahead of it starts.
+    if (t < t_end) {
+        T = locate(t);
+        find_rows(T);
+    }
     for (bool before = false;; before = true) {
         const bool more = t < t_end;
+        t += t_step;
         if (more) {                                      // the first three stages travel during the last tile's stores
-            T = locate(t);
             setup(T);
             load_scales(0);
             FENCE();
@@ -753,10 +782,15 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
             send_a(c2, 2);
             send_b(c2, 2);
             FENCE();
+            if (t < t_end) {
+                V = locate(t);
+                find_rows(V);
+            }
         }
         if (before) store(U);
         if (!more) break;
-        send_a(c3, 3);
+        U = T;
+        T = V;
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -764,18 +798,20 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[n][i][e] = 0.0f;
         write_scales(0);
-        landed(IC<2 * ND + A_DMA>{});
+        FENCE();
+        landed(IC<2 * ND>{});
+        FENCE();
+        send_a(c3, 3);
         read(c0, c0);
         read_scales(c0, 0);
-        for (int c = 0; c < nchunk; ++c) {
+        int c = 0;
+        do {                                             // K > 0: at least once
             stage(c0, c1, c3, c);
             stage(c1, c2, c0, c);
             stage(c2, c3, c1, c);
             stage(c3, c0, c2, c);
-        }
+        } while (++c < nchunk);
         landed(IC<0>{});                                 // the zeros past the end of K
-        U = T;
-        t += t_step;
     }
 }
 
