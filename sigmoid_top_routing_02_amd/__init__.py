@@ -115,6 +115,13 @@ def _check(status: int, name: str):
                        f"{L.moe_last_error().decode()}")
 
 
+try:                                # the current stream's handle without a Stream object around it
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:                 # a torch built without GPU support: every call refuses its tensors first
+    def _raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
+
+
 def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
@@ -572,60 +579,93 @@ def moe_wgrad(dh, topk_gate, slot_row, row_token, z, dh_row, u, group_offset, sh
 
 
 # ---------------------------------------------------------------- residual + RMS norm
+# The calls from here on are also made for single tokens, where the host's time
+# is most of theirs: their checks pass over each tensor once (_in) and raise
+# through _refuse, which finds out what was wrong.
 RMSNorm = namedtuple("RMSNorm", "y h rstd q scale")
 
 
-def _dt(t, name):
-    if t.dtype not in _DTYPES:
-        raise MoEError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
-    return _DTYPES[t.dtype]
+def _refuse(t, dtype, shape, name, dev):
+    _want(t, dtype, shape, name)
+    if not t.is_cuda:
+        raise MoEError(f"{name}: tensor must live on the GPU")
+    if t.get_device() != dev or dev != torch.cuda.current_device():
+        raise MoEError(f"{name}: tensor on {t.device}, expected the current GPU, cuda:{torch.cuda.current_device()}, "
+                       "for every tensor of a call")
+    raise MoEError(f"{name}: tensor must be contiguous")
 
 
-def _matrix(t, name):
+def _in(t, dtype, shape, name, dev):
+    """The address of a tensor of this type and shape, contiguous and on GPU dev."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dtype, shape, name, dev)
+    return t.data_ptr()
+
+
+def _rows(t, name):
+    """(rows, cols, MOE dtype, GPU) of a bf16 or FP32 matrix on the current GPU."""
     if t.dim() != 2:
         raise MoEError(f"{name}: shape {tuple(t.shape)}, expected two dimensions")
-    return tuple(t.shape)
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise MoEError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
+    rows, cols = t.shape
+    return rows, cols, dt, _current(t, name)
 
 
-def _on(t, *others):
-    """The tensors lie on the device whose current stream the call is put on."""
-    here = torch.device("cuda", torch.cuda.current_device()) if t.is_cuda else None
-    for o in (t, *others):
-        if o is not None and (not o.is_cuda or o.device != here):
-            raise MoEError(f"tensor on {o.device}, expected the current GPU ({here})")
+def _current(t, name):
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        _refuse(t, t.dtype, t.shape, name, dev)
+    return dev
+
+
+def _dt(t, name):
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise MoEError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
+    return dt
 
 
 def moe_add_rmsnorm(x, weight, eps, residual=None, quant=False, h_out=None, y=None, q=None, scale=None, rstd=None):
     """h = x + residual, y = bf16(h / sqrt(mean(h^2) + eps) * weight) and, with quant, the FP8 1x128
     codes and scales of y.  x, residual bf16/f32 [T,d], weight bf16/f32 [d]
     -> RMSNorm(y bf16 [T,d], h of residual's type [T,d] or None, rstd f32 [T], q uint8 [T,d] or None,
-    scale f32 [T,d/128] or None).  h_out may be residual, or x of the same type."""
-    T, d = _matrix(x, "x")
-    xd, wd = _dt(x, "x"), _dt(weight, "weight")
-    _want(weight, weight.dtype, (d,), "weight")
+    scale f32 [T,d/128] or None).  h_out may be residual, or x of the same type; y may be x or residual
+    where that is bf16."""
+    T, d, xd, dev = _rows(x, "x")
+    shape = x.shape
+    px = _in(x, x.dtype, shape, "x", dev)
+    wd = _dt(weight, "weight")
+    pw = _in(weight, weight.dtype, (d,), "weight", dev)
+    pr = ph = pq = ps = None
     rd = MOE_F32
     if residual is not None:
         rd = _dt(residual, "residual")
-        _want(residual, residual.dtype, (T, d), "residual")
-        h_out = _new((T, d), residual.dtype, x) if h_out is None else h_out
-        _want(h_out, residual.dtype, (T, d), "h_out")
+        pr = _in(residual, residual.dtype, shape, "residual", dev)
+        if h_out is None:
+            h_out = torch.empty_like(residual)
+        ph = _in(h_out, residual.dtype, shape, "h_out", dev)
     elif h_out is not None:
         raise MoEError("moe_add_rmsnorm: h_out without a residual")
-    y = _new((T, d), torch.bfloat16, x) if y is None else y
-    rstd = _new((T,), torch.float32, x) if rstd is None else rstd
-    _want(y, torch.bfloat16, (T, d), "y")
-    _want(rstd, torch.float32, (T,), "rstd")
+    if y is None:
+        y = x.new_empty(shape, dtype=torch.bfloat16)
+    if rstd is None:
+        rstd = x.new_empty((T,), dtype=torch.float32)
     if quant:
-        q = _new((T, d), torch.uint8, x) if q is None else q
-        scale = _new((T, d // 128), torch.float32, x) if scale is None else scale
-        _want(q, torch.uint8, (T, d), "q")
-        _want(scale, torch.float32, (T, d // 128), "scale")
+        if q is None:
+            q = x.new_empty(shape, dtype=torch.uint8)
+        if scale is None:
+            scale = x.new_empty((T, d // 128), dtype=torch.float32)
+        pq = _in(q, torch.uint8, shape, "q", dev)
+        ps = _in(scale, torch.float32, (T, d // 128), "scale", dev)
     elif q is not None or scale is not None:
         raise MoEError("moe_add_rmsnorm: q or scale without quant")
-    _on(x, weight, residual, h_out, y, q, scale, rstd)
-    L = load_library()
-    _check(L.moe_add_rmsnorm(_ptr(x), xd, _ptr(residual), rd, _ptr(weight), wd, T, d, eps, _ptr(h_out), _ptr(y),
-                             _ptr(q), _ptr(scale), _ptr(rstd), _stream()), "moe_add_rmsnorm")
+    L = _lib or load_library()
+    st = L.moe_add_rmsnorm(px, xd, pr, rd, pw, wd, T, d, eps, ph, _in(y, torch.bfloat16, shape, "y", dev), pq, ps,
+                           _in(rstd, torch.float32, (T,), "rstd", dev), _raw_stream(dev))
+    if st:
+        _check(st, "moe_add_rmsnorm")
     return RMSNorm(y, h_out, rstd, q, scale)
 
 
@@ -633,26 +673,26 @@ def moe_add_rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, dw=None, dx_
     """dy, h bf16/f32 [T,d], weight bf16/f32 [d], rstd f32 [T], dh (the gradient of h_out) or None
     -> (dx [T,d] of dh's type, else dx_dtype, else dy's; dw f32 [d]).  dx is the gradient of x and of
     residual alike."""
-    T, d = _matrix(dy, "dy")
-    yd, hd, wd = _dt(dy, "dy"), _dt(h, "h"), _dt(weight, "weight")
-    _want(h, h.dtype, (T, d), "h")
-    _want(weight, weight.dtype, (d,), "weight")
-    _want(rstd, torch.float32, (T,), "rstd")
+    T, d, yd, dev = _rows(dy, "dy")
+    shape = dy.shape
     if dx_dtype is None:
         dx_dtype = dh.dtype if dh is not None else dx.dtype if dx is not None else dy.dtype
-    dx = _new((T, d), dx_dtype, dy) if dx is None else dx
-    dw = _new((d,), torch.float32, dy) if dw is None else dw
-    _want(dx, dx_dtype, (T, d), "dx")
-    _want(dw, torch.float32, (d,), "dw")
-    if dh is not None:
-        _want(dh, dx_dtype, (T, d), "dh")
-    L = load_library()
+    if dx is None:
+        dx = dy.new_empty(shape, dtype=dx_dtype)
+    if dw is None:
+        dw = dy.new_empty((d,), dtype=torch.float32)
+    L = _lib or load_library()
     if ws is None:
-        ws = _new((max(L.moe_add_rmsnorm_backward_workspace_bytes(T, d), 256),), torch.uint8, dy)
-    _on(dy, h, weight, rstd, dh, dx, dw, ws)
-    _check(L.moe_add_rmsnorm_backward(_ptr(dy), yd, _ptr(h), hd, _ptr(weight), wd, _ptr(rstd), _ptr(dh), T, d,
-                                      _ptr(dx), _dt(dx, "dx"), _ptr(dw), _ptr(ws), ws.numel() * ws.element_size(),
-                                      _stream()), "moe_add_rmsnorm_backward")
+        ws = dy.new_empty((max(L.moe_add_rmsnorm_backward_workspace_bytes(T, d), 16),), dtype=torch.uint8)
+    pdh = None if dh is None else _in(dh, dx_dtype, shape, "dh", dev)
+    st = L.moe_add_rmsnorm_backward(
+        _in(dy, dy.dtype, shape, "dy", dev), yd, _in(h, h.dtype, shape, "h", dev), _dt(h, "h"),
+        _in(weight, weight.dtype, (d,), "weight", dev), _dt(weight, "weight"),
+        _in(rstd, torch.float32, (T,), "rstd", dev), pdh, T, d, _in(dx, dx_dtype, shape, "dx", dev), _dt(dx, "dx"),
+        _in(dw, torch.float32, (d,), "dw", dev), _in(ws, ws.dtype, ws.shape, "ws", dev),
+        ws.numel() * ws.element_size(), _raw_stream(dev))
+    if st:
+        _check(st, "moe_add_rmsnorm_backward")
     return dx, dw
 
 
@@ -660,45 +700,48 @@ def moe_add_rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, dw=None, dx_
 def mxfp4_quant_1x32(x, q=None, scale=None):
     """x bf16/f32 [rows, cols] -> (q uint8 [rows, cols/2], two E2M1 codes to a byte, the even column in
     the low half; scale uint8 [rows, cols/32], E8M0)."""
-    rows, cols = _matrix(x, "x")
-    dt = _dt(x, "x")
-    q = _new((rows, cols // 2), torch.uint8, x) if q is None else q
-    scale = _new((rows, cols // 32), torch.uint8, x) if scale is None else scale
-    _want(q, torch.uint8, (rows, cols // 2), "q")
-    _want(scale, torch.uint8, (rows, cols // 32), "scale")
-    _on(x, q, scale)
-    L = load_library()
-    _check(L.mxfp4_quant_1x32(_ptr(x), dt, rows, cols, _ptr(q), _ptr(scale), _stream()), "mxfp4_quant_1x32")
+    rows, cols, dt, dev = _rows(x, "x")
+    if q is None:
+        q = x.new_empty((rows, cols // 2), dtype=torch.uint8)
+    if scale is None:
+        scale = x.new_empty((rows, cols // 32), dtype=torch.uint8)
+    L = _lib or load_library()
+    st = L.mxfp4_quant_1x32(_in(x, x.dtype, x.shape, "x", dev), dt, rows, cols,
+                            _in(q, torch.uint8, (rows, cols // 2), "q", dev),
+                            _in(scale, torch.uint8, (rows, cols // 32), "scale", dev), _raw_stream(dev))
+    if st:
+        _check(st, "mxfp4_quant_1x32")
     return q, scale
+
+
+def _dequant(name, q, scale, cols, scale_dtype, per, dtype, out):
+    """The shared part of the dequantisers: values [rows, cols], `per` of them under each scale."""
+    rows = q.shape[0]
+    dev = _current(q, "q")
+    if dtype not in _DTYPES:
+        raise MoEError(f"{name}: dtype {dtype}, expected torch.bfloat16 or torch.float32")
+    if out is None:
+        out = q.new_empty((rows, cols), dtype=dtype)
+    L = _lib or load_library()
+    st = getattr(L, name)(_in(q, torch.uint8, q.shape, "q", dev), _in(scale, scale_dtype, (rows, cols // per), "scale", dev),
+                          rows, cols, _in(out, dtype, (rows, cols), "out", dev), _DTYPES[dtype], _raw_stream(dev))
+    if st:
+        _check(st, name)
+    return out
 
 
 def mxfp4_dequant_1x32(q, scale, dtype=torch.bfloat16, out=None):
     """The values of mxfp4_quant_1x32's outputs, bf16 or f32 [rows, cols]."""
-    rows, half = _matrix(q, "q")
-    cols = half * 2
-    _want(q, torch.uint8, (rows, half), "q")
-    _want(scale, torch.uint8, (rows, cols // 32), "scale")
-    out = _new((rows, cols), dtype, q) if out is None else out
-    _want(out, dtype, (rows, cols), "out")
-    _on(q, scale, out)
-    L = load_library()
-    _check(L.mxfp4_dequant_1x32(_ptr(q), _ptr(scale), rows, cols, _ptr(out), _dt(out, "out"), _stream()),
-           "mxfp4_dequant_1x32")
-    return out
+    if q.dim() != 2:
+        raise MoEError(f"q: shape {tuple(q.shape)}, expected two dimensions")
+    return _dequant("mxfp4_dequant_1x32", q, scale, 2 * q.shape[1], torch.uint8, 32, dtype, out)
 
 
 def fp8_dequant_1x128(q, scale, dtype=torch.float32, out=None):
     """The values of fp8_quant_1x128's outputs, bf16 or f32 [rows, cols]."""
-    rows, cols = _matrix(q, "q")
-    _want(q, torch.uint8, (rows, cols), "q")
-    _want(scale, torch.float32, (rows, cols // 128), "scale")
-    out = _new((rows, cols), dtype, q) if out is None else out
-    _want(out, dtype, (rows, cols), "out")
-    _on(q, scale, out)
-    L = load_library()
-    _check(L.fp8_dequant_1x128(_ptr(q), _ptr(scale), rows, cols, _ptr(out), _dt(out, "out"), _stream()),
-           "fp8_dequant_1x128")
-    return out
+    if q.dim() != 2:
+        raise MoEError(f"q: shape {tuple(q.shape)}, expected two dimensions")
+    return _dequant("fp8_dequant_1x128", q, scale, q.shape[1], torch.float32, 128, dtype, out)
 
 
 def grouped_gemm_mxfp4(a_q, a_scale, group_offset, M_total, b_q, b_scale, epi=MOE_MX_STORE_F32, a_row_index=None,
@@ -706,34 +749,44 @@ def grouped_gemm_mxfp4(a_q, a_scale, group_offset, M_total, b_q, b_scale, epi=MO
     """a_q uint8 [*,K/2], a_scale uint8 [*,K/32], group_offset i32 [G+1] (device), b_q uint8 [G,N,K/2],
     b_scale uint8 [G,N,K/32] -> out f32 or bf16 [M_total,N], h bf16 [M_total,N/2] (MOE_MX_SWIGLU_BF16), or
     (out_q uint8 [M_total,N/4], out_scale uint8 [M_total,N/64]) (MOE_MX_SWIGLU_QUANT)."""
-    if b_q.dim() != 3:
-        raise MoEError(f"b_q: shape {tuple(b_q.shape)}, expected [G, N, K/2]")
+    if b_q.dim() != 3 or a_q.dim() != 2:
+        raise MoEError(f"a_q: {tuple(a_q.shape)}, b_q: {tuple(b_q.shape)}, expected [*, K/2] and [G, N, K/2]")
     G, N, half = b_q.shape
     K = half * 2
-    _want(b_q, torch.uint8, (G, N, half), "b_q")
-    _want(b_scale, torch.uint8, (G, N, K // 32), "b_scale")
-    if a_q.dim() != 2 or a_q.dtype != torch.uint8 or a_q.shape[1] != half:
-        raise MoEError(f"a_q: {a_q.dtype} {tuple(a_q.shape)}, expected torch.uint8 [*, {half}]")
     rows = a_q.shape[0]
-    _want(a_scale, torch.uint8, (rows, K // 32), "a_scale")
-    if group_offset.dtype != torch.int32 or group_offset.numel() < G + 1:
+    dev = _current(b_q, "b_q")
+    pi = None
+    if a_row_index is not None:
+        if a_row_index.dtype is not torch.int32 or a_row_index.numel() < M_total:
+            raise MoEError(f"a_row_index: {a_row_index.dtype} with {a_row_index.numel()} entries, "
+                           f"expected int32 with at least M_total = {M_total}")
+        pi = _in(a_row_index, torch.int32, a_row_index.shape, "a_row_index", dev)
+    if group_offset.dtype is not torch.int32 or group_offset.numel() < G + 1:
         raise MoEError("group_offset must be int32 with G+1 entries")
-    if a_row_index is not None and (a_row_index.dtype != torch.int32 or a_row_index.numel() < M_total):
-        raise MoEError(f"a_row_index: {a_row_index.dtype} with {a_row_index.numel()} entries, "
-                       f"expected int32 with at least M_total = {M_total}")
+    po = pq = ps = None
     if epi == MOE_MX_SWIGLU_QUANT:
-        out_q = _new((M_total, N // 4), torch.uint8, a_q) if out_q is None else out_q
-        out_scale = _new((M_total, N // 64), torch.uint8, a_q) if out_scale is None else out_scale
-        _want(out_q, torch.uint8, (M_total, N // 4), "out_q")
-        _want(out_scale, torch.uint8, (M_total, N // 64), "out_scale")
+        if out_q is None:
+            out_q = a_q.new_empty((M_total, N // 4))
+        if out_scale is None:
+            out_scale = a_q.new_empty((M_total, N // 64))
+        pq = _in(out_q, torch.uint8, (M_total, N // 4), "out_q", dev)
+        ps = _in(out_scale, torch.uint8, (M_total, N // 64), "out_scale", dev)
+        if out is not None:
+            raise MoEError("grouped_gemm_mxfp4: this epilogue writes out_q and out_scale, not out")
     else:
         want = torch.float32 if epi == MOE_MX_STORE_F32 else torch.bfloat16
-        cols = N // 2 if epi == MOE_MX_SWIGLU_BF16 else N
-        out = _new((M_total, cols), want, a_q) if out is None else out
-        _want(out, want, (M_total, cols), "out")
-    _on(a_q, a_scale, a_row_index, group_offset, b_q, b_scale, out, out_q, out_scale)
-    L = load_library()
-    _check(L.grouped_gemm_mxfp4(_ptr(a_q), _ptr(a_scale), rows, _ptr(a_row_index), _ptr(group_offset), G, M_total,
-                                _ptr(b_q), _ptr(b_scale), N, K, epi, _ptr(out), _ptr(out_q), _ptr(out_scale),
-                                _stream()), "grouped_gemm_mxfp4")
+        shape = (M_total, N // 2 if epi == MOE_MX_SWIGLU_BF16 else N)
+        if out is None:
+            out = a_q.new_empty(shape, dtype=want)
+        po = _in(out, want, shape, "out", dev)
+        if out_q is not None or out_scale is not None:
+            raise MoEError("grouped_gemm_mxfp4: this epilogue writes out, not out_q or out_scale")
+    L = _lib or load_library()
+    st = L.grouped_gemm_mxfp4(
+        _in(a_q, torch.uint8, (rows, half), "a_q", dev), _in(a_scale, torch.uint8, (rows, K // 32), "a_scale", dev),
+        rows, pi, _in(group_offset, torch.int32, group_offset.shape, "group_offset", dev), G, M_total,
+        _in(b_q, torch.uint8, b_q.shape, "b_q", dev), _in(b_scale, torch.uint8, (G, N, K // 32), "b_scale", dev), N, K,
+        epi, po, pq, ps, _raw_stream(dev))
+    if st:
+        _check(st, "grouped_gemm_mxfp4")
     return (out_q, out_scale) if epi == MOE_MX_SWIGLU_QUANT else out

@@ -16,6 +16,7 @@
 //
 // The weights are the instruction's first operand: a lane then holds four
 // neighbouring columns of one output row.
+#include <atomic>
 #include <utility>
 
 #include "device_math.h"
@@ -815,11 +816,24 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
     }
 }
 
+// CUs of the current device, asked for once per device (any thread may call; a
+// lost race asks again).
+hipError_t cu_count(int& cus) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    cus = dev >= 0 && dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (cus > 0) return hipSuccess;
+    e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e == hipSuccess && dev >= 0 && dev < 64) known[dev].store(cus, std::memory_order_relaxed);
+    return e;
+}
+
 template <int EPI, int BM>
 hipError_t launch_tiles(const MxGemmArgs& a, hipStream_t st) {
-    int dev = 0, cus = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+    int cus = 0;
+    const hipError_t e = cu_count(cus);
     if (e != hipSuccess) return e;
     const int64_t most = ((a.M_total + BM - 1) / BM + a.G) * ((a.N + TN - 1) / TN);
     const int64_t want = most < cus ? most : cus;
