@@ -5,14 +5,10 @@
 // instruction (16x16x128 on FP4 operands) takes four blocks with their scales
 // and accumulates in FP32, so the whole of K is one chain of them.
 //
-// Which K a lane holds.  The instruction's lane l supplies row l % 16 and the
-// 32 values number l / 16 of the slice, 16 bytes, and one scale byte chosen
-// from a register at compile time.  A sum does not depend on the order of its
-// terms, so the four slices of a 512-value chunk (16 blocks) are dealt out so
-// that lane l's four operands are blocks 4 (l / 16) .. + 3: consecutive in the
-// row, 64 bytes of codes, and their four scale bytes one aligned word.  Both
-// operands are dealt the same way, and rows are read as the quantiser wrote
-// them, with no second layout of codes or scales.
+// A lane of the instruction supplies one row, 32 consecutive values of it (16
+// bytes) and one scale byte, chosen from a register at compile time.  Rows of codes
+// and scales are read as the quantiser wrote them: there is no second layout of
+// either.
 //
 // The weights are the instruction's first operand: a lane then holds four
 // neighbouring columns of one output row.
@@ -42,44 +38,47 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, ui
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
 }
 
-// c += A B over slice J of a chunk: 16 codes' bytes a lane, scale byte J of sa and sb.
-template <int J>
-__device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c, uint32_t sa, uint32_t sb) {
+// c += A B over 128 values of K: lane l has row l % 16 and block l / 16 of each
+// operand, its scale in the low byte.
+__device__ __forceinline__ v4f mfma16(v4u a, v4u b, v4f c, uint32_t sa, uint32_t sb) {
     const v8i x = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
     const v8i y = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, J, (int)sa, J, (int)sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
-// A lane's share of a chunk of one row.
-struct Chunk {
-    v4u q[4];
-    uint32_t s;
-};
-
-// Loads blocks 16 c + 4 kb .. + 3 of a row; blocks past the row's end, and rows
-// that are none (row offsets OUT), read zero codes under a zero byte, which is
-// a scale and no NaN.  KA: K % 128 == 0, so that the four blocks are in the row
-// together and the scale word is aligned.
+// 16 scale bytes of a row, blocks 16 c .. + 15; those past the row's nblk blocks
+// are zero, whatever lies there.  KA: the row starts on a word.  Otherwise the
+// five words around the bytes are read (the last row's may hold up to three bytes
+// past the tensor's end, in the word of its last byte) and shifted.
 template <bool KA>
-__device__ __forceinline__ void load_chunk(Chunk& f, __amdgpu_buffer_rsrc_t q, __amdgpu_buffer_rsrc_t s,
-                                           uint32_t row_q, uint32_t row_s, int blk, int nblk) {
-    if constexpr (KA) {
-        const bool in = blk < nblk && row_q != OUT;
-        const uint32_t o = in ? row_q + (uint32_t)blk * 16u : OUT;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f.q[j] = __builtin_amdgcn_raw_buffer_load_b128(q, o + 16u * j, 0, 0);
-        f.s = __builtin_amdgcn_raw_buffer_load_b32(s, in ? row_s + (uint32_t)blk : OUT, 0, 0);
-    } else {
-        f.s = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool in = blk + j < nblk && row_q != OUT;
-            f.q[j] = __builtin_amdgcn_raw_buffer_load_b128(q, in ? row_q + (uint32_t)(blk + j) * 16u : OUT, 0, 0);
-            f.s |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(s, in ? row_s + (uint32_t)(blk + j) : OUT, 0, 0)
-                   << (8 * j);
+struct Scales {
+    v4u w;
+    uint32_t more;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t d, uint32_t row, int c) {
+        if constexpr (KA) {
+            w = __builtin_amdgcn_raw_buffer_load_b128(d, row, c * 16, 0);
+        } else {
+            w = __builtin_amdgcn_raw_buffer_load_b128(d, row & ~3u, c * 16, 0);
+            more = __builtin_amdgcn_raw_buffer_load_b32(d, (row & ~3u) + 16u, c * 16, 0);
         }
     }
-}
+    __device__ __forceinline__ v4u bytes(uint32_t row, int c, int nblk) const {
+        v4u v = w;
+        if constexpr (!KA) {
+            const uint32_t sh = (row & 3u) * 8u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = (uint32_t)((((uint64_t)(j < 3 ? w[j + 1] : more) << 32) | w[j]) >> sh);
+        }
+        const int left = nblk - c * 16;                  // of the row's blocks
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = left - 4 * j;
+            v[j] = n >= 4 ? v[j] : n <= 0 ? 0u : KA ? v[j] : v[j] & ((1u << (8 * n)) - 1u);
+        }
+        return v;
+    }
+};
 
 // SiLU with the hardware exp and reciprocal: relative error of a few 2^-23,
 // against the 2^-9 (bf16) or 2^-2 (E2M1) of the rounding that follows.
@@ -220,15 +219,35 @@ __device__ __forceinline__ int b_row(int c0, int tile) {
     }
 }
 
-// Few rows to a group (decode): bound by the bytes of B, each read once.  A
-// block has NT tiles of 16 B rows of one group; its four waves take every fourth
-// chunk of K and add up through LDS, so that a single row of a single group
-// still fills the card.  B and the rows of A go straight to registers, the next
-// chunk's loads under way while this one is multiplied.
-template <int EPI, int MI, int NT, bool KA>
+// ---------------------------------------------------------------- few rows to a group
+//
+// Decoding: bound by the bytes of B, each read once.  A block has NT tiles of 16 B
+// rows of one group; its four waves take every fourth chunk of 512 values of K and
+// add up through LDS, so that a single row of a few groups still fills the card.
+// Operands go straight to registers, one access taking 64 consecutive bytes of each
+// of 16 rows.  Lane l takes block 4 j + l / 16 of a chunk in its slice j, and byte
+// l / 16 of the chunk's scale word j.  BUF = 2 loads the next chunk while one is
+// multiplied, BUF = 1 leaves that to the other waves of the CU.
+template <bool KA>
+struct Chunk {
+    v4u q[4];
+    Scales<KA> s;
+    // row_q, row_s: the row's first byte in codes and scales, or OUT for no row.
+    // Blocks past the row's end read zero codes; bytes() clears their scales.
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t dq, __amdgpu_buffer_rsrc_t ds, uint32_t row_q,
+                                         uint32_t row_s, int c, int kb, int nblk) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            q[j] = __builtin_amdgcn_raw_buffer_load_b128(
+                dq, c * 16 + j * 4 + kb < nblk && row_q != OUT ? row_q + (uint32_t)(j * 4 + kb) * 16u : OUT, c * 256, 0);
+        s.load(ds, c * 16 < nblk ? row_s : OUT, c);
+    }
+};
+
+template <int EPI, int MI, int NT, int BUF, bool KA>
 __global__ __launch_bounds__(256) void mxgemm_rows_kernel(MxGemmArgs p) {
     constexpr bool SWIGLU = EPI == MOE_MX_SWIGLU_BF16 || EPI == MOE_MX_SWIGLU_QUANT;
-    constexpr int COLS = SWIGLU ? NT * 8 : NT * 16;      // output columns of a block
+    constexpr int COLS = SWIGLU ? NT * 8 : NT * 16;      // output columns of the block
     __shared__ v4f red[4][MI * NT][64];
     const int lane = threadIdx.x & 63, lr = lane & 15, kb = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -240,24 +259,30 @@ __global__ __launch_bounds__(256) void mxgemm_rows_kernel(MxGemmArgs p) {
     if (lo >= hi) return;
     const int nblk = p.K / 32, nchunk = (nblk + 15) / 16;
     const uint32_t rb = (uint32_t)p.K / 2;               // bytes of a row of codes
-    const auto aq = make_rsrc(p.a_q, (uint32_t)(p.a_rows * rb)), as = make_rsrc(p.a_s, (uint32_t)(p.a_rows * nblk));
+    // Scale descriptors end on a word.  A group's scales may start off one: the
+    // descriptor then starts at the word before and the offsets begin at the rest.
+    const auto aq = make_rsrc(p.a_q, (uint32_t)(p.a_rows * rb));
+    const auto as = make_rsrc(p.a_s, ((uint32_t)(p.a_rows * nblk) + 3u) & ~3u);
     const auto bq = make_rsrc(p.b_q + (int64_t)g * p.N * rb, (uint32_t)p.N * rb);
-    const auto bs = make_rsrc(p.b_s + (int64_t)g * p.N * nblk, (uint32_t)p.N * (uint32_t)nblk);
-    const int c0 = blockIdx.x * COLS;
+    const int64_t sg = (int64_t)g * p.N * nblk;
+    const uint32_t off = KA ? 0u : (uint32_t)sg & 3u;
+    const auto bs = make_rsrc(p.b_s + (sg - off), ((uint32_t)p.N * (uint32_t)nblk + off + 3u) & ~3u);
+    const int c0 = (int)blockIdx.x * COLS;
     uint32_t bro[NT], bso[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const uint32_t n = (uint32_t)min(b_row<EPI, NT>(c0, t) + lr, p.N - 1);     // columns past N are not stored
         bro[t] = n * rb;
-        bso[t] = n * (uint32_t)nblk;
+        bso[t] = n * (uint32_t)nblk + off;
     }
-    for (int m0 = lo; m0 < hi; m0 += 16 * MI) {
+    for (int64_t row = lo + (int64_t)blockIdx.z * (16 * MI); row < hi; row += (int64_t)gridDim.z * (16 * MI)) {
+        const int m0 = (int)row;
         uint32_t aro[MI], aso[MI];
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             const int m = m0 + i * 16 + lr;
             const uint32_t r = m < hi ? (p.a_row_index ? (uint32_t)p.a_row_index[m] : (uint32_t)m) : 0xFFFFFFFFu;
-            const bool in = (int64_t)r < p.a_rows;       // a row that A does not have counts as zeros
+            const bool in = r < (uint32_t)p.a_rows;      // a row that A does not have counts as zeros
             aro[i] = in ? r * rb : OUT;
             aso[i] = in ? r * (uint32_t)nblk : OUT;
         }
@@ -266,31 +291,40 @@ __global__ __launch_bounds__(256) void mxgemm_rows_kernel(MxGemmArgs p) {
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < MI; ++i) acc[t][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        Chunk fa[2][MI], fb[2][NT];
-        auto load = [&](int buf, int c) {
-            const int blk = c * 16 + kb * 4;             // past the last chunk everything reads zero
+        Chunk<KA> fa[BUF][MI], fb[BUF][NT];
+        auto load = [&](int buf, int c) {                // past the last chunk everything reads zero
 #pragma unroll
-            for (int t = 0; t < NT; ++t) load_chunk<KA>(fb[buf][t], bq, bs, bro[t], bso[t], blk, nblk);
+            for (int t = 0; t < NT; ++t) fb[buf][t].load(bq, bs, bro[t], bso[t], c, kb, nblk);
 #pragma unroll
-            for (int i = 0; i < MI; ++i) load_chunk<KA>(fa[buf][i], aq, as, aro[i], aso[i], blk, nblk);
+            for (int i = 0; i < MI; ++i) fa[buf][i].load(aq, as, aro[i], aso[i], c, kb, nblk);
         };
-        auto multiply = [&](int buf) {
+        auto multiply = [&](int buf, int c) {
+            v4u sa[MI];
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int i = 0; i < MI; ++i) sa[i] = fa[buf][i].s.bytes(aso[i], c, nblk);
 #pragma unroll
-                for (int i = 0; i < MI; ++i) {
-                    acc[t][i] = mfma<0>(fb[buf][t].q[0], fa[buf][i].q[0], acc[t][i], fb[buf][t].s, fa[buf][i].s);
-                    acc[t][i] = mfma<1>(fb[buf][t].q[1], fa[buf][i].q[1], acc[t][i], fb[buf][t].s, fa[buf][i].s);
-                    acc[t][i] = mfma<2>(fb[buf][t].q[2], fa[buf][i].q[2], acc[t][i], fb[buf][t].s, fa[buf][i].s);
-                    acc[t][i] = mfma<3>(fb[buf][t].q[3], fa[buf][i].q[3], acc[t][i], fb[buf][t].s, fa[buf][i].s);
-                }
+            for (int t = 0; t < NT; ++t) {
+                const v4u sb = fb[buf][t].s.bytes(bso[t], c, nblk);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < MI; ++i)
+                        acc[t][i] = mfma16(fb[buf][t].q[j], fa[buf][i].q[j], acc[t][i], sb[j] >> (8 * kb), sa[i][j] >> (8 * kb));
+            }
         };
-        load(0, wave);
-        for (int c = wave; c < nchunk; c += 8) {
-            load(1, c + 4);
-            multiply(0);
-            load(0, c + 8);
-            multiply(1);
+        if constexpr (BUF == 2) {
+            load(0, wave);
+            for (int c = wave; c < nchunk; c += 8) {
+                load(1, c + 4);
+                multiply(0, c);
+                load(0, c + 8);
+                multiply(1, c + 4);
+            }
+        } else {
+            for (int c = wave; c < nchunk; c += 4) {
+                load(0, c);
+                multiply(0, c);
+            }
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -303,21 +337,29 @@ __global__ __launch_bounds__(256) void mxgemm_rows_kernel(MxGemmArgs p) {
             for (int w = 1; w < 4; ++w) s += red[w][t * MI + i][lane];
             return s;
         };
+        // the waves take the units of output in turn
         if constexpr (EPI == MOE_MX_SWIGLU_QUANT) {
-            for (int u = wave; u < NT / 4 * MI; u += 4) {          // 32 columns of 16 rows
+#pragma unroll
+            for (int u = 0; u < NT / 4 * MI; ++u) {              // 32 columns of 16 rows
+                if (u % 4 != wave) continue;
                 const int t = u / MI * 2, i = u % MI, m = m0 + i * 16 + lr;
                 const v4f a = swiglu(sum(t, i), sum(t + NT / 2, i));
                 const v4f b = swiglu(sum(t + 1, i), sum(t + 1 + NT / 2, i));
-                store_mx_block(p.out_q, p.out_s, (int64_t)m * (p.N / 64) + (c0 + t * 16) / 32, kb, m < hi, a, b);
+                store_mx_block(p.out_q, p.out_s, (int64_t)m * (p.N / 64) + (c0 + t * 16) / 32, kb,
+                               m < hi && c0 < p.N / 2, a, b);
             }
         } else if constexpr (SWIGLU) {
-            for (int u = wave; u < NT / 2 * MI; u += 4) {
+#pragma unroll
+            for (int u = 0; u < NT / 2 * MI; ++u) {
+                if (u % 4 != wave) continue;
                 const int t = u / MI, i = u % MI, m = m0 + i * 16 + lr;
                 const v4f h = swiglu(sum(t, i), sum(t + NT / 2, i));
                 if (m < hi) store4<false>(p.out, m, c0 + t * 16 + kb * 4, p.N / 2, h);
             }
         } else {
-            for (int u = wave; u < NT * MI; u += 4) {
+#pragma unroll
+            for (int u = 0; u < NT * MI; ++u) {
+                if (u % 4 != wave) continue;
                 const int t = u / MI, i = u % MI, m = m0 + i * 16 + lr;
                 const v4f v = sum(t, i);
                 if (m < hi) store4<EPI == MOE_MX_STORE_F32>(p.out, m, c0 + t * 16 + kb * 4, p.N, v);
@@ -327,18 +369,20 @@ __global__ __launch_bounds__(256) void mxgemm_rows_kernel(MxGemmArgs p) {
     }
 }
 
-template <int EPI, int MI>
-void launch_rows(const MxGemmArgs& a, hipStream_t st) {
-    constexpr int NT = 4;
-    constexpr int COLS = EPI == MOE_MX_SWIGLU_BF16 || EPI == MOE_MX_SWIGLU_QUANT ? NT * 8 : NT * 16;
-    const int cols = EPI == MOE_MX_SWIGLU_BF16 || EPI == MOE_MX_SWIGLU_QUANT ? a.N / 2 : a.N;
-    const dim3 grid((cols + COLS - 1) / COLS, a.G);
+template <int EPI, int MI, int NT, int BUF>
+hipError_t launch_rows(const MxGemmArgs& a, hipStream_t st) {
+    constexpr bool SWIGLU = EPI == MOE_MX_SWIGLU_BF16 || EPI == MOE_MX_SWIGLU_QUANT;
+    constexpr int COLS = SWIGLU ? NT * 8 : NT * 16;
+    const int cols = SWIGLU ? a.N / 2 : a.N;
+    // row tiles side by side: as many as a group has on the average, the others in turn
+    const int64_t deep = (a.M_total + (int64_t)a.G * 16 * MI - 1) / ((int64_t)a.G * 16 * MI);
+    const dim3 grid((cols + COLS - 1) / COLS, a.G, (unsigned)(deep < 65535 ? deep : 65535));
     if (a.K % 128 == 0)
-        hipLaunchKernelGGL((mxgemm_rows_kernel<EPI, MI, NT, true>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((mxgemm_rows_kernel<EPI, MI, NT, BUF, true>), grid, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((mxgemm_rows_kernel<EPI, MI, NT, false>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((mxgemm_rows_kernel<EPI, MI, NT, BUF, false>), grid, dim3(256), 0, st, a);
+    return hipGetLastError();
 }
-
 
 // ---------------------------------------------------------------- many rows to a group
 //
@@ -439,40 +483,6 @@ __device__ __forceinline__ v16f mfma32(v4u a, v4u b, v16f c, uint32_t sa, uint32
     const v8i y = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, J, (int)sa, J, (int)sb);
 }
-
-// 16 scale bytes of a row, blocks 16 c .. + 15; those past the row's nblk blocks
-// are zero, whatever lies there.  KA: the row starts on a word.  Otherwise the
-// five words around the bytes are read (the last row's may hold up to three bytes
-// past the tensor's end, in the word of its last byte) and shifted.
-template <bool KA>
-struct Scales {
-    v4u w;
-    uint32_t more;
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t d, uint32_t row, int c) {
-        if constexpr (KA) {
-            w = __builtin_amdgcn_raw_buffer_load_b128(d, row, c * 16, 0);
-        } else {
-            w = __builtin_amdgcn_raw_buffer_load_b128(d, row & ~3u, c * 16, 0);
-            more = __builtin_amdgcn_raw_buffer_load_b32(d, (row & ~3u) + 16u, c * 16, 0);
-        }
-    }
-    __device__ __forceinline__ v4u bytes(uint32_t row, int c, int nblk) const {
-        v4u v = w;
-        if constexpr (!KA) {
-            const uint32_t sh = (row & 3u) * 8u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = (uint32_t)((((uint64_t)(j < 3 ? w[j + 1] : more) << 32) | w[j]) >> sh);
-        }
-        const int left = nblk - c * 16;                  // of the row's blocks
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = left - 4 * j;
-            v[j] = n >= 4 ? v[j] : n <= 0 ? 0u : KA ? v[j] : v[j] & ((1u << (8 * n)) - 1u);
-        }
-        return v;
-    }
-};
 
 // First B row, inside the block's 256, of the wave's column tile t (of 4).
 template <bool SWIGLU>
@@ -831,10 +841,7 @@ hipError_t cu_count(int& cus) {
 }
 
 template <int EPI, int BM>
-hipError_t launch_tiles(const MxGemmArgs& a, hipStream_t st) {
-    int cus = 0;
-    const hipError_t e = cu_count(cus);
-    if (e != hipSuccess) return e;
+hipError_t launch_tiles(const MxGemmArgs& a, int cus, hipStream_t st) {
     const int64_t most = ((a.M_total + BM - 1) / BM + a.G) * ((a.N + TN - 1) / TN);
     const int64_t want = most < cus ? most : cus;
     const dim3 grid((unsigned)((want + 7) / 8 * 8));      // the same count on every XCD
@@ -843,14 +850,57 @@ hipError_t launch_tiles(const MxGemmArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
+// Which kernel.  The times below (us) were fitted to this card at K = 2048 and
+// 7168, N = 512 to 7168, 1 to 32 groups, weights from HBM and from L2; c is the
+// number of 512-value chunks of K, the work is counted in units of 16 x 16 results
+// over one chunk.  The host knows the groups' sizes on the average only.
+//   rows of 16,  2 column tiles, BUF 2:   7 + 0.6 c + units / 1260
+//   rows of 16,  4 column tiles:          7 + 1.5 c + units / 1740
+//   rows of 32,  4 column tiles:          7 + 1.1 c + units / 2800
+//   rows of 64,  4 column tiles:          7 + 1.2 c + units / 3500
+//   tiles of 128 x 256, a round of the CUs:  9 + 2.7 c, up to 9 + 3.3 c when full
+//   tiles of 256 x 256:                     11 + 2.7 c, up to 11 + 4.5 c
+// Measured at 32 groups, N = 4096, K = 7168 (the first two at 8 rows a group, then
+// 16, 64, 256 on the average): 108, 97, 112, 243, 118 (tiles of 128: 109, 109, 110,
+// 118, 275; of 256: 118, 118, 118, 125, 228); one group of one row: 10.8, 12.8,
+// 13.5, 15.7, 31, 39.
+enum Kernel { ROWS16_NT2, ROWS16, ROWS32, ROWS64, TILES128, TILES256 };
+
+Kernel choose(const MxGemmArgs& a, int cus) {
+    const double c = (double)((a.K + 511) / 512), groups = (double)(a.G < a.M_total ? a.G : a.M_total);
+    const double mean = (double)a.M_total / groups;
+    // row tiles of `high` rows, by halves: a group ends in half a tile on the average
+    auto row_tiles = [&](int high) { return mean <= 0.8 * high ? groups : (double)a.M_total / high + 0.5 * groups; };
+    const double columns = (double)((a.N + 15) / 16), wide = (double)((a.N + TN - 1) / TN);
+    auto rows = [&](int high, double at, double per, double rate) {
+        return at + per * c + row_tiles(high) * (high / 16) * columns * c / rate;
+    };
+    auto tiles = [&](int high, double at, double full) {
+        const double n = row_tiles(high) * wide, rounds = n / cus;
+        return rounds <= 1.0 ? at + (2.7 + (full - 2.7) * rounds) * c : __builtin_ceil(rounds) * (at + full * c);
+    };
+    const double t[6] = {rows(16, 7.0, 0.6, 1260.0), rows(16, 7.0, 1.5, 1740.0), rows(32, 7.0, 1.1, 2800.0),
+                         rows(64, 7.0, 1.2, 3500.0), tiles(128, 9.0, 3.3), tiles(256, 11.0, 4.5)};
+    int best = 0;
+    for (int i = 1; i < 6; ++i)
+        if (t[i] < t[best]) best = i;
+    return (Kernel)best;
+}
+
 template <int EPI>
 hipError_t launch_epi(const MxGemmArgs& a, hipStream_t st) {
-    const int64_t rows = (a.M_total + a.G - 1) / a.G;    // rows of a group, on the average
-    if (rows <= 16) launch_rows<EPI, 1>(a, st);
-    else if (rows <= 48) launch_rows<EPI, 4>(a, st);
-    else if (rows <= 192) return launch_tiles<EPI, 128>(a, st);
-    else return launch_tiles<EPI, 256>(a, st);
-    return hipGetLastError();
+    constexpr int FEW = EPI == MOE_MX_SWIGLU_QUANT ? 4 : 2;      // 32 columns of h need 4 column tiles
+    int cus = 0;
+    const hipError_t e = cu_count(cus);
+    if (e != hipSuccess) return e;
+    switch (choose(a, cus)) {
+        case ROWS16_NT2: return launch_rows<EPI, 1, FEW, 2>(a, st);
+        case ROWS16: return launch_rows<EPI, 1, 4, 1>(a, st);
+        case ROWS32: return launch_rows<EPI, 2, 4, 1>(a, st);
+        case ROWS64: return launch_rows<EPI, 4, 4, 1>(a, st);
+        case TILES128: return launch_tiles<EPI, 128>(a, cus, st);
+        default: return launch_tiles<EPI, 256>(a, cus, st);
+    }
 }
 
 }  // namespace

@@ -15,9 +15,13 @@
 // reduction and its use, and written once.
 #include "device_math.h"
 #include "kernels.h"
+#include "streaming.h"
 
 namespace moe {
 namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
@@ -67,19 +71,19 @@ __device__ __forceinline__ void load8(const void* p, bool f32, int64_t row_off, 
     }
 }
 
-template <bool VEC>
+template <bool VEC, bool NT>
 __device__ __forceinline__ void store8(void* p, bool f32, int64_t row_off, int v, int t, int tpr, int d,
                                        const float (&x)[8]) {
     if constexpr (VEC) {
         const int c = col_of<VEC>(v, 0, t, tpr);
         if (c >= d) return;
         if (f32) {
-            float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + row_off + c);
-            q[0] = make_float4(x[0], x[1], x[2], x[3]);
-            q[1] = make_float4(x[4], x[5], x[6], x[7]);
+            v4f* q = reinterpret_cast<v4f*>(static_cast<float*>(p) + row_off + c);
+            put<NT>(q, v4f{x[0], x[1], x[2], x[3]});
+            put<NT>(q + 1, v4f{x[4], x[5], x[6], x[7]});
         } else {
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + row_off + c) =
-                make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+            put<NT>(reinterpret_cast<v4u*>(static_cast<uint16_t*>(p) + row_off + c),
+                    v4u{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])});
         }
     } else {
 #pragma unroll
@@ -102,14 +106,15 @@ __device__ __forceinline__ float row_sum(float s, float (*part)[16], int flip) {
     if constexpr (WAVE_ROW) return s;
     const int nw = (int)blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0) part[flip][threadIdx.x >> 6] = s;
-    __syncthreads();
+    // a barrier for LDS alone: loads and stores under way go on
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     s = part[flip][0];
     for (int i = 1; i < nw; ++i) s += part[flip][i];
     return s;
 }
 
 // A block is one row at a time (WAVE_ROW: each of its four waves is one).
-template <int NV, bool VEC, bool WAVE_ROW>
+template <int NV, bool VEC, bool WAVE_ROW, bool NT>
 __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddRmsnormArgs a) {
     __shared__ float part[2][16];
     const int t = WAVE_ROW ? (int)threadIdx.x & 63 : (int)threadIdx.x;
@@ -136,7 +141,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddR
                 for (int j = 0; j < 8; ++j) h[v][j] += r[v][j];
             if (a.h) {
 #pragma unroll
-                for (int v = 0; v < NV; ++v) store8<VEC>(a.h, a.res_f32, off, v, t, tpr, d, h[v]);
+                for (int v = 0; v < NV; ++v) store8<VEC, NT>(a.h, a.res_f32, off, v, t, tpr, d, h[v]);
             }
         }
         float s = 0.0f;
@@ -152,7 +157,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddR
             float y[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) y[j] = h[v][j] * rstd * w[v][j];
-            if (a.y) store8<VEC>(a.y, false, off, v, t, tpr, d, y);
+            if (a.y) store8<VEC, NT>(a.y, false, off, v, t, tpr, d, y);
             if constexpr (VEC) {
                 if (a.q) {                            // d % 128 == 0: 16 lanes are one tile, all in the row or none
                     const int c = col_of<VEC>(v, 0, t, tpr);
@@ -176,9 +181,9 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddR
                     float inv, sc;
                     tile_scale(amax, inv, sc);
                     if (c < d) {
-                        *reinterpret_cast<uint2*>(a.q + off + c) =
-                            make_uint2(e4m3_encode4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                                       e4m3_encode4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+                        put<NT>(reinterpret_cast<v2u*>(a.q + off + c),
+                                v2u{e4m3_encode4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                                    e4m3_encode4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv)});
                         if ((t & 15) == 0) a.scale[row * (d / 128) + c / 128] = sc;
                     }
                 }
@@ -187,9 +192,9 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddR
     }
 }
 
-// As the forward; each row's block (WAVE_ROW: wave) keeps the sum of dy * xh of
-// its rows in registers and leaves it as one row of `part` at the end.
-template <int NV, bool VEC, bool WAVE_ROW>
+// As the forward; each block keeps the sum of dy * xh of its rows in registers and
+// leaves it as one row of `part` at the end.
+template <int NV, bool VEC, bool WAVE_ROW, bool NT>
 __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_backward_kernel(AddRmsnormBackwardArgs a) {
     __shared__ float part[2][16];
     const int t = WAVE_ROW ? (int)threadIdx.x & 63 : (int)threadIdx.x;
@@ -214,6 +219,11 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_backward_ke
         for (int v = 0; v < NV; ++v) load8<VEC>(a.dy, a.dy_f32, off, v, t, tpr, d, g[v]);
 #pragma unroll
         for (int v = 0; v < NV; ++v) load8<VEC>(a.h, a.h_f32, off, v, t, tpr, d, xh[v]);
+        float r[NV][8];                               // asked for before the reduction
+        if (a.dh) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) load8<VEC>(a.dh, a.dx_f32, off, v, t, tpr, d, r[v]);
+        }
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -230,21 +240,33 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_backward_ke
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = (g[v][j] - xh[v][j] * c) * rstd;
             if (a.dh) {
-                float r[8];
-                load8<VEC>(a.dh, a.dx_f32, off, v, t, tpr, d, r);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] += r[j];
+                for (int j = 0; j < 8; ++j) o[j] += r[v][j];
             }
-            store8<VEC>(a.dx, a.dx_f32, off, v, t, tpr, d, o);
+            store8<VEC, NT>(a.dx, a.dx_f32, off, v, t, tpr, d, o);
         }
     }
-    const int64_t prow = WAVE_ROW ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    if constexpr (WAVE_ROW) {                            // the block's four waves as one partial row
+        __shared__ float sum[4][NV * 512];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) store8<VEC>(a.part, true, prow * d, v, t, tpr, d, dw[v]);
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[threadIdx.x >> 6][(v * 8 + j) * 64 + t] = dw[v][j];
+        __syncthreads();
+        if (threadIdx.x >= 64) return;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int i = 1; i < 4; ++i) dw[v][j] += sum[i][(v * 8 + j) * 64 + t];
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) store8<VEC, false>(a.part, true, (int64_t)blockIdx.x * d, v, t, tpr, d, dw[v]);
 }
 
 // dw[c] = sum of the partial rows: 16 threads take every 16th row of a column,
-// then their sums are added in order.
+// eight loads at a time, then their sums are added in order.
 __global__ __launch_bounds__(256) void dw_reduce_kernel(const float* __restrict__ part, int rows, int d,
                                                         float* __restrict__ dw) {
     __shared__ float sum[16][17];
@@ -252,7 +274,13 @@ __global__ __launch_bounds__(256) void dw_reduce_kernel(const float* __restrict_
     const int c = blockIdx.x * 16 + cl;
     float s = 0.0f;
     if (c < d)
-        for (int r = rl; r < rows; r += 16) s += part[(int64_t)r * d + c];
+        for (int r = rl; r < rows; r += 128) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = part[(int64_t)min(r + 16 * i, rows - 1) * d + c];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += r + 16 * i < rows ? x[i] : 0.0f;
+        }
     sum[rl][cl] = s;
     __syncthreads();
     if (rl == 0 && c < d) {
@@ -294,9 +322,12 @@ struct ForwardLaunch {
     void operator()() const {
         const int64_t per = WAVE_ROW ? 4 : 1;
         int64_t blocks = (a.T + per - 1) / per;
-        if (blocks > 2048) blocks = 2048;
-        hipLaunchKernelGGL((add_rmsnorm_kernel<NV, VEC, WAVE_ROW>), dim3((unsigned)blocks), dim3(row_threads(a.d)), 0,
-                           st, a);
+        if (blocks > 0x7FFFFFFF) blocks = 0x7FFFFFFF;
+        const dim3 grid((unsigned)blocks), block(row_threads(a.d));
+        if (stored_past_l2(a.T * a.d * 2))
+            hipLaunchKernelGGL((add_rmsnorm_kernel<NV, VEC, WAVE_ROW, true>), grid, block, 0, st, a);
+        else
+            hipLaunchKernelGGL((add_rmsnorm_kernel<NV, VEC, WAVE_ROW, false>), grid, block, 0, st, a);
     }
 };
 
@@ -305,8 +336,11 @@ struct BackwardLaunch {
     hipStream_t st;
     template <int NV, bool VEC, bool WAVE_ROW>
     void operator()() const {
-        hipLaunchKernelGGL((add_rmsnorm_backward_kernel<NV, VEC, WAVE_ROW>), dim3(backward_blocks(a.T, a.d)),
-                           dim3(row_threads(a.d)), 0, st, a);
+        const dim3 grid(backward_blocks(a.T, a.d)), block(row_threads(a.d));
+        if (stored_past_l2(a.T * a.d * 2))
+            hipLaunchKernelGGL((add_rmsnorm_backward_kernel<NV, VEC, WAVE_ROW, true>), grid, block, 0, st, a);
+        else
+            hipLaunchKernelGGL((add_rmsnorm_backward_kernel<NV, VEC, WAVE_ROW, false>), grid, block, 0, st, a);
     }
 };
 
@@ -318,7 +352,7 @@ hipError_t launch_add_rmsnorm(const AddRmsnormArgs& a, hipStream_t st) {
 }
 
 size_t add_rmsnorm_backward_ws_bytes(int64_t T, int d) {
-    return (size_t)backward_blocks(T, d) * (wave_row(d) ? 4 : 1) * d * sizeof(float);
+    return (size_t)backward_blocks(T, d) * d * sizeof(float);
 }
 
 hipError_t launch_add_rmsnorm_backward(const AddRmsnormBackwardArgs& a, float* dw, hipStream_t st) {
@@ -327,7 +361,7 @@ hipError_t launch_add_rmsnorm_backward(const AddRmsnormBackwardArgs& a, float* d
         dispatch_shape(a.d, BackwardLaunch{a, st});
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        rows = backward_blocks(a.T, a.d) * (wave_row(a.d) ? 4 : 1);
+        rows = backward_blocks(a.T, a.d);
     }
     hipLaunchKernelGGL(dw_reduce_kernel, dim3((a.d + 15) / 16), dim3(256), 0, st, a.part, rows, a.d, dw);
     return hipGetLastError();

@@ -206,6 +206,49 @@ def test_product_exact(sizes, N, K):
     assert torch.equal(half, ref.float().bfloat16())
 
 
+# Sizes that the other kernels take: a wave's 16 rows in 32 groups, tiles of 128
+# rows, tiles of 256; K with and without a whole number of 128s and of 512s.
+MANY = [
+    ([13] * 31 + [0], 4096, 640), ([12] * 30 + [1, 39], 4096, 1056),
+    ([1200, 0, 500, 300], 1500, 1056), ([700, 1, 0, 1100, 199], 1536, 2048), ([129, 128, 127, 1616], 1280, 1152),
+    ([6000], 4096, 544), ([3500, 0, 2500], 4000, 672), ([2600, 1, 0, 255, 257, 2300, 31], 3840, 1024),
+    ([5000, 256], 3840, 1152),
+]
+
+
+@pytest.mark.parametrize("sz,N,K", MANY)
+def test_product_exact_of_many_rows(sz, N, K):
+    dev()
+    M, G = sum(sz), len(sz)
+    say(f"  M={M} G={G} N={N} K={K}")
+    aq, a_s, bq, b_s, idx = operands(M, M // 2 + 5, G, N, K, N + K + M)
+    idx[[0, M // 3, M - 1]] = torch.tensor([-1, M // 2 + 5, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    ref = ref_product(aq, a_s, bq, b_s, idx, sz)
+    off = offsets(sz)
+    out = torch.full((M + 2, N), 7.0, device="cuda")
+    moe.grouped_gemm_mxfp4(aq, a_s, off, M, bq, b_s, a_row_index=idx, out=out[:M])
+    half = torch.full((M + 2, N), 7.0, device="cuda", dtype=torch.bfloat16)
+    moe.grouped_gemm_mxfp4(aq, a_s, off, M, bq, b_s, a_row_index=idx, epi=moe.MOE_MX_STORE_BF16, out=half[:M])
+    torch.cuda.synchronize()
+    assert torch.equal(out[:M].to(F8), ref) and (out[M:] == 7.0).all()
+    assert torch.equal(half[:M], ref.float().bfloat16()) and (half[M:] == 7.0).all()
+    a_s[4, K // 32 - 1] = 255                       # a NaN scale stays in its rows and its column
+    b_s[G - 1 if sz[-1] else G - 2, N - 1, K // 32 - 1] = 255
+    got = moe.grouped_gemm_mxfp4(aq, a_s, off, M, bq, b_s, a_row_index=idx)
+    torch.cuda.synchronize()
+    nan = (idx == 4)[:, None].expand(M, N).clone()
+    nan[M - (sz[-1] or sz[-2]):, N - 1] = True
+    assert torch.equal(torch.isnan(got), nan) and torch.equal(got[~nan].to(F8), ref[~nan])
+    again = moe.grouped_gemm_mxfp4(aq, a_s, off, M, bq, b_s, a_row_index=idx)
+    assert torch.equal(again.view(torch.int32), got.view(torch.int32))
+
+
+@pytest.mark.parametrize("sz,N,K", [m for m in MANY if m[1] % 256 == 0])
+def test_swiglu_of_many_rows(sz, N, K):
+    dev()
+    check_swiglu(sz, N, K)
+
+
 @pytest.mark.parametrize("sizes", ["few", "dense", "uneven"])
 def test_product_without_a_row_index(sizes):
     dev()
@@ -246,9 +289,12 @@ def test_swiglu(sizes, N, K):
     argument's rounding adds |gate| 2^-24.  bf16 then rounds by 2^-8; the MXFP4 codes are the nearest to
     within that error."""
     dev()
-    sz = SIZES[sizes]
+    check_swiglu(SIZES[sizes], N, K)
+
+
+def check_swiglu(sz, N, K):
     M = sum(sz)
-    say(f"  {sizes} M={M} N={N} K={K}")
+    say(f"  M={M} G={len(sz)} N={N} K={K}")
     aq, a_s, bq, b_s, idx = operands(M, max(M, 1), len(sz), N, K, 11, low=121, high=124)
     off = offsets(sz)
     c = ref_product(aq, a_s, bq, b_s, idx, sz)
@@ -262,6 +308,9 @@ def test_swiglu(sizes, N, K):
     assert ((got.to(F8) - h).abs() <= (2.0 ** -8 + rel) * h.abs() + tiny).all()
     if M == 0:
         return
+    rows = np.unique(np.linspace(0, M - 1, 1500).astype(np.int64))        # of many, these
+    at = torch.from_numpy(rows).cuda()
+    q, s, h, rel = q[at], s[at], h[at], rel[at]
     hb, rb = np_(h).reshape(-1, 32), np_(rel).reshape(-1, 32)
     e = np_(s).reshape(-1).astype(np.int64) - 127
     _, lo = ref_quant((np.abs(hb) * (1 - rb)).astype(np.float64))
@@ -348,9 +397,9 @@ def test_offsets_past_32_bits():
 
 def test_repeatable_on_another_stream_and_in_a_graph():
     dev()
-    for sz in ([3, 0, 9, 1], [300, 40]):
+    for sz, N in (([3, 0, 9, 1], 512), ([300, 40], 512), ([1500, 0, 700], 1536), ([3000, 3000], 4096)):
         M = sum(sz)
-        aq, a_s, bq, b_s, idx = operands(M, M, len(sz), 512, 1056, 4, low=120, high=130)
+        aq, a_s, bq, b_s, idx = operands(M, M, len(sz), N, 1056, 4, low=120, high=130)
         off = offsets(sz)
         x = torch.randn((M, 1056), device="cuda")
 
