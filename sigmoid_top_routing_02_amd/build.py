@@ -27,25 +27,20 @@ FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall",
     "-Wno-unused-command-line-argument",
-    "-mllvm", "-amdgpu-mfma-vgpr-form",   # MFMA results in VGPRs: the VALU consumes every slice
     # no wave-level rewriting of atomics: the GEMM's next-tile request must not
     # be waited for (with every DMA in flight) right where it is issued
     "-mllvm", "-amdgpu-atomic-optimizer-strategy=None",
 ]
 
-# Sources that take other flags than FLAGS.  The MXFP4 product chains its
-# accumulators through the matrix instruction and fills the accumulation
-# registers with them, so it leaves the VGPR form to the others.
-WITHOUT = {"mxgemm.hip": ("-mllvm", "-amdgpu-mfma-vgpr-form")}
+# Every source but the MXFP4 product takes MFMA results in VGPRs: the VALU
+# consumes every slice there.  That product chains its results through the matrix
+# instruction and fills the accumulation registers with them.
+VGPR_RESULTS = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+CHAINED = ("mxgemm.hip",)
 
 
 def flags_of(source):
-    """FLAGS without what WITHOUT names for this source."""
-    drop = WITHOUT.get(os.path.basename(source))
-    if not drop:
-        return list(FLAGS)
-    at = next(i for i in range(len(FLAGS)) if tuple(FLAGS[i:i + len(drop)]) == drop)
-    return FLAGS[:at] + FLAGS[at + len(drop):]
+    return FLAGS + ([] if os.path.basename(source) in CHAINED else VGPR_RESULTS)
 
 
 def sources():
