@@ -31,6 +31,8 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 // reads there return 0 and touch no memory.
 constexpr uint32_t OUT = 0xFFFF0000u;
 
+#define FENCE() __builtin_amdgcn_sched_barrier(0)
+
 template <int V>
 struct IC { static constexpr int value = V; };
 
@@ -62,6 +64,7 @@ struct Scales {
             more = __builtin_amdgcn_raw_buffer_load_b32(d, (row & ~3u) + 16u, c * 16, 0);
         }
     }
+    template <bool WHOLE = false>                        // all 16 blocks are in the row
     __device__ __forceinline__ v4u bytes(uint32_t row, int c, int nblk) const {
         v4u v = w;
         if constexpr (!KA) {
@@ -70,6 +73,7 @@ struct Scales {
             for (int j = 0; j < 4; ++j)
                 v[j] = (uint32_t)((((uint64_t)(j < 3 ? w[j + 1] : more) << 32) | w[j]) >> sh);
         }
+        if constexpr (WHOLE) return v;
         const int left = nblk - c * 16;                  // of the row's blocks
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -226,37 +230,94 @@ __device__ __forceinline__ int b_row(int c0, int tile) {
 // add up through LDS, so that a single row of a few groups still fills the card.
 // Operands go straight to registers, one access taking 64 consecutive bytes of each
 // of 16 rows.  Lane l takes block 4 j + l / 16 of a chunk in its slice j, and byte
-// l / 16 of the chunk's scale word j.  BUF = 2 loads the next chunk while one is
-// multiplied, BUF = 1 leaves that to the other waves of the CU.
+// l / 16 of the chunk's scale word j.  A wave sends for a whole chunk of all its
+// tiles before it uses any (left to itself the compiler mixes the two, to save
+// registers: 105 us where this takes 93, at 256 rows in 32 groups, N = 4096, K =
+// 7168, 5.4 TB/s); the next chunk is left to the CU's other waves (two chunks in
+// turn in one wave: 112 us).
 template <bool KA>
 struct Chunk {
     v4u q[4];
     Scales<KA> s;
-    // row_q, row_s: the row's first byte in codes and scales, or OUT for no row.
-    // Blocks past the row's end read zero codes; bytes() clears their scales.
+    // row_q: the lane's first byte of the row's codes, row_s: the row's first scale,
+    // or OUT for no row.  WHOLE: all of the chunk's blocks are in the row; otherwise
+    // those past its end read zero codes, and bytes() clears their scales.
+    template <bool WHOLE>
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t dq, __amdgpu_buffer_rsrc_t ds, uint32_t row_q,
                                          uint32_t row_s, int c, int kb, int nblk) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            q[j] = __builtin_amdgcn_raw_buffer_load_b128(
-                dq, c * 16 + j * 4 + kb < nblk && row_q != OUT ? row_q + (uint32_t)(j * 4 + kb) * 16u : OUT, c * 256, 0);
-        s.load(ds, c * 16 < nblk ? row_s : OUT, c);
+        for (int j = 0; j < 4; ++j) {
+            const bool in = WHOLE || c * 16 + j * 4 + kb < nblk;
+            q[j] = __builtin_amdgcn_raw_buffer_load_b128(dq, in ? row_q + j * 64u : OUT, c * 256, 0);
+        }
+        s.load(ds, row_s, c);
     }
 };
 
-template <int EPI, int MI, int NT, int BUF, bool KA>
+// First row and number of rows of group g (none past the last group).  Offsets
+// outside [0, M_total], which the caller must not pass, are held inside it.
+__device__ __forceinline__ int2 rows_of(const MxGemmArgs& p, int g, int total) {
+    if (g >= p.G) return make_int2(0, 0);
+    const int lo = min(max(p.group_offset[g], 0), total), hi = min(max(p.group_offset[g + 1], 0), total);
+    return make_int2(lo, max(hi - lo, 0));
+}
+
+// Sum of v over the block's threads before this one (256 threads; wsum: four ints
+// of LDS that nothing else uses before the next barrier after the call).
+__device__ __forceinline__ int scan_threads(int v, int* wsum) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(incl, o, 64);
+        if (lane >= o) incl += u;
+    }
+    if (lane == 63) wsum[wave] = incl;
+    __syncthreads();
+    int at = incl - v;
+    for (int w = 0; w < wave; ++w) at += wsum[w];
+    return at;
+}
+
+template <int EPI, int MI, int NT, bool KA>
 __global__ __launch_bounds__(256) void mxgemm_rows_kernel(MxGemmArgs p) {
     constexpr bool SWIGLU = EPI == MOE_MX_SWIGLU_BF16 || EPI == MOE_MX_SWIGLU_QUANT;
     constexpr int COLS = SWIGLU ? NT * 8 : NT * 16;      // output columns of the block
     __shared__ v4f red[4][MI * NT][64];
     const int lane = threadIdx.x & 63, lr = lane & 15, kb = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int g = blockIdx.y;
     const int total = (int)p.M_total;
-    // offsets outside [0, M_total] (which the caller must not pass) are held inside it
-    const int lo = min(max(p.group_offset[g], 0), total);
-    const int hi = min(p.group_offset[g + 1], total);
-    if (lo >= hi) return;
+    // Grid row y < G has the first row tile of group y, the others one of the tiles
+    // after the first each, counted over the groups.
+    int g = blockIdx.y, m0 = 0;
+    if (g >= p.G) {
+        __shared__ int wsum[4], found[2];
+        const int tid = threadIdx.x, want = g - p.G;
+        int n[4], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            n[i] = max((rows_of(p, tid * 4 + i, total).y + 16 * MI - 1) / (16 * MI) - 1, 0);
+            sum += n[i];
+        }
+        if (tid == 0) found[0] = -1;
+        int at = scan_threads(sum, wsum);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (at <= want && want < at + n[i]) {
+                found[0] = tid * 4 + i;
+                found[1] = (want - at + 1) * 16 * MI;
+            }
+            at += n[i];
+        }
+        __syncthreads();
+        g = __builtin_amdgcn_readfirstlane(found[0]);
+        m0 = __builtin_amdgcn_readfirstlane(found[1]);
+        if (g < 0) return;
+    }
+    const int2 rows = rows_of(p, g, total);
+    const int hi = rows.x + rows.y;
+    m0 += rows.x;
+    if (m0 >= hi) return;
     const int nblk = p.K / 32, nchunk = (nblk + 15) / 16;
     const uint32_t rb = (uint32_t)p.K / 2;               // bytes of a row of codes
     // Scale descriptors end on a word.  A group's scales may start off one: the
@@ -272,115 +333,111 @@ __global__ __launch_bounds__(256) void mxgemm_rows_kernel(MxGemmArgs p) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const uint32_t n = (uint32_t)min(b_row<EPI, NT>(c0, t) + lr, p.N - 1);     // columns past N are not stored
-        bro[t] = n * rb;
+        bro[t] = n * rb + (uint32_t)kb * 16u;
         bso[t] = n * (uint32_t)nblk + off;
     }
-    for (int64_t row = lo + (int64_t)blockIdx.z * (16 * MI); row < hi; row += (int64_t)gridDim.z * (16 * MI)) {
-        const int m0 = (int)row;
-        uint32_t aro[MI], aso[MI];
+    uint32_t aro[MI], aso[MI];
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const int m = m0 + i * 16 + lr;
-            const uint32_t r = m < hi ? (p.a_row_index ? (uint32_t)p.a_row_index[m] : (uint32_t)m) : 0xFFFFFFFFu;
-            const bool in = r < (uint32_t)p.a_rows;      // a row that A does not have counts as zeros
-            aro[i] = in ? r * rb : OUT;
-            aso[i] = in ? r * (uint32_t)nblk : OUT;
+    for (int i = 0; i < MI; ++i) {
+        const int m = m0 + i * 16 + lr;
+        const uint32_t r = m < hi ? (p.a_row_index ? (uint32_t)p.a_row_index[m] : (uint32_t)m) : 0xFFFFFFFFu;
+        const bool in = r < (uint32_t)p.a_rows;      // a row that A does not have counts as zeros
+        aro[i] = in ? r * rb + (uint32_t)kb * 16u : OUT;
+        aso[i] = in ? r * (uint32_t)nblk : OUT;
+    }
+    v4f acc[NT][MI];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < MI; ++i) acc[t][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    Chunk<KA> fa[MI], fb[NT];
+    auto load = [&](auto whole, int c) {
+        constexpr bool W = decltype(whole)::value;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) fb[t].template load<W>(bq, bs, bro[t], bso[t], c, kb, nblk);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) fa[i].template load<W>(aq, as, aro[i], aso[i], c, kb, nblk);
+        FENCE();                                         // all of them are sent for before any is used
+    };
+    auto multiply = [&](auto whole, int c) {
+        constexpr bool W = decltype(whole)::value;
+        v4u sa[MI];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) sa[i] = fa[i].s.template bytes<W>(aso[i], c, nblk);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const v4u sb = fb[t].s.template bytes<W>(bso[t], c, nblk);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+                    acc[t][i] = mfma16(fb[t].q[j], fa[i].q[j], acc[t][i], sb[j] >> (8 * kb), sa[i][j] >> (8 * kb));
         }
-        v4f acc[NT][MI];
+        FENCE();
+    };
+    constexpr IC<1> whole{};
+    constexpr IC<0> part{};
+    const int n_whole = nblk / 16;                       // chunks that K fills; what it leaves comes last
+    for (int c = wave; c < n_whole; c += 4) {
+        load(whole, c);
+        multiply(whole, c);
+    }
+    if (n_whole < nchunk && n_whole % 4 == wave) {
+        load(part, n_whole);
+        multiply(part, n_whole);
+    }
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < MI; ++i) acc[t][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        Chunk<KA> fa[BUF][MI], fb[BUF][NT];
-        auto load = [&](int buf, int c) {                // past the last chunk everything reads zero
+        for (int i = 0; i < MI; ++i) red[wave][t * MI + i][lane] = acc[t][i];
+    __syncthreads();
+    auto sum = [&](int t, int i) {
+        v4f s = red[0][t * MI + i][lane];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) fb[buf][t].load(bq, bs, bro[t], bso[t], c, kb, nblk);
+        for (int w = 1; w < 4; ++w) s += red[w][t * MI + i][lane];
+        return s;
+    };
+    // the waves take the units of output in turn
+    if constexpr (EPI == MOE_MX_SWIGLU_QUANT) {
 #pragma unroll
-            for (int i = 0; i < MI; ++i) fa[buf][i].load(aq, as, aro[i], aso[i], c, kb, nblk);
-        };
-        auto multiply = [&](int buf, int c) {
-            v4u sa[MI];
-#pragma unroll
-            for (int i = 0; i < MI; ++i) sa[i] = fa[buf][i].s.bytes(aso[i], c, nblk);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const v4u sb = fb[buf][t].s.bytes(bso[t], c, nblk);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int i = 0; i < MI; ++i)
-                        acc[t][i] = mfma16(fb[buf][t].q[j], fa[buf][i].q[j], acc[t][i], sb[j] >> (8 * kb), sa[i][j] >> (8 * kb));
-            }
-        };
-        if constexpr (BUF == 2) {
-            load(0, wave);
-            for (int c = wave; c < nchunk; c += 8) {
-                load(1, c + 4);
-                multiply(0, c);
-                load(0, c + 8);
-                multiply(1, c + 4);
-            }
-        } else {
-            for (int c = wave; c < nchunk; c += 4) {
-                load(0, c);
-                multiply(0, c);
-            }
+        for (int u = 0; u < NT / 4 * MI; ++u) {              // 32 columns of 16 rows
+            if (u % 4 != wave) continue;
+            const int t = u / MI * 2, i = u % MI, m = m0 + i * 16 + lr;
+            const v4f a = swiglu(sum(t, i), sum(t + NT / 2, i));
+            const v4f b = swiglu(sum(t + 1, i), sum(t + 1 + NT / 2, i));
+            store_mx_block(p.out_q, p.out_s, (int64_t)m * (p.N / 64) + (c0 + t * 16) / 32, kb,
+                           m < hi && c0 < p.N / 2, a, b);
         }
+    } else if constexpr (SWIGLU) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < MI; ++i) red[wave][t * MI + i][lane] = acc[t][i];
-        __syncthreads();
-        auto sum = [&](int t, int i) {
-            v4f s = red[0][t * MI + i][lane];
-#pragma unroll
-            for (int w = 1; w < 4; ++w) s += red[w][t * MI + i][lane];
-            return s;
-        };
-        // the waves take the units of output in turn
-        if constexpr (EPI == MOE_MX_SWIGLU_QUANT) {
-#pragma unroll
-            for (int u = 0; u < NT / 4 * MI; ++u) {              // 32 columns of 16 rows
-                if (u % 4 != wave) continue;
-                const int t = u / MI * 2, i = u % MI, m = m0 + i * 16 + lr;
-                const v4f a = swiglu(sum(t, i), sum(t + NT / 2, i));
-                const v4f b = swiglu(sum(t + 1, i), sum(t + 1 + NT / 2, i));
-                store_mx_block(p.out_q, p.out_s, (int64_t)m * (p.N / 64) + (c0 + t * 16) / 32, kb,
-                               m < hi && c0 < p.N / 2, a, b);
-            }
-        } else if constexpr (SWIGLU) {
-#pragma unroll
-            for (int u = 0; u < NT / 2 * MI; ++u) {
-                if (u % 4 != wave) continue;
-                const int t = u / MI, i = u % MI, m = m0 + i * 16 + lr;
-                const v4f h = swiglu(sum(t, i), sum(t + NT / 2, i));
-                if (m < hi) store4<false>(p.out, m, c0 + t * 16 + kb * 4, p.N / 2, h);
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < NT * MI; ++u) {
-                if (u % 4 != wave) continue;
-                const int t = u / MI, i = u % MI, m = m0 + i * 16 + lr;
-                const v4f v = sum(t, i);
-                if (m < hi) store4<EPI == MOE_MX_STORE_F32>(p.out, m, c0 + t * 16 + kb * 4, p.N, v);
-            }
+        for (int u = 0; u < NT / 2 * MI; ++u) {
+            if (u % 4 != wave) continue;
+            const int t = u / MI, i = u % MI, m = m0 + i * 16 + lr;
+            const v4f h = swiglu(sum(t, i), sum(t + NT / 2, i));
+            if (m < hi) store4<false>(p.out, m, c0 + t * 16 + kb * 4, p.N / 2, h);
         }
-        __syncthreads();
+    } else {
+#pragma unroll
+        for (int u = 0; u < NT * MI; ++u) {
+            if (u % 4 != wave) continue;
+            const int t = u / MI, i = u % MI, m = m0 + i * 16 + lr;
+            const v4f v = sum(t, i);
+            if (m < hi) store4<EPI == MOE_MX_STORE_F32>(p.out, m, c0 + t * 16 + kb * 4, p.N, v);
+        }
     }
 }
 
-template <int EPI, int MI, int NT, int BUF>
+template <int EPI, int MI, int NT>
 hipError_t launch_rows(const MxGemmArgs& a, hipStream_t st) {
     constexpr bool SWIGLU = EPI == MOE_MX_SWIGLU_BF16 || EPI == MOE_MX_SWIGLU_QUANT;
     constexpr int COLS = SWIGLU ? NT * 8 : NT * 16;
     const int cols = SWIGLU ? a.N / 2 : a.N;
-    // row tiles side by side: as many as a group has on the average, the others in turn
-    const int64_t deep = (a.M_total + (int64_t)a.G * 16 * MI - 1) / ((int64_t)a.G * 16 * MI);
-    const dim3 grid((cols + COLS - 1) / COLS, a.G, (unsigned)(deep < 65535 ? deep : 65535));
+    // a grid row for every group's first row tile, and for all that M_total rows can make after those
+    const dim3 grid((cols + COLS - 1) / COLS, (unsigned)(a.G + a.M_total / (16 * MI)));
     if (a.K % 128 == 0)
-        hipLaunchKernelGGL((mxgemm_rows_kernel<EPI, MI, NT, BUF, true>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((mxgemm_rows_kernel<EPI, MI, NT, true>), grid, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((mxgemm_rows_kernel<EPI, MI, NT, BUF, false>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((mxgemm_rows_kernel<EPI, MI, NT, false>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
@@ -444,7 +501,6 @@ __device__ __forceinline__ v4u deal_scales(v4u v) {
 // 64 banks.
 __device__ __forceinline__ int swz(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
 
-#define FENCE() __builtin_amdgcn_sched_barrier(0)
 #define SCHED(KIND, N) __builtin_amdgcn_sched_group_barrier(KIND, N, 0)
 constexpr int MFMA = 0x8, VMEM = 0x20, DS_READ = 0x100;
 
@@ -506,32 +562,19 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
     const int nblk = p.K / 32, nchunk = (nblk + 15) / 16;
     const uint32_t rb = (uint32_t)p.K / 2;
 
-    // Row tiles before each group: four groups a thread, then a scan of the threads.
+    // Row tiles before each group, four groups a thread.
     {
         int n[4], sum = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int g = tid * 4 + i;
-            n[i] = 0;
-            if (g < p.G) {
-                const int lo = min(max(p.group_offset[g], 0), total), hi = min(max(p.group_offset[g + 1], 0), total);
-                n[i] = hi > lo ? (hi - lo + BM - 1) / BM : 0;
-                rows[g] = lo;
-                if (g == p.G - 1) rows[p.G] = hi;
-            }
+            const int2 r = rows_of(p, g, total);
+            n[i] = (r.y + BM - 1) / BM;
+            if (g < p.G) rows[g] = r.x;
+            if (g == p.G - 1) rows[p.G] = r.x + r.y;
             sum += n[i];
         }
-        int incl = sum;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(incl, o, 64);
-            if (lane >= o) incl += v;
-        }
-        int* wsum = reinterpret_cast<int*>(g_s0);
-        if (lane == 63) wsum[wave] = incl;
-        __syncthreads();
-        int at = incl - sum;
-        for (int w = 0; w < wave; ++w) at += wsum[w];
+        int at = scan_threads(sum, reinterpret_cast<int*>(g_s0));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             start[tid * 4 + i] = at;
@@ -851,20 +894,20 @@ hipError_t launch_tiles(const MxGemmArgs& a, int cus, hipStream_t st) {
 }
 
 // Which kernel.  The times below (us) were fitted to this card at K = 2048 and
-// 7168, N = 512 to 7168, 1 to 32 groups, weights from HBM and from L2; c is the
+// 7168, N = 512 to 7168, 1 to 257 groups, weights from HBM and from L2; c is the
 // number of 512-value chunks of K, the work is counted in units of 16 x 16 results
 // over one chunk.  The host knows the groups' sizes on the average only.
-//   rows of 16,  2 column tiles, BUF 2:   7 + 0.6 c + units / 1260
-//   rows of 16,  4 column tiles:          7 + 1.5 c + units / 1740
-//   rows of 32,  4 column tiles:          7 + 1.1 c + units / 2800
-//   rows of 64,  4 column tiles:          7 + 1.2 c + units / 3500
+//   16 rows, 2 column tiles:  6 + 0.3 c + units / 1600
+//   16 rows, 4 column tiles:  6 + 0.5 c + units / 1800
+//   32 rows, 4 column tiles:  6 + 0.65 c + units / 3000
+//   64 rows, 4 column tiles:  6 + 0.95 c + units / 3500
 //   tiles of 128 x 256, a round of the CUs:  9 + 2.7 c, up to 9 + 3.3 c when full
 //   tiles of 256 x 256:                     11 + 2.7 c, up to 11 + 4.5 c
-// Measured at 32 groups, N = 4096, K = 7168 (the first two at 8 rows a group, then
-// 16, 64, 256 on the average): 108, 97, 112, 243, 118 (tiles of 128: 109, 109, 110,
-// 118, 275; of 256: 118, 118, 118, 125, 228); one group of one row: 10.8, 12.8,
-// 13.5, 15.7, 31, 39.
-enum Kernel { ROWS16_NT2, ROWS16, ROWS32, ROWS64, TILES128, TILES256 };
+// Measured, in that order: 32 groups of 8 rows on the average, N = 4096, K = 7168:
+// 102, 93, 95, 136, 109, 118; of 64 rows: -, 361, 252, 243, 118, 125; of 256 rows: -,
+// 1262, 808, 652, 275, 228.  One group of 64 rows, N = 512, K = 7168: 10.9, 14.2,
+// 16.3, 20.1, 32, 40; of 1024 rows, N = 4096: 186, 138, 88, 66, 42, 46.
+enum Kernel { ROWS16_NARROW, ROWS16, ROWS32, ROWS64, TILES128, TILES256 };
 
 Kernel choose(const MxGemmArgs& a, int cus) {
     const double c = (double)((a.K + 511) / 512), groups = (double)(a.G < a.M_total ? a.G : a.M_total);
@@ -879,10 +922,10 @@ Kernel choose(const MxGemmArgs& a, int cus) {
         const double n = row_tiles(high) * wide, rounds = n / cus;
         return rounds <= 1.0 ? at + (2.7 + (full - 2.7) * rounds) * c : __builtin_ceil(rounds) * (at + full * c);
     };
-    const double t[6] = {rows(16, 7.0, 0.6, 1260.0), rows(16, 7.0, 1.5, 1740.0), rows(32, 7.0, 1.1, 2800.0),
-                         rows(64, 7.0, 1.2, 3500.0), tiles(128, 9.0, 3.3), tiles(256, 11.0, 4.5)};
-    int best = 0;
-    for (int i = 1; i < 6; ++i)
+    const double t[6] = {rows(16, 6.0, 0.3, 1600.0), rows(16, 6.0, 0.5, 1800.0), rows(32, 6.0, 0.65, 3000.0),
+                         rows(64, 6.0, 0.95, 3500.0), tiles(128, 9.0, 3.3), tiles(256, 11.0, 4.5)};
+    int best = a.G + a.M_total / 16 <= 65535 ? 0 : 4;    // the first four have a grid row for every row tile
+    for (int i = best + 1; i < 6; ++i)
         if (t[i] < t[best]) best = i;
     return (Kernel)best;
 }
@@ -894,10 +937,10 @@ hipError_t launch_epi(const MxGemmArgs& a, hipStream_t st) {
     const hipError_t e = cu_count(cus);
     if (e != hipSuccess) return e;
     switch (choose(a, cus)) {
-        case ROWS16_NT2: return launch_rows<EPI, 1, FEW, 2>(a, st);
-        case ROWS16: return launch_rows<EPI, 1, 4, 1>(a, st);
-        case ROWS32: return launch_rows<EPI, 2, 4, 1>(a, st);
-        case ROWS64: return launch_rows<EPI, 4, 4, 1>(a, st);
+        case ROWS16_NARROW: return launch_rows<EPI, 1, FEW>(a, st);
+        case ROWS16: return launch_rows<EPI, 1, 4>(a, st);
+        case ROWS32: return launch_rows<EPI, 2, 4>(a, st);
+        case ROWS64: return launch_rows<EPI, 4, 4>(a, st);
         case TILES128: return launch_tiles<EPI, 128>(a, cus, st);
         default: return launch_tiles<EPI, 256>(a, cus, st);
     }
