@@ -443,12 +443,14 @@ hipError_t launch_rows(const MxGemmArgs& a, hipStream_t st) {
 
 // ---------------------------------------------------------------- many rows to a group
 //
-// Block tile BM (256 or 128) x 256, one block of four waves to a CU, a wave has
-// BM/2 x 128 of it in 32 x 32 tiles (32x32x64 scaled instructions, which reach
-// a higher rate than 16x16x128 on this card's power: 6.7 against 6.3 PFLOP/s
-// from registers with random codes).  The accumulators fill the 256
-// accumulation registers of a wave, so one operand byte read from LDS serves
-// 128 multiplications and LDS is read at half its rate.
+// Block tile 256 x 256, one block of four waves to a CU, a wave has 128 x 128 of it
+// in 32 x 32 tiles (32x32x64 scaled instructions, which reach a higher rate than
+// 16x16x128 on this card's power: 6.7 against 6.3 PFLOP/s from registers with
+// random codes).  The accumulators fill the 256 accumulation registers of a wave,
+// so one operand byte read from LDS serves 128 multiplications and LDS is read at a
+// quarter of its rate.  Half tiles, 128 x 256, take the groups of up to 128 rows
+// and, where that ends sooner, the tiles of a last round that would not fill the CUs
+// (8192 x 7168 x 16384: 528 us, 541 with whole tiles alone).
 //
 // Stages of 128 values of K (64-byte rows) go from memory to LDS by DMA through a
 // ring of four, sent for three stages ahead.  The scales of a chunk of four stages
@@ -546,50 +548,28 @@ __device__ __forceinline__ int tile_row(int wn, int t) {
     return SWIGLU ? wn * 64 + (t & 1) * 32 + (t >> 1) * 128 : wn * 128 + t * 32;
 }
 
+// Row tiles of all groups, in LDS: the number of tiles of 256 and of half tiles
+// before each group, and each group's first row (and the last one's end).
+struct TileLists {
+    int full[1025], half[1025], rows[1025];
+    int found;
+};
+
+// The tiles t, t + t_step, .. < t_end of the list of height BM (256 or 128).
 template <int EPI, int BM, bool KA>
-__global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
+__device__ __forceinline__ void run_tiles(const MxGemmArgs& p, TileLists& lists, int t, int t_end, int t_step) {
     constexpr bool SWIGLU = EPI == MOE_MX_SWIGLU_BF16 || EPI == MOE_MX_SWIGLU_QUANT;
     constexpr int MT = BM / 64;                          // 32-row tiles of a wave
     constexpr int A_DMA = BM / 64, B_DMA = TN / 64;      // 1 KiB (16 rows) DMAs of a wave per stage
     constexpr int ND = A_DMA + B_DMA, NSC = KA ? 2 : 4;  // vector loads of a stage, and of a chunk's scales
     constexpr int CHUNK_M = 2048 / BM;                   // row tiles that go through the columns together
-    __shared__ int start[1025], rows[1025];              // first row tile and first row of each group
-    __shared__ int found;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
     const int lr = lane & 31, kb = lane >> 5;
-    const int total = (int)p.M_total;
     const int nblk = p.K / 32, nchunk = (nblk + 15) / 16;
-    const uint32_t rb = (uint32_t)p.K / 2;
-
-    // Row tiles before each group, four groups a thread.
-    {
-        int n[4], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int g = tid * 4 + i;
-            const int2 r = rows_of(p, g, total);
-            n[i] = (r.y + BM - 1) / BM;
-            if (g < p.G) rows[g] = r.x;
-            if (g == p.G - 1) rows[p.G] = r.x + r.y;
-            sum += n[i];
-        }
-        int at = scan_threads(sum, reinterpret_cast<int*>(g_s0));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            start[tid * 4 + i] = at;
-            at += n[i];
-        }
-        if (tid == 255) start[1024] = at;
-        __syncthreads();
-    }
     const int n_tiles = (p.N + TN - 1) / TN;
-    const int tiles = start[p.G] * n_tiles;              // the C ABI keeps it under 2^31
-    // Blocks go to the eight XCDs in turn; each XCD has one stretch of the tiles
-    // and its blocks take neighbouring ones, which share operands in its L2.
-    const int share = (tiles + 7) / 8, xcd = (int)blockIdx.x & 7, t_step = (int)gridDim.x >> 3;
-    const int t_end = min(tiles, (xcd + 1) * share);
-    int t = xcd * share + ((int)blockIdx.x >> 3);
+    const uint32_t rb = (uint32_t)p.K / 2;
+    const int* start = BM == 256 ? lists.full : lists.half;
 
     // Scale descriptors end on a word.  A group's scales may start off one: the
     // descriptor then starts at the word before and the offsets begin at the rest.
@@ -611,18 +591,20 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int g = tid * 4 + i;
-            if (start[g] <= rt && rt < start[g + 1]) found = g;
+            if (start[g] <= rt && rt < start[g + 1]) lists.found = g;
         }
         lds_barrier();
         Tile v;
-        v.g = __builtin_amdgcn_readfirstlane(found);
+        v.g = __builtin_amdgcn_readfirstlane(lists.found);
         const int first = __builtin_amdgcn_readfirstlane(start[v.g]);
         const int n = __builtin_amdgcn_readfirstlane(start[v.g + 1]) - first;    // the group's row tiles
         const int inside = at - first * n_tiles;
         const int chunk = inside / (CHUNK_M * n_tiles), left = inside - chunk * CHUNK_M * n_tiles;
         const int cm = min(CHUNK_M, n - chunk * CHUNK_M);
-        v.hi = __builtin_amdgcn_readfirstlane(rows[v.g + 1]);
-        v.m0 = __builtin_amdgcn_readfirstlane(rows[v.g]) + (chunk * CHUNK_M + left % cm) * BM;
+        v.hi = __builtin_amdgcn_readfirstlane(lists.rows[v.g + 1]);
+        v.m0 = __builtin_amdgcn_readfirstlane(lists.rows[v.g]) + (chunk * CHUNK_M + left % cm) * BM;
+        if constexpr (BM == 128)                         // the half tiles come after the whole ones
+            v.m0 += __builtin_amdgcn_readfirstlane(lists.full[v.g + 1] - lists.full[v.g]) * 256;
         v.n0 = left / cm * TN;
         return v;
     };
@@ -678,7 +660,7 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
     auto write_scales = [&](int c) {
         char* to = g_s0 + SCALE_AT + (c & 1) * SCALE_BYTES + tid * 16;
         const v4u a = deal_scales(ca.bytes(aso, c, nblk)), b = deal_scales(cb.bytes(bso, c, nblk));
-        if (BM == 256 || tid < BM) lds_put(to, a);
+        lds_put(to, a);                                  // of a half tile, 128 rows of zeros that nothing reads
         lds_put(to + 256 * 16, b);
     };
     uint32_t slot[2];                                    // the lane's chunk of step j in its row
@@ -869,6 +851,96 @@ __global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
     }
 }
 
+template <int EPI, bool KA>
+__global__ __launch_bounds__(256, 1) void mxgemm_tile_kernel(MxGemmArgs p) {
+    __shared__ TileLists lists;
+    const int tid = threadIdx.x, total = (int)p.M_total;
+    const int nchunk = (p.K / 32 + 15) / 16, n_tiles = (p.N + TN - 1) / TN;
+    const int xcd = (int)blockIdx.x & 7, t_step = (int)gridDim.x >> 3, block = (int)blockIdx.x >> 3;
+    int n_full, n_half;
+    {
+        // Four groups a thread: a half tile for up to 128 rows, else whole tiles.  (A
+        // half tile for a larger group's rest would run after the whole tiles and read
+        // B again: 245 us against 235 at 32 groups of 256 rows on the average.)
+        int nf[4], nh[4], sum_f = 0, sum_h = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int g = tid * 4 + i;
+            const int2 r = rows_of(p, g, total);
+            nf[i] = r.y > 128 ? (r.y + 255) / 256 : 0;
+            nh[i] = r.y > 0 && r.y <= 128;
+            if (g < p.G) lists.rows[g] = r.x;
+            if (g == p.G - 1) lists.rows[p.G] = r.x + r.y;
+            sum_f += nf[i];
+            sum_h += nh[i];
+        }
+        int* scratch = reinterpret_cast<int*>(g_s0);
+        int at_f = scan_threads(sum_f, scratch), at_h = scan_threads(sum_h, scratch + 4);
+        if (tid == 255) {
+            scratch[8] = at_f + sum_f;
+            scratch[9] = at_h + sum_h;
+        }
+        __syncthreads();
+        n_full = __builtin_amdgcn_readfirstlane(scratch[8]);
+        n_half = __builtin_amdgcn_readfirstlane(scratch[9]);
+        // How many whole row tiles, the last ones of the list, to make half tiles of:
+        // thread x tries x, and the x whose busiest block is done first is taken.  A
+        // tile of c chunks takes 11 + 4.5 c us, a half tile 9 + 3.6 c.
+        unsigned long long best = ~0ull;
+        if (tid <= n_full) {
+            const int f = ((n_full - tid) * n_tiles + 7) / 8, all = f + ((n_half + 2 * tid) * n_tiles + 7) / 8;
+            const int at[6] = {0, f % t_step - 1, f % t_step, all % t_step - 1, all % t_step, t_step - 1};
+            int64_t most = 0;
+#pragma unroll
+            for (int i = 0; i < 6; ++i) {                // the load changes at these blocks only
+                const int j = max(at[i], 0);
+                const int whole = f > j ? (f - 1 - j) / t_step + 1 : 0, tiles = all > j ? (all - 1 - j) / t_step + 1 : 0;
+                most = max(most, (int64_t)whole * (110 + 45 * nchunk) + (int64_t)(tiles - whole) * (90 + 36 * nchunk));
+            }
+            best = (unsigned long long)most << 8 | (unsigned)tid;
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const unsigned long long b = __shfl_xor(best, o, 64);
+            best = b < best ? b : best;
+        }
+        auto* least = reinterpret_cast<unsigned long long*>(scratch + 16);
+        if ((tid & 63) == 0) least[tid >> 6] = best;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) best = least[i] < best ? least[i] : best;
+        const int split = __builtin_amdgcn_readfirstlane((int)(best & 255u));
+        n_full -= split;
+        n_half += 2 * split;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lists.full[tid * 4 + i] = min(at_f, n_full);
+            lists.half[tid * 4 + i] = at_h + 2 * max(at_f - n_full, 0);
+            at_f += nf[i];
+            at_h += nh[i];
+        }
+        if (tid == 255) {
+            lists.full[1024] = n_full;
+            lists.half[1024] = n_half;
+        }
+        __syncthreads();
+    }
+    // Blocks go to the eight XCDs in turn; each XCD has one stretch of each list and
+    // its blocks take neighbouring tiles, which share operands in its L2.  The whole
+    // tiles are dealt first and the half tiles go on where those end.
+    auto stretch = [&](int n, int& first, int& count) {
+        const int share = (n + 7) / 8;
+        first = xcd * share;
+        count = max(min(share, n - first), 0);
+    };
+    int f0, nf, h0, nh;
+    stretch(n_full * n_tiles, f0, nf);                   // the C ABI keeps these under 2^31
+    stretch(n_half * n_tiles, h0, nh);
+    run_tiles<EPI, 256, KA>(p, lists, f0 + block, f0 + nf, t_step);
+    const int behind = block < nf ? (nf - block + t_step - 1) / t_step * t_step + block - nf : block - nf;
+    run_tiles<EPI, 128, KA>(p, lists, h0 + behind, h0 + nh, t_step);
+}
+
 // CUs of the current device, asked for once per device (any thread may call; a
 // lost race asks again).
 hipError_t cu_count(int& cus) {
@@ -883,13 +955,13 @@ hipError_t cu_count(int& cus) {
     return e;
 }
 
-template <int EPI, int BM>
+template <int EPI>
 hipError_t launch_tiles(const MxGemmArgs& a, int cus, hipStream_t st) {
-    const int64_t most = ((a.M_total + BM - 1) / BM + a.G) * ((a.N + TN - 1) / TN);
+    const int64_t most = ((a.M_total + 127) / 128 + a.G) * ((a.N + TN - 1) / TN);
     const int64_t want = most < cus ? most : cus;
     const dim3 grid((unsigned)((want + 7) / 8 * 8));      // the same count on every XCD
-    if (a.K % 128 == 0) hipLaunchKernelGGL((mxgemm_tile_kernel<EPI, BM, true>), grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((mxgemm_tile_kernel<EPI, BM, false>), grid, dim3(256), 0, st, a);
+    if (a.K % 128 == 0) hipLaunchKernelGGL((mxgemm_tile_kernel<EPI, true>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((mxgemm_tile_kernel<EPI, false>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
@@ -901,13 +973,13 @@ hipError_t launch_tiles(const MxGemmArgs& a, int cus, hipStream_t st) {
 //   16 rows, 4 column tiles:  6 + 0.5 c + units / 1800
 //   32 rows, 4 column tiles:  6 + 0.65 c + units / 3000
 //   64 rows, 4 column tiles:  6 + 0.95 c + units / 3500
-//   tiles of 128 x 256, a round of the CUs:  9 + 2.7 c, up to 9 + 3.3 c when full
-//   tiles of 256 x 256:                     11 + 2.7 c, up to 11 + 4.5 c
+//   tiles of 256 x 256, a round of the CUs: 11 + 2.7 c, up to 11 + 4.5 c when full
+//   half tiles:                              9 + 2.7 c, up to 9 + 3.6 c
 // Measured, in that order: 32 groups of 8 rows on the average, N = 4096, K = 7168:
 // 102, 93, 95, 136, 109, 118; of 64 rows: -, 361, 252, 243, 118, 125; of 256 rows: -,
 // 1262, 808, 652, 275, 228.  One group of 64 rows, N = 512, K = 7168: 10.9, 14.2,
 // 16.3, 20.1, 32, 40; of 1024 rows, N = 4096: 186, 138, 88, 66, 42, 46.
-enum Kernel { ROWS16_NARROW, ROWS16, ROWS32, ROWS64, TILES128, TILES256 };
+enum Kernel { ROWS16_NARROW, ROWS16, ROWS32, ROWS64, TILES };
 
 Kernel choose(const MxGemmArgs& a, int cus) {
     const double c = (double)((a.K + 511) / 512), groups = (double)(a.G < a.M_total ? a.G : a.M_total);
@@ -922,10 +994,11 @@ Kernel choose(const MxGemmArgs& a, int cus) {
         const double n = row_tiles(high) * wide, rounds = n / cus;
         return rounds <= 1.0 ? at + (2.7 + (full - 2.7) * rounds) * c : __builtin_ceil(rounds) * (at + full * c);
     };
-    const double t[6] = {rows(16, 6.0, 0.3, 1600.0), rows(16, 6.0, 0.5, 1800.0), rows(32, 6.0, 0.65, 3000.0),
-                         rows(64, 6.0, 0.95, 3500.0), tiles(128, 9.0, 3.3), tiles(256, 11.0, 4.5)};
+    const double halves = tiles(128, 9.0, 3.6), wholes = tiles(256, 11.0, 4.5);
+    const double t[5] = {rows(16, 6.0, 0.3, 1600.0), rows(16, 6.0, 0.5, 1800.0), rows(32, 6.0, 0.65, 3000.0),
+                         rows(64, 6.0, 0.95, 3500.0), halves < wholes ? halves : wholes};
     int best = a.G + a.M_total / 16 <= 65535 ? 0 : 4;    // the first four have a grid row for every row tile
-    for (int i = best + 1; i < 6; ++i)
+    for (int i = best + 1; i < 5; ++i)
         if (t[i] < t[best]) best = i;
     return (Kernel)best;
 }
@@ -941,8 +1014,7 @@ hipError_t launch_epi(const MxGemmArgs& a, hipStream_t st) {
         case ROWS16: return launch_rows<EPI, 1, 4>(a, st);
         case ROWS32: return launch_rows<EPI, 2, 4>(a, st);
         case ROWS64: return launch_rows<EPI, 4, 4>(a, st);
-        case TILES128: return launch_tiles<EPI, 128>(a, cus, st);
-        default: return launch_tiles<EPI, 256>(a, cus, st);
+        default: return launch_tiles<EPI>(a, cus, st);
     }
 }
 
