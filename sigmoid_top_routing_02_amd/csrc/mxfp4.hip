@@ -10,8 +10,8 @@
 // ties to even, by gfx950's conversion, which saturates at 6 and keeps signs.
 //
 // All three stream HBM and write what they write once: every access of a wave is
-// one contiguous run, at most 16 bytes a lane, and outputs past what L2 holds are
-// stored past it (stored_past_l2 below).
+// one contiguous run, at most 16 bytes a lane, and large outputs are stored
+// non-temporally (streamed).
 #include "device_math.h"
 #include "kernels.h"
 #include "streaming.h"
@@ -174,7 +174,7 @@ hipError_t launch_mxfp4_quant(const void* x, int in_is_f32, int64_t n_blocks, ui
         hipLaunchKernelGGL(kernel, dim3(grid_for(lanes, per)), dim3(256), 0, st, x, lanes, qw, scale);
         return hipGetLastError();
     };
-    if (stored_past_l2(n_blocks * 17)) return in_is_f32 ? go(mxfp4_quant_kernel<true, true>, 1) : go(mxfp4_quant_kernel<false, true>, 2);
+    if (streamed(n_blocks * 17)) return in_is_f32 ? go(mxfp4_quant_kernel<true, true>, 1) : go(mxfp4_quant_kernel<false, true>, 2);
     return in_is_f32 ? go(mxfp4_quant_kernel<true, false>, 1) : go(mxfp4_quant_kernel<false, false>, 2);
 }
 
@@ -186,7 +186,7 @@ hipError_t launch_mxfp4_dequant(const uint8_t* q, const uint8_t* scale, int64_t 
                            static_cast<v4u*>(out));
         return hipGetLastError();
     };
-    if (stored_past_l2(lanes * 16)) return out_is_f32 ? go(mxfp4_dequant_kernel<true, true>) : go(mxfp4_dequant_kernel<false, true>);
+    if (streamed(lanes * 16)) return out_is_f32 ? go(mxfp4_dequant_kernel<true, true>) : go(mxfp4_dequant_kernel<false, true>);
     return out_is_f32 ? go(mxfp4_dequant_kernel<true, false>) : go(mxfp4_dequant_kernel<false, false>);
 }
 
@@ -198,7 +198,7 @@ hipError_t launch_fp8_dequant_1x128(const uint8_t* q, const float* scale, int64_
                            static_cast<v4u*>(out));
         return hipGetLastError();
     };
-    if (stored_past_l2(lanes * 16)) return out_is_f32 ? go(fp8_dequant_1x128_kernel<true, true>) : go(fp8_dequant_1x128_kernel<false, true>);
+    if (streamed(lanes * 16)) return out_is_f32 ? go(fp8_dequant_1x128_kernel<true, true>) : go(fp8_dequant_1x128_kernel<false, true>);
     return out_is_f32 ? go(fp8_dequant_1x128_kernel<true, false>) : go(fp8_dequant_1x128_kernel<false, false>);
 }
 

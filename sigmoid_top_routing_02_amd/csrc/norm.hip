@@ -113,8 +113,15 @@ __device__ __forceinline__ float row_sum(float s, float (*part)[16], int flip) {
     return s;
 }
 
-// A block is one row at a time (WAVE_ROW: each of its four waves is one).
-template <int NV, bool VEC, bool WAVE_ROW, bool NT>
+// A block is one row (WAVE_ROW: each of its four waves is one); only a grid that
+// would pass the largest one makes it take more.  16384 rows of 7168 bf16 values
+// with residual: 196 us with the FP8 copy (5.4 TB/s), 164 us without (5.75 TB/s),
+// above the 4.9 TB/s of a plain copy, since the outputs are stored non-temporally
+// and leave the caches to the inputs (211 us with plain stores; 256 rows 6.0 us
+// against 6.8, and with a kernel that reads y right after 9.1 against 9.8).  Rows
+// in turn on 2048 resident blocks lost to one block a row, 234 us: the next row's
+// loads then wait for the last one's reduction.
+template <int NV, bool VEC, bool WAVE_ROW>
 __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddRmsnormArgs a) {
     __shared__ float part[2][16];
     const int t = WAVE_ROW ? (int)threadIdx.x & 63 : (int)threadIdx.x;
@@ -141,7 +148,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddR
                 for (int j = 0; j < 8; ++j) h[v][j] += r[v][j];
             if (a.h) {
 #pragma unroll
-                for (int v = 0; v < NV; ++v) store8<VEC, NT>(a.h, a.res_f32, off, v, t, tpr, d, h[v]);
+                for (int v = 0; v < NV; ++v) store8<VEC, true>(a.h, a.res_f32, off, v, t, tpr, d, h[v]);
             }
         }
         float s = 0.0f;
@@ -157,7 +164,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddR
             float y[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) y[j] = h[v][j] * rstd * w[v][j];
-            if (a.y) store8<VEC, NT>(a.y, false, off, v, t, tpr, d, y);
+            if (a.y) store8<VEC, true>(a.y, false, off, v, t, tpr, d, y);
             if constexpr (VEC) {
                 if (a.q) {                            // d % 128 == 0: 16 lanes are one tile, all in the row or none
                     const int c = col_of<VEC>(v, 0, t, tpr);
@@ -181,7 +188,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddR
                     float inv, sc;
                     tile_scale(amax, inv, sc);
                     if (c < d) {
-                        put<NT>(reinterpret_cast<v2u*>(a.q + off + c),
+                        put<true>(reinterpret_cast<v2u*>(a.q + off + c),
                                 v2u{e4m3_encode4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
                                     e4m3_encode4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv)});
                         if ((t & 15) == 0) a.scale[row * (d / 128) + c / 128] = sc;
@@ -193,7 +200,8 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddR
 }
 
 // As the forward; each block keeps the sum of dy * xh of its rows in registers and
-// leaves it as one row of `part` at the end.
+// leaves it as one row of `part` at the end.  8192 rows of 7168 bf16 values with dh:
+// 98 us (4.8 TB/s, the rate of a plain copy) and 4 us for dw_reduce_kernel.
 template <int NV, bool VEC, bool WAVE_ROW, bool NT>
 __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_backward_kernel(AddRmsnormBackwardArgs a) {
     __shared__ float part[2][16];
@@ -266,7 +274,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_backward_ke
 }
 
 // dw[c] = sum of the partial rows: 16 threads take every 16th row of a column,
-// eight loads at a time, then their sums are added in order.
+// eight loads at a time, then their sums are added in order (512 rows of 7168: 4 us).
 __global__ __launch_bounds__(256) void dw_reduce_kernel(const float* __restrict__ part, int rows, int d,
                                                         float* __restrict__ dw) {
     __shared__ float sum[16][17];
@@ -290,27 +298,37 @@ __global__ __launch_bounds__(256) void dw_reduce_kernel(const float* __restrict_
     }
 }
 
-// Rows up to 1024 wide are one wave each, four to a block; a wider one is a
-// block of as many waves as hold it at 16 values a thread.
-bool wave_row(int d) { return d <= 1024; }
+// A row of up to `narrow` values is one wave, four to a block; a wider one is a
+// block of as many waves as hold it at 16 values a thread.  In the forward four
+// rows a block pay where half a wave's registers hold a row (16384 rows of 128
+// values 6.1 us against 7.0, 512 values 6.4 against 7.2, 1024 values 12.3 against
+// 11.0).  In the backward a block keeps one partial row of dw, and its four rows at
+// a time are worth more (16384 rows of 128 values 12.2 us against 38.8, 1024
+// values 24.0 against 66.3).
+constexpr int FORWARD_NARROW = 512, BACKWARD_NARROW = 1024;
 
-template <typename Launch>
+template <int NARROW, typename Launch>
 void dispatch_shape(int d, Launch&& go) {
     const bool vec = d % 8 == 0;
-    if (wave_row(d)) {
-        if (d <= 512) vec ? go.template operator()<1, true, true>() : go.template operator()<1, false, true>();
-        else vec ? go.template operator()<2, true, true>() : go.template operator()<2, false, true>();
-    } else {
-        vec ? go.template operator()<2, true, false>() : go.template operator()<2, false, false>();
+    if (d <= 512) {
+        vec ? go.template operator()<1, true, true>() : go.template operator()<1, false, true>();
+        return;
     }
+    if constexpr (NARROW > 512) {
+        if (d <= NARROW) {
+            vec ? go.template operator()<2, true, true>() : go.template operator()<2, false, true>();
+            return;
+        }
+    }
+    vec ? go.template operator()<2, true, false>() : go.template operator()<2, false, false>();
 }
 
-int row_threads(int d) { return wave_row(d) ? 256 : (d + 1023) / 1024 * 64; }
+int row_threads(int d, int narrow) { return d <= narrow ? 256 : (d + 1023) / 1024 * 64; }
 
 // Blocks of the backward: a few per CU, so that the partial rows stay small
 // beside the data; a function of the sizes alone, so dw's bits are too.
 int backward_blocks(int64_t T, int d) {
-    const int64_t per = wave_row(d) ? 4 : 1;
+    const int64_t per = d <= BACKWARD_NARROW ? 4 : 1;
     const int64_t b = (T + per - 1) / per;
     return (int)(b < 512 ? b : 512);
 }
@@ -323,11 +341,8 @@ struct ForwardLaunch {
         const int64_t per = WAVE_ROW ? 4 : 1;
         int64_t blocks = (a.T + per - 1) / per;
         if (blocks > 0x7FFFFFFF) blocks = 0x7FFFFFFF;
-        const dim3 grid((unsigned)blocks), block(row_threads(a.d));
-        if (stored_past_l2(a.T * a.d * 2))
-            hipLaunchKernelGGL((add_rmsnorm_kernel<NV, VEC, WAVE_ROW, true>), grid, block, 0, st, a);
-        else
-            hipLaunchKernelGGL((add_rmsnorm_kernel<NV, VEC, WAVE_ROW, false>), grid, block, 0, st, a);
+        const dim3 grid((unsigned)blocks), block(row_threads(a.d, FORWARD_NARROW));
+        hipLaunchKernelGGL((add_rmsnorm_kernel<NV, VEC, WAVE_ROW>), grid, block, 0, st, a);
     }
 };
 
@@ -336,8 +351,8 @@ struct BackwardLaunch {
     hipStream_t st;
     template <int NV, bool VEC, bool WAVE_ROW>
     void operator()() const {
-        const dim3 grid(backward_blocks(a.T, a.d)), block(row_threads(a.d));
-        if (stored_past_l2(a.T * a.d * 2))
+        const dim3 grid(backward_blocks(a.T, a.d)), block(row_threads(a.d, BACKWARD_NARROW));
+        if (streamed(a.T * a.d * 2))
             hipLaunchKernelGGL((add_rmsnorm_backward_kernel<NV, VEC, WAVE_ROW, true>), grid, block, 0, st, a);
         else
             hipLaunchKernelGGL((add_rmsnorm_backward_kernel<NV, VEC, WAVE_ROW, false>), grid, block, 0, st, a);
@@ -347,7 +362,7 @@ struct BackwardLaunch {
 }  // namespace
 
 hipError_t launch_add_rmsnorm(const AddRmsnormArgs& a, hipStream_t st) {
-    dispatch_shape(a.d, ForwardLaunch{a, st});
+    dispatch_shape<FORWARD_NARROW>(a.d, ForwardLaunch{a, st});
     return hipGetLastError();
 }
 
@@ -358,7 +373,7 @@ size_t add_rmsnorm_backward_ws_bytes(int64_t T, int d) {
 hipError_t launch_add_rmsnorm_backward(const AddRmsnormBackwardArgs& a, float* dw, hipStream_t st) {
     int rows = 0;                                   // no rows: the reduction alone, which writes zeros
     if (a.T > 0) {
-        dispatch_shape(a.d, BackwardLaunch{a, st});
+        dispatch_shape<BACKWARD_NARROW>(a.d, BackwardLaunch{a, st});
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         rows = backward_blocks(a.T, a.d);
