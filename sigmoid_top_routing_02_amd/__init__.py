@@ -602,6 +602,14 @@ def _in(t, dtype, shape, name, dev):
     return t.data_ptr()
 
 
+def _out(t, like, dtype, shape, name, dev):
+    """An output of this type and shape, allocated beside `like` where t is None, and its address."""
+    if t is None:
+        t = like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    return t, _in(t, dtype, shape, name, dev)
+
+
 def _rows(t, name):
     """(rows, cols, MOE dtype, GPU) of a bf16 or FP32 matrix on the current GPU."""
     if t.dim() != 2:
@@ -643,27 +651,18 @@ def moe_add_rmsnorm(x, weight, eps, residual=None, quant=False, h_out=None, y=No
     if residual is not None:
         rd = _dt(residual, "residual")
         pr = _in(residual, residual.dtype, shape, "residual", dev)
-        if h_out is None:
-            h_out = torch.empty_like(residual)
-        ph = _in(h_out, residual.dtype, shape, "h_out", dev)
+        h_out, ph = _out(h_out, x, residual.dtype, shape, "h_out", dev)
     elif h_out is not None:
         raise MoEError("moe_add_rmsnorm: h_out without a residual")
-    if y is None:
-        y = x.new_empty(shape, dtype=torch.bfloat16)
-    if rstd is None:
-        rstd = x.new_empty((T,), dtype=torch.float32)
+    y, py = _out(y, x, torch.bfloat16, shape, "y", dev)
+    rstd, prs = _out(rstd, x, torch.float32, (T,), "rstd", dev)
     if quant:
-        if q is None:
-            q = x.new_empty(shape, dtype=torch.uint8)
-        if scale is None:
-            scale = x.new_empty((T, d // 128), dtype=torch.float32)
-        pq = _in(q, torch.uint8, shape, "q", dev)
-        ps = _in(scale, torch.float32, (T, d // 128), "scale", dev)
+        q, pq = _out(q, x, torch.uint8, shape, "q", dev)
+        scale, ps = _out(scale, x, torch.float32, (T, d // 128), "scale", dev)
     elif q is not None or scale is not None:
         raise MoEError("moe_add_rmsnorm: q or scale without quant")
     L = _lib or load_library()
-    st = L.moe_add_rmsnorm(px, xd, pr, rd, pw, wd, T, d, eps, ph, _in(y, torch.bfloat16, shape, "y", dev), pq, ps,
-                           _in(rstd, torch.float32, (T,), "rstd", dev), _raw_stream(dev))
+    st = L.moe_add_rmsnorm(px, xd, pr, rd, pw, wd, T, d, eps, ph, py, pq, ps, prs, _raw_stream(dev))
     if st:
         _check(st, "moe_add_rmsnorm")
     return RMSNorm(y, h_out, rstd, q, scale)
@@ -677,20 +676,21 @@ def moe_add_rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, dw=None, dx_
     shape = dy.shape
     if dx_dtype is None:
         dx_dtype = dh.dtype if dh is not None else dx.dtype if dx is not None else dy.dtype
-    if dx is None:
-        dx = dy.new_empty(shape, dtype=dx_dtype)
-    if dw is None:
-        dw = dy.new_empty((d,), dtype=torch.float32)
+    dx, pdx = _out(dx, dy, dx_dtype, shape, "dx", dev)
+    dw, pdw = _out(dw, dy, torch.float32, (d,), "dw", dev)
     L = _lib or load_library()
     if ws is None:
-        ws = dy.new_empty((max(L.moe_add_rmsnorm_backward_workspace_bytes(T, d), 16),), dtype=torch.uint8)
+        ws_bytes = max(L.moe_add_rmsnorm_backward_workspace_bytes(T, d), 16)
+        ws = dy.new_empty((ws_bytes,), dtype=torch.uint8)
+        pws = ws.data_ptr()
+    else:
+        ws_bytes, pws = ws.numel() * ws.element_size(), _in(ws, ws.dtype, ws.shape, "ws", dev)
     pdh = None if dh is None else _in(dh, dx_dtype, shape, "dh", dev)
     st = L.moe_add_rmsnorm_backward(
         _in(dy, dy.dtype, shape, "dy", dev), yd, _in(h, h.dtype, shape, "h", dev), _dt(h, "h"),
         _in(weight, weight.dtype, (d,), "weight", dev), _dt(weight, "weight"),
-        _in(rstd, torch.float32, (T,), "rstd", dev), pdh, T, d, _in(dx, dx_dtype, shape, "dx", dev), _dt(dx, "dx"),
-        _in(dw, torch.float32, (d,), "dw", dev), _in(ws, ws.dtype, ws.shape, "ws", dev),
-        ws.numel() * ws.element_size(), _raw_stream(dev))
+        _in(rstd, torch.float32, (T,), "rstd", dev), pdh, T, d, pdx, _dt(dx, "dx"), pdw, pws, ws_bytes,
+        _raw_stream(dev))
     if st:
         _check(st, "moe_add_rmsnorm_backward")
     return dx, dw
@@ -701,14 +701,10 @@ def mxfp4_quant_1x32(x, q=None, scale=None):
     """x bf16/f32 [rows, cols] -> (q uint8 [rows, cols/2], two E2M1 codes to a byte, the even column in
     the low half; scale uint8 [rows, cols/32], E8M0)."""
     rows, cols, dt, dev = _rows(x, "x")
-    if q is None:
-        q = x.new_empty((rows, cols // 2), dtype=torch.uint8)
-    if scale is None:
-        scale = x.new_empty((rows, cols // 32), dtype=torch.uint8)
+    q, pq = _out(q, x, torch.uint8, (rows, cols // 2), "q", dev)
+    scale, ps = _out(scale, x, torch.uint8, (rows, cols // 32), "scale", dev)
     L = _lib or load_library()
-    st = L.mxfp4_quant_1x32(_in(x, x.dtype, x.shape, "x", dev), dt, rows, cols,
-                            _in(q, torch.uint8, (rows, cols // 2), "q", dev),
-                            _in(scale, torch.uint8, (rows, cols // 32), "scale", dev), _raw_stream(dev))
+    st = L.mxfp4_quant_1x32(_in(x, x.dtype, x.shape, "x", dev), dt, rows, cols, pq, ps, _raw_stream(dev))
     if st:
         _check(st, "mxfp4_quant_1x32")
     return q, scale
@@ -720,11 +716,10 @@ def _dequant(name, q, scale, cols, scale_dtype, per, dtype, out):
     dev = _current(q, "q")
     if dtype not in _DTYPES:
         raise MoEError(f"{name}: dtype {dtype}, expected torch.bfloat16 or torch.float32")
-    if out is None:
-        out = q.new_empty((rows, cols), dtype=dtype)
+    out, po = _out(out, q, dtype, (rows, cols), "out", dev)
     L = _lib or load_library()
     st = getattr(L, name)(_in(q, torch.uint8, q.shape, "q", dev), _in(scale, scale_dtype, (rows, cols // per), "scale", dev),
-                          rows, cols, _in(out, dtype, (rows, cols), "out", dev), _DTYPES[dtype], _raw_stream(dev))
+                          rows, cols, po, _DTYPES[dtype], _raw_stream(dev))
     if st:
         _check(st, name)
     return out
@@ -765,20 +760,14 @@ def grouped_gemm_mxfp4(a_q, a_scale, group_offset, M_total, b_q, b_scale, epi=MO
         raise MoEError("group_offset must be int32 with G+1 entries")
     po = pq = ps = None
     if epi == MOE_MX_SWIGLU_QUANT:
-        if out_q is None:
-            out_q = a_q.new_empty((M_total, N // 4))
-        if out_scale is None:
-            out_scale = a_q.new_empty((M_total, N // 64))
-        pq = _in(out_q, torch.uint8, (M_total, N // 4), "out_q", dev)
-        ps = _in(out_scale, torch.uint8, (M_total, N // 64), "out_scale", dev)
+        out_q, pq = _out(out_q, b_q, torch.uint8, (M_total, N // 4), "out_q", dev)
+        out_scale, ps = _out(out_scale, b_q, torch.uint8, (M_total, N // 64), "out_scale", dev)
         if out is not None:
             raise MoEError("grouped_gemm_mxfp4: this epilogue writes out_q and out_scale, not out")
     else:
         want = torch.float32 if epi == MOE_MX_STORE_F32 else torch.bfloat16
         shape = (M_total, N // 2 if epi == MOE_MX_SWIGLU_BF16 else N)
-        if out is None:
-            out = a_q.new_empty(shape, dtype=want)
-        po = _in(out, want, shape, "out", dev)
+        out, po = _out(out, b_q, want, shape, "out", dev)
         if out_q is not None or out_scale is not None:
             raise MoEError("grouped_gemm_mxfp4: this epilogue writes out, not out_q or out_scale")
     L = _lib or load_library()
