@@ -2,8 +2,9 @@
 // MXFP4 product):
 //     C[m,n] = sum_b 2^(ea[m,b] + eb[n,b]) * sum_{k in block b} a[m,k] b[n,k],
 // blocks of 32 along K, E2M1 codes, E8M0 scale bytes.  One scaled matrix
-// instruction (16x16x128 on FP4 operands) takes four blocks with their scales
-// and accumulates in FP32, so the whole of K is one chain of them.
+// instruction on FP4 operands takes four blocks of 16 rows (16x16x128, the few-row
+// kernel) or two of 32 (32x32x64, the tiles) with their scales and accumulates in
+// FP32, so the whole of K is one chain of them.
 //
 // A lane of the instruction supplies one row, 32 consecutive values of it (16
 // bytes) and one scale byte, chosen from a register at compile time.  Rows of codes
@@ -232,9 +233,10 @@ __device__ __forceinline__ int b_row(int c0, int tile) {
 // of 16 rows.  Lane l takes block 4 j + l / 16 of a chunk in its slice j, and byte
 // l / 16 of the chunk's scale word j.  A wave sends for a whole chunk of all its
 // tiles before it uses any (left to itself the compiler mixes the two, to save
-// registers: 105 us where this takes 93, at 256 rows in 32 groups, N = 4096, K =
-// 7168, 5.4 TB/s); the next chunk is left to the CU's other waves (two chunks in
-// turn in one wave: 112 us).
+// registers: 105 us where this took 93, at 256 rows in 32 groups, N = 4096, K =
+// 7168), A first and each line's two halves right after each other (89.7 us, 5.6
+// TB/s; in the compiler's order 91 to 95); the next chunk is left to the CU's other
+// waves (two chunks in turn in one wave: 112 us).
 template <bool KA>
 struct Chunk {
     v4u q[4];
@@ -249,6 +251,7 @@ struct Chunk {
         for (int j = 0; j < 4; ++j) {
             const bool in = WHOLE || c * 16 + j * 4 + kb < nblk;
             q[j] = __builtin_amdgcn_raw_buffer_load_b128(dq, in ? row_q + j * 64u : OUT, c * 256, 0);
+            FENCE();                                     // the two halves of a 128-byte line right after each other
         }
         s.load(ds, row_s, c);
     }
@@ -260,6 +263,46 @@ __device__ __forceinline__ int2 rows_of(const MxGemmArgs& p, int g, int total) {
     if (g >= p.G) return make_int2(0, 0);
     const int lo = min(max(p.group_offset[g], 0), total), hi = min(max(p.group_offset[g + 1], 0), total);
     return make_int2(lo, max(hi - lo, 0));
+}
+
+// The few-row kernel's tile of T rows for grid row y: rows m0 to `end` of group g
+// (the tile may end before), none where m0 >= end.  With a row for each group on the
+// average, grid row y < G has the first tile of group y, and row G - 1 + s the tile,
+// not the first of its group, that starts in rows s T to s T + T - 1 of all: there
+// is one at most.  With fewer rows, grid row y has the tile that starts at row y;
+// blocks of the empty groups, though they end at once, would leave the others
+// unevenly dealt to the CUs (8 rows in 8 of 32 groups, N = 4096, K = 7168: 24.1 us
+// against 27.5; in 7 of 256 groups, K = 2048: 8.0 against 11.8; but 64 rows of 256
+// groups, N = 1024, K = 2048: 15.2 against 13.6).  Every wave looks for itself.
+struct RowTile { int g, m0, end; };
+
+template <int T>
+__device__ __forceinline__ RowTile find_tile(const MxGemmArgs& p, int y) {
+    const int total = (int)p.M_total, lane = threadIdx.x & 63;
+    const bool firsts = total >= p.G;
+    if (firsts && y < p.G) {
+        const int2 r = rows_of(p, y, total);
+        return {y, r.x, r.x + r.y};
+    }
+    const int slot = firsts ? (y - p.G + 1) * T : y;
+    for (int base = 0; base < p.G; base += 256) {
+        int at[4], end[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int2 r = rows_of(p, base + i * 64 + lane, total);
+            at[i] = r.x + max((slot - r.x + T - 1) & -T, firsts ? T : 0);
+            end[i] = r.x + r.y;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t hit = __ballot(at[i] < end[i] && at[i] < slot + (firsts ? T : 1));
+            if (hit) {
+                const int l = __builtin_ctzll(hit);
+                return {base + i * 64 + l, __builtin_amdgcn_readlane(at[i], l), __builtin_amdgcn_readlane(end[i], l)};
+            }
+        }
+    }
+    return {0, 0, 0};
 }
 
 // Sum of v over the block's threads before this one (256 threads; wsum: four ints
@@ -286,37 +329,9 @@ __global__ __launch_bounds__(256) void mxgemm_rows_kernel(MxGemmArgs p) {
     __shared__ v4f red[4][MI * NT][64];
     const int lane = threadIdx.x & 63, lr = lane & 15, kb = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int total = (int)p.M_total;
-    // Grid row y < G has the first row tile of group y, the others one of the tiles
-    // after the first each, counted over the groups.
-    int g = blockIdx.y, m0 = 0;
-    if (g >= p.G) {
-        __shared__ int wsum[4], found[2];
-        const int tid = threadIdx.x, want = g - p.G;
-        int n[4], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            n[i] = max((rows_of(p, tid * 4 + i, total).y + 16 * MI - 1) / (16 * MI) - 1, 0);
-            sum += n[i];
-        }
-        if (tid == 0) found[0] = -1;
-        int at = scan_threads(sum, wsum);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (at <= want && want < at + n[i]) {
-                found[0] = tid * 4 + i;
-                found[1] = (want - at + 1) * 16 * MI;
-            }
-            at += n[i];
-        }
-        __syncthreads();
-        g = __builtin_amdgcn_readfirstlane(found[0]);
-        m0 = __builtin_amdgcn_readfirstlane(found[1]);
-        if (g < 0) return;
-    }
-    const int2 rows = rows_of(p, g, total);
-    const int hi = rows.x + rows.y;
-    m0 += rows.x;
+    const RowTile tile = find_tile<16 * MI>(p, blockIdx.y);
+    const int g = __builtin_amdgcn_readfirstlane(tile.g), m0 = __builtin_amdgcn_readfirstlane(tile.m0);
+    const int hi = __builtin_amdgcn_readfirstlane(tile.end);
     if (m0 >= hi) return;
     const int nblk = p.K / 32, nchunk = (nblk + 15) / 16;
     const uint32_t rb = (uint32_t)p.K / 2;               // bytes of a row of codes
@@ -354,9 +369,9 @@ __global__ __launch_bounds__(256) void mxgemm_rows_kernel(MxGemmArgs p) {
     auto load = [&](auto whole, int c) {
         constexpr bool W = decltype(whole)::value;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) fb[t].template load<W>(bq, bs, bro[t], bso[t], c, kb, nblk);
-#pragma unroll
         for (int i = 0; i < MI; ++i) fa[i].template load<W>(aq, as, aro[i], aso[i], c, kb, nblk);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) fb[t].template load<W>(bq, bs, bro[t], bso[t], c, kb, nblk);
         FENCE();                                         // all of them are sent for before any is used
     };
     auto multiply = [&](auto whole, int c) {
@@ -432,8 +447,8 @@ hipError_t launch_rows(const MxGemmArgs& a, hipStream_t st) {
     constexpr bool SWIGLU = EPI == MOE_MX_SWIGLU_BF16 || EPI == MOE_MX_SWIGLU_QUANT;
     constexpr int COLS = SWIGLU ? NT * 8 : NT * 16;
     const int cols = SWIGLU ? a.N / 2 : a.N;
-    // a grid row for every group's first row tile, and for all that M_total rows can make after those
-    const dim3 grid((cols + COLS - 1) / COLS, (unsigned)(a.G + a.M_total / (16 * MI)));
+    // as find_tile deals them
+    const dim3 grid((cols + COLS - 1) / COLS, (unsigned)(a.M_total < a.G ? a.M_total : a.G + a.M_total / (16 * MI)));
     if (a.K % 128 == 0)
         hipLaunchKernelGGL((mxgemm_rows_kernel<EPI, MI, NT, true>), grid, dim3(256), 0, st, a);
     else
@@ -965,38 +980,46 @@ hipError_t launch_tiles(const MxGemmArgs& a, int cus, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Which kernel.  The times below (us) were fitted to this card at K = 2048 and
-// 7168, N = 512 to 7168, 1 to 257 groups, weights from HBM and from L2; c is the
-// number of 512-value chunks of K, the work is counted in units of 16 x 16 results
-// over one chunk.  The host knows the groups' sizes on the average only.
-//   16 rows, 2 column tiles:  6 + 0.3 c + units / 1600
-//   16 rows, 4 column tiles:  6 + 0.5 c + units / 1800
-//   32 rows, 4 column tiles:  6 + 0.65 c + units / 3000
-//   64 rows, 4 column tiles:  6 + 0.95 c + units / 3500
-//   tiles of 256 x 256, a round of the CUs: 11 + 2.7 c, up to 11 + 4.5 c when full
-//   half tiles:                              9 + 2.7 c, up to 9 + 3.6 c
-// Measured, in that order: 32 groups of 8 rows on the average, N = 4096, K = 7168:
-// 102, 93, 95, 136, 109, 118; of 64 rows: -, 361, 252, 243, 118, 125; of 256 rows: -,
-// 1262, 808, 652, 275, 228.  One group of 64 rows, N = 512, K = 7168: 10.9, 14.2,
-// 16.3, 20.1, 32, 40; of 1024 rows, N = 4096: 186, 138, 88, 66, 42, 46.
+// Which kernel: the one that the times below (us) make the fastest.  They were
+// fitted to 445 measured calls, 1 to 256 groups of 1 to 4096 rows, even and skewed,
+// N = 256 to 14336, K = 1024 to 32768, weights from HBM and from the caches; the choice
+// costs 1.4 % over the fastest kernel on the average and 37 % at most.  The host
+// knows the groups' sizes on the average only.  c is the number of 512-value chunks
+// of K; a round is a block (a tile) on every CU, and a call's last round counts
+// whole while there are few of them.
+//   16 rows, 2 column tiles: 3.8 + 0.4 c a round     16 rows, 4: 4.2 + 0.69 c
+//   32 rows, 4 column tiles: 3.8 + 0.8 c             64 rows, 4: 4 + 1.19 c
+//   whole tiles: 8.8 + 1.8 c up to 8.8 + 3.3 c when the round is full
+//   half tiles:  8.8 + 2.4 c,   to 8.8 + 2.2 c
+// and none takes less than B does from HBM at 5.5 TB/s, beside which a twentieth of
+// the work shows.  Measured, in the order 16 x 2, 16 x 4, 32 x 4, 64 x 4, tiles:
+// 32 groups, N = 4096, K = 7168: of 8 rows 103, 88, 90, 110, 107; of 32 rows 244, 202,
+// 115, 129, 112; of 256 rows 1305, 1075, 670, 541, 160.  8 such groups of 32 rows: 52,
+// 47, 24, 30, 38.  One group of N = 7168, K = 16384: 16 rows 17, 25, 26, 29, 63; 48
+// rows 43, 47, 30, 36, 65; 128 rows 95, 90, 57, 39, 67.
 enum Kernel { ROWS16_NARROW, ROWS16, ROWS32, ROWS64, TILES };
 
 Kernel choose(const MxGemmArgs& a, int cus) {
     const double c = (double)((a.K + 511) / 512), groups = (double)(a.G < a.M_total ? a.G : a.M_total);
     const double mean = (double)a.M_total / groups;
-    // row tiles of `high` rows, by halves: a group ends in half a tile on the average
-    auto row_tiles = [&](int high) { return mean <= 0.8 * high ? groups : (double)a.M_total / high + 0.5 * groups; };
-    const double columns = (double)((a.N + 15) / 16), wide = (double)((a.N + TN - 1) / TN);
-    auto rows = [&](int high, double at, double per, double rate) {
-        return at + per * c + row_tiles(high) * (high / 16) * columns * c / rate;
+    const double hbm = groups * a.N * a.K / 2 / 5.5e6;
+    // row tiles of `high` rows: a group ends in half a tile on the average
+    auto row_tiles = [&](int high) {
+        if (groups == 1.0) return __builtin_ceil(mean / high);
+        return mean <= 0.68 * high ? groups : (double)a.M_total / high + 0.5 * groups;
     };
-    auto tiles = [&](int high, double at, double full) {
-        const double n = row_tiles(high) * wide, rounds = n / cus;
-        return rounds <= 1.0 ? at + (2.7 + (full - 2.7) * rounds) * c : __builtin_ceil(rounds) * (at + full * c);
+    auto beside = [&](double work) { return work > hbm ? work + 0.05 * hbm : hbm + 0.05 * work; };
+    auto rows = [&](int high, int wide, double at, double per) {
+        const double rounds = row_tiles(high) * ((a.N + wide - 1) / wide) / cus;
+        return at + beside(per * c * (rounds < 4.0 ? __builtin_ceil(rounds) : rounds));
     };
-    const double halves = tiles(128, 9.0, 3.6), wholes = tiles(256, 11.0, 4.5);
-    const double t[5] = {rows(16, 6.0, 0.3, 1600.0), rows(16, 6.0, 0.5, 1800.0), rows(32, 6.0, 0.65, 3000.0),
-                         rows(64, 6.0, 0.95, 3500.0), halves < wholes ? halves : wholes};
+    auto tiles = [&](int high, double low, double full) {
+        const double rounds = row_tiles(high) * ((a.N + TN - 1) / TN) / cus;
+        return 8.8 + beside(rounds <= 1.0 ? (low + (full - low) * rounds) * c : __builtin_ceil(rounds) * (8.8 + full * c) - 8.8);
+    };
+    const double halves = tiles(128, 2.4, 2.2), wholes = tiles(256, 1.8, 3.3);
+    const double t[5] = {rows(16, 32, 3.8, 0.4), rows(16, 64, 4.2, 0.69), rows(32, 64, 3.8, 0.8), rows(64, 64, 4.0, 1.19),
+                         halves < wholes ? halves : wholes};
     int best = a.G + a.M_total / 16 <= 65535 ? 0 : 4;    // the first four have a grid row for every row tile
     for (int i = best + 1; i < 5; ++i)
         if (t[i] < t[best]) best = i;

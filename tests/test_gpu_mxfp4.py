@@ -206,13 +206,16 @@ def test_product_exact(sizes, N, K):
     assert torch.equal(half, ref.float().bfloat16())
 
 
-# Sizes that the other kernels take: a wave's 16 rows in 32 groups, tiles of 128
-# rows, tiles of 256; K with and without a whole number of 128s and of 512s.
+# Sizes that the other kernels take: a wave's 16, 32 and 64 rows, whole and half
+# tiles; K with and without a whole number of 128s and of 512s.
 MANY = [
     ([13] * 31 + [0], 4096, 640), ([12] * 30 + [1, 39], 4096, 1056),
     ([1200, 0, 500, 300], 1500, 1056), ([700, 1, 0, 1100, 199], 1536, 2048), ([129, 128, 127, 1616], 1280, 1152),
     ([6000], 4096, 544), ([3500, 0, 2500], 4000, 672), ([2600, 1, 0, 255, 257, 2300, 31], 3840, 1024),
-    ([5000, 256], 3840, 1152),
+    ([5000, 256], 3840, 1152), ([12] * 30 + [0, 9], 4608, 1152), ([11] * 30 + [1, 39], 4608, 1056),
+    ([10] * 13 + [0, 2, 0], 4608, 4128), ([10] * 15 + [21], 4608, 4096), ([0, 0, 1, 0] * 16, 1024, 640),
+    ([0] * 280 + [3, 0, 17] + [0] * 17, 512, 672),
+    ([217, 183], 1536, 4096), ([200, 0, 143, 1], 1536, 4128),
 ]
 
 
