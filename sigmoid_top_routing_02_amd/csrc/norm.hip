@@ -201,7 +201,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddR
 
 // As the forward; each block keeps the sum of dy * xh of its rows in registers and
 // leaves it as one row of `part` at the end.  8192 rows of 7168 bf16 values with dh:
-// 98 us (4.8 TB/s, the rate of a plain copy) and 4 us for dw_reduce_kernel.
+// 98 us (4.8 TB/s, the rate of a plain copy) and 6 us for dw_reduce_kernel.
 template <int NV, bool VEC, bool WAVE_ROW, bool NT>
 __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_backward_kernel(AddRmsnormBackwardArgs a) {
     __shared__ float part[2][16];
@@ -274,7 +274,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_backward_ke
 }
 
 // dw[c] = sum of the partial rows: 16 threads take every 16th row of a column,
-// eight loads at a time, then their sums are added in order (512 rows of 7168: 4 us).
+// eight loads at a time, then their sums are added in order (512 rows of 7168: 6 us).
 __global__ __launch_bounds__(256) void dw_reduce_kernel(const float* __restrict__ part, int rows, int d,
                                                         float* __restrict__ dw) {
     __shared__ float sum[16][17];
