@@ -602,10 +602,10 @@ def _in(t, dtype, shape, name, dev):
     return t.data_ptr()
 
 
-def _out(t, like, dtype, shape, name, dev):
-    """An output of this type and shape, allocated beside `like` where t is None, and its address."""
+def _out(t, dtype, shape, name, dev):
+    """An output of this type and shape, allocated on GPU dev where t is None, and its address."""
     if t is None:
-        t = like.new_empty(shape, dtype=dtype)
+        t = torch.empty(*shape, dtype=dtype, device=dev)
         return t, t.data_ptr()
     return t, _in(t, dtype, shape, name, dev)
 
@@ -651,14 +651,14 @@ def moe_add_rmsnorm(x, weight, eps, residual=None, quant=False, h_out=None, y=No
     if residual is not None:
         rd = _dt(residual, "residual")
         pr = _in(residual, residual.dtype, shape, "residual", dev)
-        h_out, ph = _out(h_out, x, residual.dtype, shape, "h_out", dev)
+        h_out, ph = _out(h_out, residual.dtype, shape, "h_out", dev)
     elif h_out is not None:
         raise MoEError("moe_add_rmsnorm: h_out without a residual")
-    y, py = _out(y, x, torch.bfloat16, shape, "y", dev)
-    rstd, prs = _out(rstd, x, torch.float32, (T,), "rstd", dev)
+    y, py = _out(y, torch.bfloat16, shape, "y", dev)
+    rstd, prs = _out(rstd, torch.float32, (T,), "rstd", dev)
     if quant:
-        q, pq = _out(q, x, torch.uint8, shape, "q", dev)
-        scale, ps = _out(scale, x, torch.float32, (T, d // 128), "scale", dev)
+        q, pq = _out(q, torch.uint8, shape, "q", dev)
+        scale, ps = _out(scale, torch.float32, (T, d // 128), "scale", dev)
     elif q is not None or scale is not None:
         raise MoEError("moe_add_rmsnorm: q or scale without quant")
     L = _lib or load_library()
@@ -676,12 +676,12 @@ def moe_add_rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, dw=None, dx_
     shape = dy.shape
     if dx_dtype is None:
         dx_dtype = dh.dtype if dh is not None else dx.dtype if dx is not None else dy.dtype
-    dx, pdx = _out(dx, dy, dx_dtype, shape, "dx", dev)
-    dw, pdw = _out(dw, dy, torch.float32, (d,), "dw", dev)
+    dx, pdx = _out(dx, dx_dtype, shape, "dx", dev)
+    dw, pdw = _out(dw, torch.float32, (d,), "dw", dev)
     L = _lib or load_library()
     if ws is None:
         ws_bytes = max(L.moe_add_rmsnorm_backward_workspace_bytes(T, d), 16)
-        ws = dy.new_empty((ws_bytes,), dtype=torch.uint8)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         pws = ws.data_ptr()
     else:
         ws_bytes, pws = ws.numel() * ws.element_size(), _in(ws, ws.dtype, ws.shape, "ws", dev)
@@ -701,8 +701,8 @@ def mxfp4_quant_1x32(x, q=None, scale=None):
     """x bf16/f32 [rows, cols] -> (q uint8 [rows, cols/2], two E2M1 codes to a byte, the even column in
     the low half; scale uint8 [rows, cols/32], E8M0)."""
     rows, cols, dt, dev = _rows(x, "x")
-    q, pq = _out(q, x, torch.uint8, (rows, cols // 2), "q", dev)
-    scale, ps = _out(scale, x, torch.uint8, (rows, cols // 32), "scale", dev)
+    q, pq = _out(q, torch.uint8, (rows, cols // 2), "q", dev)
+    scale, ps = _out(scale, torch.uint8, (rows, cols // 32), "scale", dev)
     L = _lib or load_library()
     st = L.mxfp4_quant_1x32(_in(x, x.dtype, x.shape, "x", dev), dt, rows, cols, pq, ps, _raw_stream(dev))
     if st:
@@ -716,7 +716,7 @@ def _dequant(name, q, scale, cols, scale_dtype, per, dtype, out):
     dev = _current(q, "q")
     if dtype not in _DTYPES:
         raise MoEError(f"{name}: dtype {dtype}, expected torch.bfloat16 or torch.float32")
-    out, po = _out(out, q, dtype, (rows, cols), "out", dev)
+    out, po = _out(out, dtype, (rows, cols), "out", dev)
     L = _lib or load_library()
     st = getattr(L, name)(_in(q, torch.uint8, q.shape, "q", dev), _in(scale, scale_dtype, (rows, cols // per), "scale", dev),
                           rows, cols, po, _DTYPES[dtype], _raw_stream(dev))
@@ -760,14 +760,14 @@ def grouped_gemm_mxfp4(a_q, a_scale, group_offset, M_total, b_q, b_scale, epi=MO
         raise MoEError("group_offset must be int32 with G+1 entries")
     po = pq = ps = None
     if epi == MOE_MX_SWIGLU_QUANT:
-        out_q, pq = _out(out_q, b_q, torch.uint8, (M_total, N // 4), "out_q", dev)
-        out_scale, ps = _out(out_scale, b_q, torch.uint8, (M_total, N // 64), "out_scale", dev)
+        out_q, pq = _out(out_q, torch.uint8, (M_total, N // 4), "out_q", dev)
+        out_scale, ps = _out(out_scale, torch.uint8, (M_total, N // 64), "out_scale", dev)
         if out is not None:
             raise MoEError("grouped_gemm_mxfp4: this epilogue writes out_q and out_scale, not out")
     else:
         want = torch.float32 if epi == MOE_MX_STORE_F32 else torch.bfloat16
         shape = (M_total, N // 2 if epi == MOE_MX_SWIGLU_BF16 else N)
-        out, po = _out(out, b_q, want, shape, "out", dev)
+        out, po = _out(out, want, shape, "out", dev)
         if out_q is not None or out_scale is not None:
             raise MoEError("grouped_gemm_mxfp4: this epilogue writes out, not out_q or out_scale")
     L = _lib or load_library()
