@@ -162,8 +162,7 @@ __global__ __launch_bounds__(256) void fp8_dequant_1x128_kernel(const void* __re
 }
 
 unsigned grid_for(int64_t lanes, int per) {
-    const int64_t b = (lanes + 256 * per - 1) / (256 * per);
-    return (unsigned)(b < 0x7FFFFFFF ? b : 0x7FFFFFFF);
+    return launch_blocks((lanes + 256 * per - 1) / (256 * per), 256);
 }
 
 }  // namespace

@@ -339,9 +339,7 @@ struct ForwardLaunch {
     template <int NV, bool VEC, bool WAVE_ROW>
     void operator()() const {
         const int64_t per = WAVE_ROW ? 4 : 1;
-        int64_t blocks = (a.T + per - 1) / per;
-        if (blocks > 0x7FFFFFFF) blocks = 0x7FFFFFFF;
-        const dim3 grid((unsigned)blocks), block(row_threads(a.d, FORWARD_NARROW));
+        const dim3 block(row_threads(a.d, FORWARD_NARROW)), grid(launch_blocks((a.T + per - 1) / per, block.x));
         hipLaunchKernelGGL((add_rmsnorm_kernel<NV, VEC, WAVE_ROW>), grid, block, 0, st, a);
     }
 };

@@ -25,4 +25,11 @@ __device__ __forceinline__ void put(T* p, T v) {
 // rows of 512 values and 128 MiB 87 / 117.
 inline bool streamed(int64_t bytes) { return bytes > ((int64_t)64 << 20); }
 
+// Blocks of a launch that has work for `want` blocks: a launch is held under 2^32
+// threads, and kernels whose work may pass that go on in steps of the grid.
+inline unsigned launch_blocks(int64_t want, int threads) {
+    const int64_t most = 0xFFFFFFFFll / threads;
+    return (unsigned)(want < most ? want : most);
+}
+
 }  // namespace moe

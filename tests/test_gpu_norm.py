@@ -91,6 +91,23 @@ def test_forward_more_rows_than_the_grid(T, d):
     _check_forward(*_inputs(T, d, "bf16", "bf16", "f32"), quant=True)
 
 
+def test_forward_rows_that_pass_a_launch():
+    """Four rows of 8 values to a block of 256 threads: more than 2^32 threads."""
+    dev()
+    T, d = (1 << 26) + 5, 8
+    say(f"  T={T}")
+    x = torch.empty((T, d), dtype=torch.int8, device="cuda").random_(-100, 100, generator=_gen(3)).bfloat16()
+    w = torch.linspace(0.5, 2.0, d, device="cuda")
+    r = moe.moe_add_rmsnorm(x, w, EPS)
+    torch.cuda.synchronize()
+    for at in range(0, T, 1 << 23):
+        h = x[at:at + (1 << 23)].to(F8)
+        rstd = 1.0 / torch.sqrt((h * h).mean(1) + EPS)
+        assert (r.rstd[at:at + (1 << 23)].to(F8) / rstd - 1).abs().max() <= 64 * U
+        y = h * rstd[:, None] * w.to(F8)
+        assert ((r.y[at:at + (1 << 23)].to(F8) - y).abs() <= (BF + 80 * U) * y.abs() + 2.0 ** -133).all()
+
+
 def test_forward_special_rows():
     """A row of zeros normalises to zeros; NaN and infinity stay in their row; tiny and huge rows
     keep their precision as long as their squares are binary32 numbers."""
