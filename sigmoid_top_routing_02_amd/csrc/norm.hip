@@ -325,12 +325,26 @@ void dispatch_shape(int d, Launch&& go) {
 
 int row_threads(int d, int narrow) { return d <= narrow ? 256 : (d + 1023) / 1024 * 64; }
 
-// Blocks of the backward: a few per CU, so that the partial rows stay small
-// beside the data; a function of the sizes alone, so dw's bits are too.
+// Blocks of the backward: a power of two of them per CU that comes to at most 16
+// waves there (32 where a row is one wave that holds it in two steps), as long as
+// each has four rows to go through (eight where a row is a wave), so that the
+// partial rows stay few beside the data.  Measured with 256 / 512 / 1024 / 2048
+// blocks, us: 32768 rows of 2048 values 268 / 156 / 104 / 80, 2048 of them 18 / 14 /
+// 16 / 21; 32768 rows of 7168 values 459 / 283 / 292 / 350, 517 of them 15 / 18 / 19 /
+// 19; 8192 rows of 16384 values 172 / 180 / 198 / 236.  131072 rows with 512 / 1024 /
+// 2048 blocks: of 128 values 76 / 46 / 49, of 1024 values 218 / 214 / 182; 8192 rows of
+// 128 values with 256 / 512 / 1024: 11.2 / 9.1 / 9.4.  Functions of the sizes alone, so
+// dw's bits are too.
+int backward_most(int d) {
+    const int waves = (d + 1023) / 1024;
+    return d <= 512 ? 1024 : waves <= 2 ? 2048 : waves <= 4 ? 1024 : waves <= 8 ? 512 : 256;
+}
+
 int backward_blocks(int64_t T, int d) {
-    const int64_t per = d <= BACKWARD_NARROW ? 4 : 1;
-    const int64_t b = (T + per - 1) / per;
-    return (int)(b < 512 ? b : 512);
+    const bool narrow = d <= BACKWARD_NARROW;
+    const int64_t rows = narrow ? (T + 3) / 4 : T, few = rows / (narrow ? 8 : 4), least = narrow ? 512 : 256;
+    const int64_t most = backward_most(d), b = few < least ? least : few < most ? few : most;
+    return (int)(rows < b ? rows : b);
 }
 
 struct ForwardLaunch {
@@ -365,7 +379,8 @@ hipError_t launch_add_rmsnorm(const AddRmsnormArgs& a, hipStream_t st) {
 }
 
 size_t add_rmsnorm_backward_ws_bytes(int64_t T, int d) {
-    return (size_t)backward_blocks(T, d) * d * sizeof(float);
+    const int64_t most = backward_most(d) < 512 ? 512 : backward_most(d);       // backward_blocks or more
+    return (size_t)(T < most ? T : most) * d * sizeof(float);
 }
 
 hipError_t launch_add_rmsnorm_backward(const AddRmsnormBackwardArgs& a, float* dw, hipStream_t st) {
