@@ -29,69 +29,70 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
-// How a row of d values lies in the NV * 8 registers of each of its TPR threads.
-// VEC (d % 8 == 0, rows then 16-byte aligned): thread t holds 8 consecutive
-// values at ((v * TPR) + t) * 8.  Otherwise value j of step v is at
-// (v * 8 + j) * TPR + t, one element per access, neighbours on neighbouring
-// threads.
-template <bool VEC>
-__device__ __forceinline__ int col_of(int v, int j, int t, int tpr) {
-    return VEC ? (v * tpr + t) * 8 + j : (v * 8 + j) * tpr + t;
-}
+// A row of d values lies in the NV * 8 registers of each of its threads as 8
+// consecutive values at ((v * tpr) + t) * 8, t of tpr threads.  VEC: d % 8 == 0, so
+// that each such 8 lie on 16 bytes and in the row or past it; otherwise the vector
+// accesses are to addresses of the values' own alignment, which this GPU takes, and
+// the row's last up to 7 values are accessed one by one (32768 rows of bf16 values
+// with residual: 999 wide 59 us against 84 with one value an access throughout, 4095
+// wide 305 against 494, but 100 wide 22 against 16; the backward of 131072 rows, 999
+// wide, 345 against 766).
+__device__ __forceinline__ int col_of(int v, int t, int tpr) { return (v * tpr + t) * 8; }
+
+template <bool VEC> struct Aligned {                     // four words
+    typedef uint32_t bf16 __attribute__((ext_vector_type(4)));
+    typedef float f32 __attribute__((ext_vector_type(4)));
+};
+template <> struct Aligned<false> {
+    typedef uint32_t bf16 __attribute__((ext_vector_type(4), aligned(2)));
+    typedef float f32 __attribute__((ext_vector_type(4), aligned(4)));
+};
 
 // 8 values of a row (zero past its end).  f32 is uniform over the launch.
 template <bool VEC>
 __device__ __forceinline__ void load8(const void* p, bool f32, int64_t row_off, int v, int t, int tpr, int d,
                                       float (&x)[8]) {
-    if constexpr (VEC) {
-        const int c = col_of<VEC>(v, 0, t, tpr);
-        if (c < d) {
-            if (f32) {
-                const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + row_off + c);
-                const float4 a = q[0], b = q[1];
-                x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-                x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-            } else {
-                const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + row_off + c);
-                x[0] = bf16_lo(a.x); x[1] = bf16_hi(a.x); x[2] = bf16_lo(a.y); x[3] = bf16_hi(a.y);
-                x[4] = bf16_lo(a.z); x[5] = bf16_hi(a.z); x[6] = bf16_lo(a.w); x[7] = bf16_hi(a.w);
-            }
+    const int c = col_of(v, t, tpr);
+    if (VEC ? c < d : c + 8 <= d) {
+        if (f32) {
+            const auto* q = reinterpret_cast<const typename Aligned<VEC>::f32*>(static_cast<const float*>(p) + row_off + c);
+            const v4f a = q[0], b = q[1];
+            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
         } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+            const v4u a = *reinterpret_cast<const typename Aligned<VEC>::bf16*>(static_cast<const uint16_t*>(p) + row_off + c);
+            x[0] = bf16_lo(a.x); x[1] = bf16_hi(a.x); x[2] = bf16_lo(a.y); x[3] = bf16_hi(a.y);
+            x[4] = bf16_lo(a.z); x[5] = bf16_hi(a.z); x[6] = bf16_lo(a.w); x[7] = bf16_hi(a.w);
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = col_of<VEC>(v, j, t, tpr);
-            x[j] = c >= d ? 0.0f
-                   : f32  ? static_cast<const float*>(p)[row_off + c]
-                          : bf16_to_f32(static_cast<const uint16_t*>(p)[row_off + c]);
-        }
+        for (int j = 0; j < 8; ++j)
+            x[j] = VEC || c + j >= d ? 0.0f
+                   : f32             ? static_cast<const float*>(p)[row_off + c + j]
+                                     : bf16_to_f32(static_cast<const uint16_t*>(p)[row_off + c + j]);
     }
 }
 
 template <bool VEC, bool NT>
 __device__ __forceinline__ void store8(void* p, bool f32, int64_t row_off, int v, int t, int tpr, int d,
                                        const float (&x)[8]) {
-    if constexpr (VEC) {
-        const int c = col_of<VEC>(v, 0, t, tpr);
-        if (c >= d) return;
+    const int c = col_of(v, t, tpr);
+    if (VEC ? c < d : c + 8 <= d) {
         if (f32) {
-            v4f* q = reinterpret_cast<v4f*>(static_cast<float*>(p) + row_off + c);
-            put<NT>(q, v4f{x[0], x[1], x[2], x[3]});
-            put<NT>(q + 1, v4f{x[4], x[5], x[6], x[7]});
+            auto* q = reinterpret_cast<typename Aligned<VEC>::f32*>(static_cast<float*>(p) + row_off + c);
+            put<NT>(q, typename Aligned<VEC>::f32{x[0], x[1], x[2], x[3]});
+            put<NT>(q + 1, typename Aligned<VEC>::f32{x[4], x[5], x[6], x[7]});
         } else {
-            put<NT>(reinterpret_cast<v4u*>(static_cast<uint16_t*>(p) + row_off + c),
-                    v4u{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])});
+            put<NT>(reinterpret_cast<typename Aligned<VEC>::bf16*>(static_cast<uint16_t*>(p) + row_off + c),
+                    typename Aligned<VEC>::bf16{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                                                pack_bf16(x[6], x[7])});
         }
-    } else {
+    } else if (!VEC) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int c = col_of<VEC>(v, j, t, tpr);
-            if (c >= d) continue;
-            if (f32) static_cast<float*>(p)[row_off + c] = x[j];
-            else static_cast<uint16_t*>(p)[row_off + c] = (uint16_t)pack_bf16(x[j], 0.0f);
+            if (c + j >= d) continue;
+            if (f32) static_cast<float*>(p)[row_off + c + j] = x[j];
+            else static_cast<uint16_t*>(p)[row_off + c + j] = (uint16_t)pack_bf16(x[j], 0.0f);
         }
     }
 }
@@ -167,7 +168,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddR
             if (a.y) store8<VEC, true>(a.y, false, off, v, t, tpr, d, y);
             if constexpr (VEC) {
                 if (a.q) {                            // d % 128 == 0: 16 lanes are one tile, all in the row or none
-                    const int c = col_of<VEC>(v, 0, t, tpr);
+                    const int c = col_of(v, t, tpr);
                     float amax = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 8; j += 2) {
