@@ -54,6 +54,9 @@ def _run(cmd, verbose):
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("hipcc failed to build libmoefp8.so")
+    if r.stderr:                    # warnings of a build that went through
+        sys.stderr.write(r.stderr)
+        sys.stderr.flush()
 
 
 def build(verbose: bool = False) -> str:

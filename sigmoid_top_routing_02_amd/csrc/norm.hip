@@ -73,19 +73,29 @@ __device__ __forceinline__ void load8(const void* p, bool f32, int64_t row_off, 
     }
 }
 
+// (not through put(): a template's argument drops the vector types' lower alignment)
 template <bool VEC, bool NT>
 __device__ __forceinline__ void store8(void* p, bool f32, int64_t row_off, int v, int t, int tpr, int d,
                                        const float (&x)[8]) {
     const int c = col_of(v, t, tpr);
     if (VEC ? c < d : c + 8 <= d) {
         if (f32) {
-            auto* q = reinterpret_cast<typename Aligned<VEC>::f32*>(static_cast<float*>(p) + row_off + c);
-            put<NT>(q, typename Aligned<VEC>::f32{x[0], x[1], x[2], x[3]});
-            put<NT>(q + 1, typename Aligned<VEC>::f32{x[4], x[5], x[6], x[7]});
+            typedef typename Aligned<VEC>::f32 V;
+            V* q = reinterpret_cast<V*>(static_cast<float*>(p) + row_off + c);
+            const V a = {x[0], x[1], x[2], x[3]}, b = {x[4], x[5], x[6], x[7]};
+            if constexpr (NT) {
+                __builtin_nontemporal_store(a, q);
+                __builtin_nontemporal_store(b, q + 1);
+            } else {
+                q[0] = a;
+                q[1] = b;
+            }
         } else {
-            put<NT>(reinterpret_cast<typename Aligned<VEC>::bf16*>(static_cast<uint16_t*>(p) + row_off + c),
-                    typename Aligned<VEC>::bf16{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                                                pack_bf16(x[6], x[7])});
+            typedef typename Aligned<VEC>::bf16 V;
+            V* q = reinterpret_cast<V*>(static_cast<uint16_t*>(p) + row_off + c);
+            const V a = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+            if constexpr (NT) __builtin_nontemporal_store(a, q);
+            else *q = a;
         }
     } else if (!VEC) {
 #pragma unroll
