@@ -20,8 +20,7 @@ def _compile(source, *extra):
 def test_sources_compile_without_warnings():
     with ThreadPoolExecutor(max_workers=8) as ex:
         for source, r in zip(b.sources(), ex.map(lambda s: _compile(s, "-fsyntax-only"), b.sources())):
-            # the host pass does not know the GPU feature that the flags turn off
-            said = [line for line in r.stderr.splitlines() if "warning:" in line and "packed-fp32-ops" not in line]
+            said = [line for line in r.stderr.splitlines() if "warning:" in line]
             assert r.returncode == 0 and not said, f"{os.path.basename(source)}: {said}"
 
 
