@@ -19,6 +19,7 @@
 #include "device_math.h"
 #include "kernels.h"
 #include "moe_fp8.h"
+#include "mxoffsets.h"
 
 namespace moe {
 namespace {
@@ -26,11 +27,6 @@ namespace {
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-
-// Past the end of every descriptor below (the C ABI keeps their sizes at or
-// under it), with room for a 16-byte access and its immediate offset under 2^32:
-// reads there return 0 and touch no memory.
-constexpr uint32_t OUT = 0xFFFF0000u;
 
 #define FENCE() __builtin_amdgcn_sched_barrier(0)
 
@@ -57,15 +53,13 @@ template <bool KA>
 struct Scales {
     v4u w;
     uint32_t more;
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t d, uint32_t row, int c) {
-        if constexpr (KA) {
-            w = __builtin_amdgcn_raw_buffer_load_b128(d, row, c * 16, 0);
-        } else {
-            w = __builtin_amdgcn_raw_buffer_load_b128(d, row & ~3u, c * 16, 0);
-            more = __builtin_amdgcn_raw_buffer_load_b32(d, (row & ~3u) + 16u, c * 16, 0);
-        }
-    }
     template <bool WHOLE = false>                        // all 16 blocks are in the row
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t d, uint32_t row, int c) {
+        const BufferOffset at = scales_of_chunk(KA && WHOLE, KA ? row : row & ~3u, c);
+        w = __builtin_amdgcn_raw_buffer_load_b128(d, at.vector, at.scalar, 0);
+        if constexpr (!KA) more = __builtin_amdgcn_raw_buffer_load_b32(d, at.vector + 16u, at.scalar, 0);
+    }
+    template <bool WHOLE = false>
     __device__ __forceinline__ v4u bytes(uint32_t row, int c, int nblk) const {
         v4u v = w;
         if constexpr (!KA) {
@@ -249,11 +243,11 @@ struct Chunk {
                                          uint32_t row_s, int c, int kb, int nblk) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const bool in = WHOLE || c * 16 + j * 4 + kb < nblk;
-            q[j] = __builtin_amdgcn_raw_buffer_load_b128(dq, in ? row_q + j * 64u : OUT, c * 256, 0);
+            const BufferOffset at = code_of_chunk(WHOLE || c * 16 + j * 4 + kb < nblk, row_q, c, j);
+            q[j] = __builtin_amdgcn_raw_buffer_load_b128(dq, at.vector, at.scalar, 0);
             FENCE();                                     // the two halves of a 128-byte line right after each other
         }
-        s.load(ds, row_s, c);
+        s.template load<WHOLE>(ds, row_s, c);
     }
 };
 
@@ -337,12 +331,12 @@ __global__ __launch_bounds__(256) void mxgemm_rows_kernel(MxGemmArgs p) {
     const uint32_t rb = (uint32_t)p.K / 2;               // bytes of a row of codes
     // Scale descriptors end on a word.  A group's scales may start off one: the
     // descriptor then starts at the word before and the offsets begin at the rest.
-    const auto aq = make_rsrc(p.a_q, (uint32_t)(p.a_rows * rb));
-    const auto as = make_rsrc(p.a_s, ((uint32_t)(p.a_rows * nblk) + 3u) & ~3u);
-    const auto bq = make_rsrc(p.b_q + (int64_t)g * p.N * rb, (uint32_t)p.N * rb);
+    const auto aq = make_rsrc(p.a_q, code_records(p.a_rows, rb));
+    const auto as = make_rsrc(p.a_s, scale_records(p.a_rows, nblk, 0u));
+    const auto bq = make_rsrc(p.b_q + (int64_t)g * p.N * rb, code_records(p.N, rb));
     const int64_t sg = (int64_t)g * p.N * nblk;
     const uint32_t off = KA ? 0u : (uint32_t)sg & 3u;
-    const auto bs = make_rsrc(p.b_s + (sg - off), ((uint32_t)p.N * (uint32_t)nblk + off + 3u) & ~3u);
+    const auto bs = make_rsrc(p.b_s + (sg - off), scale_records(p.N, nblk, off));
     const int c0 = (int)blockIdx.x * COLS;
     uint32_t bro[NT], bso[NT];
 #pragma unroll
@@ -588,8 +582,8 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, TileLists& lists,
 
     // Scale descriptors end on a word.  A group's scales may start off one: the
     // descriptor then starts at the word before and the offsets begin at the rest.
-    const auto aq = make_rsrc(p.a_q, (uint32_t)(p.a_rows * rb));
-    const auto as = make_rsrc(p.a_s, ((uint32_t)(p.a_rows * nblk) + 3u) & ~3u);
+    const auto aq = make_rsrc(p.a_q, code_records(p.a_rows, rb));
+    const auto as = make_rsrc(p.a_s, scale_records(p.a_rows, nblk, 0u));
     auto bq = aq, bs = as;
     struct Tile { int g, m0, hi, n0; } T{}, U{}, V{};   // the tile at work, the one before, the next
     uint32_t aro[A_DMA], bro[B_DMA], aso, bso;
@@ -637,10 +631,10 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, TileLists& lists,
         }
     };
     auto setup = [&](const Tile& v) {
-        bq = make_rsrc(p.b_q + (int64_t)v.g * p.N * rb, (uint32_t)p.N * rb);
+        bq = make_rsrc(p.b_q + (int64_t)v.g * p.N * rb, code_records(p.N, rb));
         const int64_t sg = (int64_t)v.g * p.N * nblk;
         const uint32_t off = KA ? 0u : (uint32_t)sg & 3u;
-        bs = make_rsrc(p.b_s + (sg - off), ((uint32_t)p.N * (uint32_t)nblk + off + 3u) & ~3u);
+        bs = make_rsrc(p.b_s + (sg - off), scale_records(p.N, nblk, off));
         auto has = [&](int i) {                          // a row of the tile, and of A
             return row_of(i) < BM && v.m0 + row_of(i) < v.hi && am[i] < (uint32_t)p.a_rows;
         };
@@ -656,17 +650,19 @@ __device__ __forceinline__ void run_tiles(const MxGemmArgs& p, TileLists& lists,
     // Stage s of K into LDS stage ST, A and B.  Blocks past the end of K read zero.
     auto send_a = [&](auto stc, int s) {
         constexpr int ST = decltype(stc)::value;
-        const bool in = s * 4 + chunk_of < nblk;
 #pragma unroll
-        for (int i = 0; i < A_DMA; ++i)
-            lds_dma16(aq, in ? aro[i] : OUT, s * STAGE_BYTES, stage_buf<ST>() + (wave * A_DMA + i) * 1024);
+        for (int i = 0; i < A_DMA; ++i) {
+            const BufferOffset at = code_of_stage(aro[i], s, chunk_of, nblk);
+            lds_dma16(aq, at.vector, at.scalar, stage_buf<ST>() + (wave * A_DMA + i) * 1024);
+        }
     };
     auto send_b = [&](auto stc, int s) {
         constexpr int ST = decltype(stc)::value;
-        const bool in = s * 4 + chunk_of < nblk;
 #pragma unroll
-        for (int i = 0; i < B_DMA; ++i)
-            lds_dma16(bq, in ? bro[i] : OUT, s * STAGE_BYTES, stage_buf<ST>() + B_AT + (wave * B_DMA + i) * 1024);
+        for (int i = 0; i < B_DMA; ++i) {
+            const BufferOffset at = code_of_stage(bro[i], s, chunk_of, nblk);
+            lds_dma16(bq, at.vector, at.scalar, stage_buf<ST>() + B_AT + (wave * B_DMA + i) * 1024);
+        }
     };
     auto load_scales = [&](int c) {
         ca.load(as, aso, c);

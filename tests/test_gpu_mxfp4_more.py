@@ -1,0 +1,27 @@
+"""Further cases of the MXFP4 quantiser, dequantisers and grouped product on the GPU."""
+import pytest
+import torch
+
+import sigmoid_top_routing_02_amd as moe
+from helpers import dev, say
+from test_gpu_mxfp4 import F8, offsets, operands, ref_product
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("M,N,K", [(40000, 1, 65536), (1100000, 1, 32), (1100000, 1, 96), (20000, 1024, 32),
+                                   (5000, 256, 65536), (40, 1, 65536), (5, 3, 1056)])
+def test_one_row_of_a_and_few_of_b(M, N, K):
+    """A of one row, which every row of the product (but two outside A) names, and B of few: the tensors
+    are smaller than what the kernels send for ahead.  Scales of 1: every product is a multiple of 1/4 of at
+    most 36, so that sums of 65536 are binary32 numbers."""
+    dev()
+    say(f"  M={M} N={N} K={K}")
+    aq, a_s, bq, b_s, idx = operands(M, 1, 1, N, K, N + K, low=127, high=128)
+    idx[[0, M // 2]] = torch.tensor([1, -1], dtype=torch.int32, device="cuda")
+    got = moe.grouped_gemm_mxfp4(aq, a_s, offsets([M]), M, bq, b_s, a_row_index=idx)
+    torch.cuda.synchronize()
+    row = ref_product(aq, a_s, bq, b_s, None, [1])
+    zero = torch.zeros(M, dtype=torch.bool, device="cuda")
+    zero[[0, M // 2]] = True
+    assert (got[zero] == 0).all() and (got[~zero].to(F8) == row).all()
