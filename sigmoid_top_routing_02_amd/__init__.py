@@ -583,6 +583,11 @@ def moe_wgrad(dh, topk_gate, slot_row, row_token, z, dh_row, u, group_offset, sh
 # is most of theirs: their checks pass over each tensor once (_in) and raise
 # through _refuse, which finds out what was wrong.
 RMSNorm = namedtuple("RMSNorm", "y h rstd q scale")
+_INT_MAX = 2 ** 31 - 1              # ctypes hands a larger C int over modulo 2^32
+
+
+def _too_large(name, n):
+    raise MoEError(f"{name}: {n} is past a C int")
 
 
 def _refuse(t, dtype, shape, name, dev):
@@ -618,6 +623,8 @@ def _rows(t, name):
     if dt is None:
         raise MoEError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
     rows, cols = t.shape
+    if cols > _INT_MAX:
+        _too_large(f"{name}'s columns", cols)
     return rows, cols, dt, _current(t, name)
 
 
@@ -714,6 +721,8 @@ def _dequant(name, q, scale, cols, scale_dtype, per, dtype, out):
     """The shared part of the dequantisers: values [rows, cols], `per` of them under each scale."""
     rows = q.shape[0]
     dev = _current(q, "q")
+    if cols > _INT_MAX:
+        _too_large("columns", cols)
     if dtype not in _DTYPES:
         raise MoEError(f"{name}: dtype {dtype}, expected torch.bfloat16 or torch.float32")
     out, po = _out(out, dtype, (rows, cols), "out", dev)
@@ -749,6 +758,8 @@ def grouped_gemm_mxfp4(a_q, a_scale, group_offset, M_total, b_q, b_scale, epi=MO
     G, N, half = b_q.shape
     K = half * 2
     rows = a_q.shape[0]
+    if G > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
+        _too_large("G, N or K", max(G, N, K))
     dev = _current(b_q, "b_q")
     pi = None
     if a_row_index is not None:

@@ -25,3 +25,35 @@ def test_one_row_of_a_and_few_of_b(M, N, K):
     zero = torch.zeros(M, dtype=torch.bool, device="cuda")
     zero[[0, M // 2]] = True
     assert (got[zero] == 0).all() and (got[~zero].to(F8) == row).all()
+
+
+def test_sizes_past_the_c_abis_integers_are_refused():
+    """Widths that a C int would hold modulo 2^32 (as 32, 128 or 1): refused, not taken for those."""
+    dev()
+    new = lambda *s, dtype=torch.uint8: torch.empty(s, dtype=dtype, device="cuda")  # noqa: E731
+    wide, index = 2 ** 32, torch.zeros(1, dtype=torch.int32, device="cuda")
+    bad = [
+        lambda: moe.mxfp4_quant_1x32(new(1, wide + 32, dtype=torch.bfloat16)),
+        lambda: moe.mxfp4_dequant_1x32(new(1, wide // 2 + 16), new(1, wide // 32 + 1)),
+        lambda: moe.fp8_dequant_1x128(new(1, wide + 128), new(1, wide // 128 + 1, dtype=torch.float32)),
+        lambda: moe.moe_add_rmsnorm(new(1, wide + 1, dtype=torch.bfloat16), new(wide + 1, dtype=torch.bfloat16), 1e-6),
+        lambda: moe.moe_add_rmsnorm_backward(new(1, wide + 1, dtype=torch.bfloat16), new(1, wide + 1, dtype=torch.bfloat16),
+                                             new(wide + 1, dtype=torch.bfloat16), new(1, dtype=torch.float32)),
+        lambda: moe.grouped_gemm_mxfp4(new(1, 16), new(1, 1), offsets([1]), 1, new(1, wide + 1, 16), new(1, wide + 1, 1),
+                                       a_row_index=index),
+        lambda: moe.grouped_gemm_mxfp4(new(1, wide // 2 + 16), new(1, wide // 32 + 1), offsets([1]), 1,
+                                       new(1, 1, wide // 2 + 16), new(1, 1, wide // 32 + 1)),
+        lambda: moe.grouped_gemm_mxfp4(new(1, 16), new(1, 1), new(wide + 2, dtype=torch.int32), 1, new(wide + 1, 1, 16),
+                                       new(wide + 1, 1, 1), a_row_index=index),
+    ]
+    taken = []
+    for i, f in enumerate(bad):
+        say(f"  call {i}")
+        try:
+            f()
+            taken.append(i)
+        except moe.MoEError:
+            pass
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+    assert not taken
