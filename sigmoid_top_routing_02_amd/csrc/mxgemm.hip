@@ -19,6 +19,7 @@
 #include "device_math.h"
 #include "kernels.h"
 #include "moe_fp8.h"
+#include "mxchoose.h"
 #include "mxoffsets.h"
 
 namespace moe {
@@ -436,13 +437,11 @@ __global__ __launch_bounds__(256) void mxgemm_rows_kernel(MxGemmArgs p) {
     }
 }
 
-template <int EPI, int MI, int NT>
+template <int EPI, MxKernel K>
 hipError_t launch_rows(const MxGemmArgs& a, hipStream_t st) {
-    constexpr bool SWIGLU = EPI == MOE_MX_SWIGLU_BF16 || EPI == MOE_MX_SWIGLU_QUANT;
-    constexpr int COLS = SWIGLU ? NT * 8 : NT * 16;
-    const int cols = SWIGLU ? a.N / 2 : a.N;
-    // as find_tile deals them
-    const dim3 grid((cols + COLS - 1) / COLS, (unsigned)(a.M_total < a.G ? a.M_total : a.G + a.M_total / (16 * MI)));
+    constexpr int MI = mx_rows(K).high / 16, NT = mx_rows(K).tiles;
+    const MxGrid g = mx_rows_grid(mx_rows(K), a.M_total, a.G, a.N);
+    const dim3 grid((unsigned)g.x, (unsigned)g.y);
     if (a.K % 128 == 0)
         hipLaunchKernelGGL((mxgemm_rows_kernel<EPI, MI, NT, true>), grid, dim3(256), 0, st, a);
     else
@@ -468,7 +467,7 @@ hipError_t launch_rows(const MxGemmArgs& a, hipStream_t st) {
 // every wave in every stage.  Lane l's two operands of a stage are blocks
 // 2 (l / 32) and + 1 of its four: a row's 16 bytes are put into LDS as the 8 of
 // lanes 0-31, stage by stage, then the 8 of lanes 32-63.
-constexpr int TN = 256;
+constexpr int TN = MX_TILE_COLS;
 constexpr int STAGE_BYTES = 64;                          // of a row
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
@@ -976,63 +975,17 @@ hipError_t launch_tiles(const MxGemmArgs& a, int cus, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Which kernel: the one that the times below (us) make the fastest.  They were
-// fitted to 445 measured calls, 1 to 256 groups of 1 to 4096 rows, even and skewed,
-// N = 256 to 14336, K = 1024 to 32768, weights from HBM and from the caches; the choice
-// costs 1.4 % over the fastest kernel on the average and 37 % at most.  The host
-// knows the groups' sizes on the average only.  c is the number of 512-value chunks
-// of K; a round is a block (a tile) on every CU, and a call's last round counts
-// whole while there are few of them.
-//   16 rows, 2 column tiles: 3.8 + 0.4 c a round     16 rows, 4: 4.2 + 0.69 c
-//   32 rows, 4 column tiles: 3.8 + 0.8 c             64 rows, 4: 4 + 1.19 c
-//   whole tiles: 8.8 + 1.8 c up to 8.8 + 3.3 c when the round is full
-//   half tiles:  8.8 + 2.4 c,   to 8.8 + 2.2 c
-// and none takes less than B does from HBM at 5.5 TB/s, beside which a twentieth of
-// the work shows.  Measured, in the order 16 x 2, 16 x 4, 32 x 4, 64 x 4, tiles:
-// 32 groups, N = 4096, K = 7168: of 8 rows 103, 88, 90, 110, 107; of 32 rows 244, 202,
-// 115, 129, 112; of 256 rows 1305, 1075, 670, 541, 160.  8 such groups of 32 rows: 52,
-// 47, 24, 30, 38.  One group of N = 7168, K = 16384: 16 rows 17, 25, 26, 29, 63; 48
-// rows 43, 47, 30, 36, 65; 128 rows 95, 90, 57, 39, 67.
-enum Kernel { ROWS16_NARROW, ROWS16, ROWS32, ROWS64, TILES };
-
-Kernel choose(const MxGemmArgs& a, int cus) {
-    const double c = (double)((a.K + 511) / 512), groups = (double)(a.G < a.M_total ? a.G : a.M_total);
-    const double mean = (double)a.M_total / groups;
-    const double hbm = groups * a.N * a.K / 2 / 5.5e6;
-    // row tiles of `high` rows: a group ends in half a tile on the average
-    auto row_tiles = [&](int high) {
-        if (groups == 1.0) return __builtin_ceil(mean / high);
-        return mean <= 0.68 * high ? groups : (double)a.M_total / high + 0.5 * groups;
-    };
-    auto beside = [&](double work) { return work > hbm ? work + 0.05 * hbm : hbm + 0.05 * work; };
-    auto rows = [&](int high, int wide, double at, double per) {
-        const double rounds = row_tiles(high) * ((a.N + wide - 1) / wide) / cus;
-        return at + beside(per * c * (rounds < 4.0 ? __builtin_ceil(rounds) : rounds));
-    };
-    auto tiles = [&](int high, double low, double full) {
-        const double rounds = row_tiles(high) * ((a.N + TN - 1) / TN) / cus;
-        return 8.8 + beside(rounds <= 1.0 ? (low + (full - low) * rounds) * c : __builtin_ceil(rounds) * (8.8 + full * c) - 8.8);
-    };
-    const double halves = tiles(128, 2.4, 2.2), wholes = tiles(256, 1.8, 3.3);
-    const double t[5] = {rows(16, 32, 3.8, 0.4), rows(16, 64, 4.2, 0.69), rows(32, 64, 3.8, 0.8), rows(64, 64, 4.0, 1.19),
-                         halves < wholes ? halves : wholes};
-    int best = a.G + a.M_total / 16 <= 65535 ? 0 : 4;    // the first four have a grid row for every row tile
-    for (int i = best + 1; i < 5; ++i)
-        if (t[i] < t[best]) best = i;
-    return (Kernel)best;
-}
-
 template <int EPI>
 hipError_t launch_epi(const MxGemmArgs& a, hipStream_t st) {
-    constexpr int FEW = EPI == MOE_MX_SWIGLU_QUANT ? 4 : 2;      // 32 columns of h need 4 column tiles
+    constexpr MxKernel FEW = EPI == MOE_MX_SWIGLU_QUANT ? ROWS16 : ROWS16_NARROW;   // 32 columns of h need 4 column tiles
     int cus = 0;
     const hipError_t e = cu_count(cus);
     if (e != hipSuccess) return e;
-    switch (choose(a, cus)) {
-        case ROWS16_NARROW: return launch_rows<EPI, 1, FEW>(a, st);
-        case ROWS16: return launch_rows<EPI, 1, 4>(a, st);
-        case ROWS32: return launch_rows<EPI, 2, 4>(a, st);
-        case ROWS64: return launch_rows<EPI, 4, 4>(a, st);
+    switch (mx_choose(a.M_total, a.G, a.N, a.K, cus)) {
+        case ROWS16_NARROW: return launch_rows<EPI, FEW>(a, st);
+        case ROWS16: return launch_rows<EPI, ROWS16>(a, st);
+        case ROWS32: return launch_rows<EPI, ROWS32>(a, st);
+        case ROWS64: return launch_rows<EPI, ROWS64>(a, st);
         default: return launch_tiles<EPI>(a, cus, st);
     }
 }

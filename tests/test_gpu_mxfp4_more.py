@@ -57,3 +57,19 @@ def test_sizes_past_the_c_abis_integers_are_refused():
         torch.cuda.synchronize()
         torch.cuda.empty_cache()
     assert not taken
+
+
+def test_more_columns_than_a_few_row_launch_takes():
+    """Few rows on 2^27 columns: 1.5 times 2^32 threads of the kernel that few rows take otherwise.  B repeats
+    4099 rows."""
+    dev()
+    G, per, N, K, period = 8, 8, 2 ** 27, 32, 4099
+    M = G * per
+    aq, a_s, bq, b_s, _ = operands(M, M, 1, period, K, 12)
+    bq, b_s = (t[0].repeat(N // period + 1, 1)[:N].expand(G, N, t.shape[2]).contiguous() for t in (bq, b_s))
+    out = moe.grouped_gemm_mxfp4(aq, a_s, offsets([per] * G), M, bq, b_s, epi=moe.MOE_MX_STORE_BF16)
+    torch.cuda.synchronize()
+    want = ref_product(aq, a_s, bq[:1, :period], b_s[:1, :period], None, [M]).float().bfloat16()
+    whole = N // period * period
+    assert (out[:, :whole].view(M, -1, period) == want[:, None]).all()
+    assert torch.equal(out[:, whole:], want[:, :N - whole])

@@ -23,3 +23,7 @@ def _run(name, tmp_path):
 
 def test_offsets_stay_inside_the_tensors(tmp_path):
     assert "reads checked" in _run("mx_offsets", tmp_path)
+
+
+def test_few_row_launches_stay_under_their_limits(tmp_path):
+    assert "few rows" in _run("mx_choose", tmp_path)
