@@ -977,7 +977,12 @@ hipError_t launch_tiles(const MxGemmArgs& a, int cus, hipStream_t st) {
 
 template <int EPI>
 hipError_t launch_epi(const MxGemmArgs& a, hipStream_t st) {
-    constexpr MxKernel FEW = EPI == MOE_MX_SWIGLU_QUANT ? ROWS16 : ROWS16_NARROW;   // 32 columns of h need 4 column tiles
+    // MXFP4 output has no narrow kernel (its blocks of 32 columns of h need four column
+    // tiles) and takes 16 rows, 4 tiles in its place.  Choosing among the other four by
+    // their times gives 32 rows, 4 tiles there, which is slower (us, 16 / 32 rows): 1 row
+    // of N = 4096, K = 1024 3.8 / 4.1, 8 of 8 groups 6.1 / 6.4, 8 rows in each of 32 groups
+    // of N = 4096, K = 512 9.9 / 14.5.
+    constexpr MxKernel FEW = EPI == MOE_MX_SWIGLU_QUANT ? ROWS16 : ROWS16_NARROW;
     int cus = 0;
     const hipError_t e = cu_count(cus);
     if (e != hipSuccess) return e;
