@@ -375,6 +375,9 @@ struct BackwardLaunch {
     template <int NV, bool VEC, bool WAVE_ROW>
     void operator()() const {
         const dim3 grid(backward_blocks(a.T, a.d)), block(row_threads(a.d, BACKWARD_NARROW));
+        // two bytes a value for an FP32 dx too: of 64 to 128 MiB it is better stored plainly
+        // for its reader (a quantisation of it right after; so / plainly: 94 MiB with dh
+        // 106 / 103 us, without 89 / 84, 123 MiB 130 / 128) and no worse alone (85 / 85)
         if (streamed(a.T * a.d * 2))
             hipLaunchKernelGGL((add_rmsnorm_backward_kernel<NV, VEC, WAVE_ROW, true>), grid, block, 0, st, a);
         else
