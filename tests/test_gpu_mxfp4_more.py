@@ -4,7 +4,7 @@ import torch
 
 import sigmoid_top_routing_02_amd as moe
 from helpers import dev, say
-from test_gpu_mxfp4 import F8, offsets, operands, ref_product
+from test_gpu_mxfp4 import F8, check_quant, offsets, operands, ref_product
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,119 @@ def test_more_columns_than_a_few_row_launch_takes():
     whole = N // period * period
     assert (out[:, :whole].view(M, -1, period) == want[:, None]).all()
     assert torch.equal(out[:, whole:], want[:, :N - whole])
+
+
+# ------------------------------------------------------------------ large outputs
+
+def _bits(t):
+    return t.view({2: torch.int16, 4: torch.int32, 1: torch.uint8}[t.element_size()])
+
+
+@pytest.mark.parametrize("rows,cols", [(17700, 7168), (61681, 2080), (4100001, 32)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quant_and_back_past_the_caches(rows, cols, dtype):
+    """More than 64 MiB of output, which is stored past the caches: bit for bit what calls on a few rows at a
+    time give, and the values back."""
+    dev()
+    say(f"  {rows} x {cols} {dtype}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    x = torch.randn((rows, cols), generator=g, device="cuda")
+    x.mul_(torch.exp2(torch.randint(-20, 20, (rows, 1), generator=g, device="cuda").float()))
+    x = x.to(dtype)
+    x[::1009, 5], x[::2003, 31] = float("nan"), -float("inf")
+    q, s = moe.mxfp4_quant_1x32(x)
+    v = {d: moe.mxfp4_dequant_1x32(q, s, dtype=d) for d in (torch.bfloat16, torch.float32)}
+    torch.cuda.synchronize()
+    step = max(1, 2 ** 22 // cols)                       # outputs of under 64 MiB
+    check_quant(x[:step])
+    check_quant(x[rows - step:])
+    for at in range(0, rows, step):
+        part = slice(at, min(at + step, rows))
+        pq, ps = moe.mxfp4_quant_1x32(x[part])
+        assert torch.equal(pq, q[part]) and torch.equal(ps, s[part]), at
+        for d, t in v.items():
+            assert torch.equal(_bits(moe.mxfp4_dequant_1x32(pq, ps, dtype=d)), _bits(t[part])), (at, d)
+
+
+@pytest.mark.parametrize("rows,cols", [(17700, 7168), (550001, 128)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_fp8_dequant_past_the_caches(rows, cols, out):
+    dev()
+    say(f"  {rows} x {cols} {out}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    q = torch.randint(0, 256, (rows, cols), generator=g, device="cuda", dtype=torch.int32).to(torch.uint8)
+    s = torch.rand((rows, cols // 128), generator=g, device="cuda") + 0.1
+    v = moe.fp8_dequant_1x128(q, s, dtype=out)
+    torch.cuda.synchronize()
+    step = max(1, 2 ** 22 // cols)
+    for at in range(0, rows, step):
+        part = slice(at, min(at + step, rows))
+        want = (q[part].view(torch.float8_e4m3fn).float() * s[part].repeat_interleave(128, 1)).to(out)
+        nan = torch.isnan(want)
+        assert torch.equal(torch.isnan(v[part]), nan) and torch.equal(v[part][~nan], want[~nan]), at
+
+
+PERIOD, WIDE = 4099, 4096           # the rows that the largest cases repeat, and their width
+
+
+def _repeated(t, rows):
+    """[rows, ..] of t's rows over and over."""
+    out = torch.empty((rows, *t.shape[1:]), dtype=t.dtype, device="cuda")
+    whole = rows // PERIOD * PERIOD
+    out[:whole].view(-1, *t.shape).copy_(t.expand(whole // PERIOD, *t.shape))
+    out[whole:] = t[:rows - whole]
+    return out
+
+
+def _repeats(got, want):
+    """Whether got's rows are want's over and over, a GiB or so at a time."""
+    whole, at = got.shape[0] // PERIOD * PERIOD, 0
+    per = max(1, 2 ** 30 // (want.numel() * want.element_size())) * PERIOD
+    while at < whole:
+        part = _bits(got[at:min(at + per, whole)])
+        if not bool((part.view(-1, *want.shape) == _bits(want)).all()):
+            return False
+        at += per
+    return torch.equal(_bits(got[whole:]), _bits(want[:got.shape[0] - whole]))
+
+
+def _small(dtype):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    return torch.randn((PERIOD, WIDE), generator=g, device="cuda").to(dtype)
+
+
+# Rows whose threads pass the 2^32 of a launch: 8 values a thread, and for bf16 two steps of the grid at once.
+@pytest.mark.parametrize("dtype,values", [(torch.float32, 2 ** 35), (torch.bfloat16, 2 ** 36)])
+def test_quant_that_passes_a_launch(dtype, values):
+    dev()
+    torch.cuda.empty_cache()
+    rows = values // WIDE + 333
+    say(f"  {rows} x {WIDE} {dtype}")
+    x = _small(dtype)
+    pq, ps = moe.mxfp4_quant_1x32(x)
+    q, s = moe.mxfp4_quant_1x32(_repeated(x, rows))
+    torch.cuda.synchronize()
+    assert _repeats(q, pq) and _repeats(s, ps)
+    del q, s
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("which", ["mxfp4", "fp8"])
+@pytest.mark.parametrize("out,values", [(torch.float32, 2 ** 34), (torch.bfloat16, 2 ** 35)])
+def test_dequant_that_passes_a_launch(which, out, values):
+    dev()
+    torch.cuda.empty_cache()
+    rows = values // WIDE + 333
+    say(f"  {which} {rows} x {WIDE} {out}")
+    quant, back = {"mxfp4": (moe.mxfp4_quant_1x32, moe.mxfp4_dequant_1x32),
+                   "fp8": (moe.fp8_quant_1x128, moe.fp8_dequant_1x128)}[which]
+    pq, ps = quant(_small(torch.bfloat16))
+    want = back(pq, ps, dtype=out)
+    v = back(_repeated(pq, rows), _repeated(ps, rows), dtype=out)
+    torch.cuda.synchronize()
+    assert _repeats(v, want)
+    del v
+    torch.cuda.empty_cache()
