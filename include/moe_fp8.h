@@ -69,8 +69,9 @@ typedef enum {
     MOE_MX_STORE_F32 = 0,    /* out = C, FP32 [M_total, N] */
     MOE_MX_STORE_BF16 = 1,   /* out = C, bf16 [M_total, N] */
     MOE_MX_SWIGLU_BF16 = 2,  /* out = h = SiLU(C_gate) * C_up, bf16 [M_total, N/2] */
-    MOE_MX_SWIGLU_QUANT = 3  /* the same h, quantised as by mxfp4_quant_1x32 into
-                                out_q [M_total, N/4 bytes] + out_scale [M_total, N/64] */
+    MOE_MX_SWIGLU_QUANT = 3  /* h in FP32, not rounded to bf16 first, quantised as by
+                                mxfp4_quant_1x32 into out_q [M_total, N/4 bytes] +
+                                out_scale [M_total, N/64] */
 } moe_mx_epilogue;
 
 const char* moe_status_string(int status);
@@ -556,7 +557,10 @@ int fp8_dequant_1x128(const uint8_t* q, const float* scale, int64_t rows, int co
  *        projection's rows [128j, 128j+128), the next 128 the up projection's.
  *        out is NULL for MOE_MX_SWIGLU_QUANT; out_q and out_scale are NULL for
  *        the others.
- * One launch and no workspace.  Limits: 1 <= G <= 1024, 0 <= M_total <= 2^31 - 2^16,
+ * One launch and no workspace.  The order in which a row's products are added up
+ * follows from G, M_total, N, K and the epilogue alone: the same call gives the
+ * same bits, but the same row in a call of other sizes may differ in its last ones.
+ * Limits: 1 <= G <= 1024, 0 <= M_total <= 2^31 - 2^16,
  * N >= 1 (N % 256 == 0 for SwiGLU), K a multiple of 32 up to 65536, a_rows * K / 2
  * and (N + 256) * K / 2 at most 4294901760 (32-bit offsets inside A and inside
  * one group's B), (ceil(M_total / 128) + G) * ceil(N / 256) < 2^31, M_total <=

@@ -34,9 +34,13 @@ inline bool mx_launches(MxRows r, int64_t M, int G, int N) {
 // fitted to 445 measured calls, 1 to 256 groups of 1 to 4096 rows, even and skewed,
 // N = 256 to 14336, K = 1024 to 32768, weights from HBM and from the caches; the choice
 // costs 1.4 % over the fastest kernel on the average and 37 % at most.  The host
-// knows the groups' sizes on the average only.  c is the number of 512-value chunks
-// of K; a round is a block (a tile) on every CU, and a call's last round counts
-// whole while there are few of them.
+// knows the groups' sizes on the average only, and all groups of those calls had rows
+// (but for a few of the skewed ones): where most are empty a large group goes to a
+// kernel for few rows, which takes B once per row tile.  4 of 256 groups with 512
+// rows each, N = 4096, K = 2048: 105 us, 21 without the empty ones; 16 with 256 rows
+// 140 and 32.  A caller that knows such groups leaves them out.  c is the number of
+// 512-value chunks of K; a round is a block (a tile) on every CU, and a call's last
+// round counts whole while there are few of them.
 //   16 rows, 2 column tiles: 3.8 + 0.4 c a round     16 rows, 4: 4.2 + 0.69 c
 //   32 rows, 4 column tiles: 3.8 + 0.8 c             64 rows, 4: 4 + 1.19 c
 //   whole tiles: 8.8 + 1.8 c up to 8.8 + 3.3 c when the round is full

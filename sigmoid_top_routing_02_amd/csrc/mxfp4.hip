@@ -11,9 +11,10 @@
 //
 // All three stream HBM and write what they write once: every access of a wave is
 // one contiguous run, at most 16 bytes a lane, and large outputs are stored
-// non-temporally (streamed).  On 32768 x 7168 values: quantised from FP32 in 179 us
-// (6.0 TB/s), from bf16 in 99 us (6.0); back to FP32 147 us (7.2 TB/s), to bf16 86 us
-// (6.9); FP8 to FP32 167 us (7.1), to bf16 101 us (7.0).
+// non-temporally (streamed).  On 32768 x 7168 values, bytes read and written: quantised
+// from FP32 in 179 us (5.9 TB/s), from bf16 in 98 us (6.1); FP8 to FP32 167 us (7.1),
+// to bf16 103 us (6.9); back to FP32 148 us (7.2) and to bf16 86 us (6.9) in a stream
+// of such calls alone, to FP32 198 us (5.4) right after a quantisation each.
 #include "device_math.h"
 #include "kernels.h"
 #include "streaming.h"
@@ -110,9 +111,9 @@ __device__ __forceinline__ v4u pack_values(const float* v) {
 
 // Exact: an E2M1 value times a power of two is a bf16 and a binary32 value
 // (subnormals included), but for 4 and 6 times the scale 2^127, which no
-// quantiser output has and which overflow to infinity.  FP32: 146 us at 32768 x
-// 7168 (6.4 TB/s; 199 us with 8 values a lane, whose two 16-byte stores each skip
-// every other 16 bytes).
+// quantiser output has and which overflow to infinity.  (8 FP32 values a lane, whose
+// two 16-byte stores each skip every other 16 bytes, lost: 199 us against 148 in a
+// stream of calls on 32768 x 7168 values.)
 template <bool OUT_F32, bool NT>
 __global__ __launch_bounds__(256) void mxfp4_dequant_kernel(const void* __restrict__ q,
                                                             const uint8_t* __restrict__ scale, int64_t lanes,

@@ -126,9 +126,9 @@ __device__ __forceinline__ float row_sum(float s, float (*part)[16], int flip) {
 
 // A block is one row (WAVE_ROW: each of its four waves is one); only a grid that
 // would pass the largest one makes it take more.  16384 rows of 7168 bf16 values
-// with residual: 196 us with the FP8 copy (5.4 TB/s), 164 us without (5.75 TB/s),
-// above the 4.9 TB/s of a plain copy, since the outputs are stored non-temporally
-// and leave the caches to the inputs (211 us with plain stores; 256 rows 6.0 us
+// with residual: 196 us with the FP8 copy (5.4 TB/s), 164 us without (5.75 TB/s;
+// the library's row copy reaches 6.3).  The outputs are stored non-temporally and
+// leave the caches to the inputs (211 us with plain stores; 256 rows 6.0 us
 // against 6.8, and with a kernel that reads y right after 9.1 against 9.8).  Rows
 // in turn on 2048 resident blocks lost to one block a row, 234 us: the next row's
 // loads then wait for the last one's reduction.
@@ -212,7 +212,8 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddR
 
 // As the forward; each block keeps the sum of dy * xh of its rows in registers and
 // leaves it as one row of `part` at the end.  8192 rows of 7168 bf16 values with dh:
-// 98 us (4.8 TB/s, the rate of a plain copy) and 6 us for dw_reduce_kernel.
+// 98 us (4.8 TB/s, where a copy reaches 6.3: a block asks for its next row only
+// after the last one's reduction and stores) and 6 us for dw_reduce_kernel.
 template <int NV, bool VEC, bool WAVE_ROW, bool NT>
 __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_backward_kernel(AddRmsnormBackwardArgs a) {
     __shared__ float part[2][16];
@@ -300,9 +301,10 @@ __device__ __forceinline__ float pairwise(const float (&x)[N]) {
 
 // dw[c] = sum of the partial rows, pairwise: 16 threads take every 16th row of a
 // column, eight loads at a time, then their sums are added (512 rows of 7168: 6 us,
-// as with the rows one after the other, whose dw has 1.2 to 2.1 times the error:
-// 2.4e-7 against 1.2e-7 of it at 32768 rows of 2048 FP32 values).
-constexpr int MOST_PARTIAL_ROWS = 2048;
+// in which two blocks read every line, the 64 bytes of a row that one takes being half).
+// Added one after the other they took the same time and left dw 1.2 to 2.1 times the
+// error (32768 rows of 2048 FP32 values: 2.4e-7 of it, now 1.2e-7).
+constexpr int MOST_PARTIAL_ROWS = 2048;                  // of backward_most
 __global__ __launch_bounds__(256) void dw_reduce_kernel(const float* __restrict__ part, int rows, int d,
                                                         float* __restrict__ dw) {
     __shared__ float sum[16][17];
