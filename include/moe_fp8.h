@@ -142,6 +142,59 @@ int moe_seq_balance_loss(const float* scores, const int32_t* topk_idx, int64_t T
                          int seq_len, float alpha, float* loss, void* ws, size_t ws_bytes,
                          moe_stream_t stream);
 
+/* moe_balance_loss, moe_balance_loss_backward -- the same loss (moe_seq_balance_loss
+ * above) over sequences of any lengths packed one after the other, with the counts
+ * that it and the bias update take, and its gradient with respect to the router's
+ * logits x (scores = sigmoid(x)).  Sequence q is the L_q tokens [seq_start[q],
+ * seq_start[q+1]); with p[t,i] = scores[t,i] / sum_j scores[t,j] (0 where the sum is 0):
+ *   seq_count[q,i]  = #{(t,k) : t in q, topk_idx[t,k] = i}          (n)
+ *   f[q,i] = E n / (K L_q),  P[q,i] = (1/L_q) sum_t p[t,i]
+ *   loss[q] = alpha * sum_i f P                                     (0 if L_q = 0)
+ *   expert_count[i] = sum_q seq_count[q,i]   (what moe_bias_update takes)
+ *   dlogits[t,i] = dlogits_in[t,i] + dloss[q] * alpha / L_q * p[t,i] * (1 - scores[t,i])
+ *                  * (f[q,i] - sum_j f[q,j] p[t,j])
+ * The counts are held fixed in the gradient, as the choice of the experts is
+ * elsewhere.  Tokens before seq_start[0] and from seq_start[n_seq] on (padding) are
+ * in no sequence: not counted, and dlogits = dlogits_in there.  moe_seq_balance_loss
+ * gives the same loss for equal lengths but for the order of its sums.
+ *
+ * scores FP32 [T,E]; topk_idx int32 [T,K] (values outside [0,E) are not counted);
+ * seq_start int32 [n_seq+1] (device), non-decreasing, values held inside [0, T];
+ * NULL: one sequence of all T tokens (n_seq = 1), the loss of the whole batch.
+ * loss FP32 [n_seq], seq_count int32 [n_seq,E], expert_count int32 [E] or NULL;
+ * dloss FP32 [n_seq], the gradient of each loss (NULL: ones); dlogits_in FP32 [T,E]
+ * (NULL: zeros), dlogits FP32 [T,E], which may be dlogits_in itself.  ws: scratch of
+ * moe_balance_loss_workspace_bytes(T, n_seq) bytes, no setup needed.  T = 0 gives
+ * zeros.  Nothing is read back to the host, so both calls can be captured in a graph
+ * whose replays take other starts.
+ * Limits: 0 <= T <= 2^30, 1 <= n_seq <= 2^20, 1 <= E <= 256, 1 <= K <= min(E, 16).
+ */
+size_t moe_balance_loss_workspace_bytes(int64_t T, int n_seq);   /* 0 outside the limits */
+int moe_balance_loss(const float* scores, const int32_t* topk_idx, const int32_t* seq_start, int n_seq, int64_t T, int E,
+                     int K, float alpha, float* loss, int32_t* seq_count, int32_t* expert_count, void* ws,
+                     size_t ws_bytes, moe_stream_t stream);
+int moe_balance_loss_backward(const float* scores, const int32_t* seq_count, const int32_t* seq_start, int n_seq,
+                              int64_t T, int E, int K, float alpha, const float* dloss, const float* dlogits_in,
+                              float* dlogits, moe_stream_t stream);
+
+/* moe_router_logits_backward -- the router's backward from a gradient of all its
+ * logits (x = u . e), such as the balance loss's, where moe_router_backward takes the
+ * gates', K values a token:
+ *   du = du_in + dlogits . e,   de = de_in + dlogits^T . u
+ * dlogits FP32 [T,E], u bf16 [T,d], centroids (e) bf16 [E,d]; du_in, du FP32 [T,d] and
+ * de_in, de FP32 [E,d]; du_in or de_in NULL: zeros; du or de NULL: not asked for (not
+ * both).  du may be du_in itself and de de_in, so that the sums go on from
+ * moe_router_backward's outputs in place.  The products are exact and summed in FP32
+ * in an order that depends on T, d and E alone.  Infinite values of u or the centroids
+ * give NaN.  ws: scratch of moe_router_logits_backward_workspace_bytes(T, d, E) bytes
+ * (no setup needed; may be NULL when de is).
+ * Limits: 0 <= T <= 2^24, d % 128 == 0, d <= 65536, 1 <= E <= 256.
+ */
+size_t moe_router_logits_backward_workspace_bytes(int64_t T, int d, int E);   /* 0 outside the limits */
+int moe_router_logits_backward(const float* dlogits, const void* u_bf16, const void* centroids_bf16, int64_t T, int d,
+                               int E, const float* du_in, const float* de_in, float* du, float* de, void* ws,
+                               size_t ws_bytes, moe_stream_t stream);
+
 /* ------------------------------------------------------------------ dispatch
  * moe_dispatch -- turns the routing into GEMM rows.  No token is ever dropped
  * ([LINEAGE] "The idea", load-balancing bullet): there is no capacity limit.
@@ -290,6 +343,19 @@ int grouped_gemm_fp8_blockscaled_noalloc(const uint8_t* a_q, const float* a_scal
                                          const float* b_scale, int N, int K, int epi, float* out,
                                          uint8_t* out_q, float* out_scale, moe_stream_t stream);
 
+/* grouped_gemm_fp8_swiglu_zq -- grouped_gemm_fp8_blockscaled with MOE_EPI_SWIGLU_QUANT,
+ * keeping C, the SwiGLU's input z that a backward pass needs, in 8 bits: z_q and
+ * z_scale are fp8_quant_1x128 of the FP32 z that MOE_EPI_SWIGLU_QUANT_Z writes, bit for
+ * bit, in a quarter of its bytes and without writing it.  h_q E4M3 [M_total, N/2],
+ * h_scale FP32 [M_total, N/256], z_q E4M3 [M_total, N], z_scale FP32 [M_total, N/128];
+ * h as MOE_EPI_SWIGLU_QUANT's, bit for bit.  Other arguments, scratch and limits as
+ * there (N % 256 == 0).  moe_swiglu_backward_zq and moe_wgrad_operands_zq take z_q.
+ */
+int grouped_gemm_fp8_swiglu_zq(const uint8_t* a_q, const float* a_scale, const int32_t* a_row_index,
+                               const int32_t* group_offset, int G, int64_t M_total, const uint8_t* b_q,
+                               const float* b_scale, int N, int K, uint8_t* h_q, float* h_scale, uint8_t* z_q,
+                               float* z_scale, void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* moe_fp8_mfma_accumulation_probe -- a measurement beside the GEMM, not a
  * step of the layer.  [IFS] FP8-accumulation paragraph: FP8 products summed
  * inside a matrix core with limited accumulation precision lose accuracy over
@@ -403,6 +469,14 @@ int moe_gate_backward(const float* dh, const float* y, int64_t shared_row0, cons
 int moe_swiglu_backward(const float* z, const float* dh_row, int64_t R, int I, uint8_t* dz_q, float* dz_scale,
                         moe_stream_t stream);
 
+/* moe_swiglu_backward_zq -- moe_swiglu_backward from z kept in 8 bits
+ * (grouped_gemm_fp8_swiglu_zq): z = E4M3(z_q) * z_scale, then the same.  z_q E4M3
+ * [R, 2I], z_scale FP32 [R, 2I/128]; dz_q may be z_q and dz_scale z_scale.
+ * Limits: R < 2^31, I % 128 == 0, I <= 65536.
+ */
+int moe_swiglu_backward_zq(const uint8_t* z_q, const float* z_scale, const float* dh_row, int64_t R, int I,
+                           uint8_t* dz_q, float* dz_scale, moe_stream_t stream);
+
 /* moe_router_backward --
  *   du[t] = dh[t] + dx[shared_row0 + t] + sum_k dx[slot_row[t,k]]
  *           + sum_k dlogit[t,k] * e[topk_idx[t,k]]               (FP32, in that order)
@@ -457,6 +531,15 @@ int moe_wgrad_operands(const float* dh, const float* topk_gate, const int32_t* s
                        const int32_t* kb_start, int G, int n_kb, int64_t T, int K, int d, int I,
                        int64_t shared_row0, uint8_t* dyT_q, float* dyT_scale, uint8_t* hT_q, float* hT_scale,
                        uint8_t* dzT_q, float* dzT_scale, uint8_t* xT_q, float* xT_scale, moe_stream_t stream);
+
+/* moe_wgrad_operands_zq -- the same from z kept in 8 bits (z_q, z_scale as
+ * grouped_gemm_fp8_swiglu_zq writes them): h and dz are of z = E4M3(z_q) * z_scale. */
+int moe_wgrad_operands_zq(const float* dh, const float* topk_gate, const int32_t* slot_row, const int32_t* row_token,
+                          const uint8_t* z_q, const float* z_scale, const float* dh_row, const void* u_bf16,
+                          const int32_t* group_offset, const int32_t* kb_start, int G, int n_kb, int64_t T, int K,
+                          int d, int I, int64_t shared_row0, uint8_t* dyT_q, float* dyT_scale, uint8_t* hT_q,
+                          float* hT_scale, uint8_t* dzT_q, float* dzT_scale, uint8_t* xT_q, float* xT_scale,
+                          moe_stream_t stream);
 
 /* moe_wgrad -- the expert weight gradients from moe_wgrad_operands' buffers:
  * for every group g, dW2[g] = GEMM(dY^T_g, h^T_g) FP32 [d, I] and
@@ -516,6 +599,36 @@ size_t moe_add_rmsnorm_backward_workspace_bytes(int64_t T, int d);
 int moe_add_rmsnorm_backward(const void* dy, int dy_dt, const void* h, int h_dt, const void* weight, int w_dt,
                              const float* rstd, const void* dh, int64_t T, int d, void* dx, int dx_dt, float* dw,
                              void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------ residual + layer norm
+ * moe_add_layernorm -- as moe_add_rmsnorm, with the mean taken off and a bias:
+ *   h    = x + residual                      (FP32; h = x when residual is NULL)
+ *   mean = mean(h),  rstd = 1 / sqrt(mean((h - mean)^2) + eps)
+ *                                            (FP32, of the unrounded h; the squares
+ *                                            are summed about the mean)
+ *   y    = bf16((h - mean) * rstd * weight + bias)
+ *   q, scale = fp8_quant_1x128(y), bit for bit
+ * bias [d] of w_dt, or NULL; mean and rstd FP32 [T] (what the backward takes), each
+ * NULL when not asked for; everything else as there, what may overlap included.  A row
+ * of equal values with eps = 0 gives NaN.
+ * Limits: 1 <= d <= 16384, d % 128 == 0 with q, eps >= 0.
+ */
+int moe_add_layernorm(const void* x, int x_dt, const void* residual, int res_dt, const void* weight, const void* bias,
+                      int w_dt, int64_t T, int d, float eps, void* h_out, void* y_bf16, uint8_t* q, float* scale,
+                      float* mean, float* rstd, moe_stream_t stream);
+
+/* moe_add_layernorm_backward -- as moe_add_rmsnorm_backward:
+ *   xh = (h - mean) * rstd,  g = dy * weight
+ *   dx = rstd * (g - mean(g) - xh * mean(g * xh)) + dh
+ *   dw = sum over the rows of dy * xh,  db = sum over the rows of dy
+ * db FP32 [d], NULL when not asked for.  T = 0 writes zeros to dw and db.
+ * Limits: 1 <= d <= 16384.
+ */
+/* 0 outside the call's limits (T < 1, d outside [1, 16384]). */
+size_t moe_add_layernorm_backward_workspace_bytes(int64_t T, int d);
+int moe_add_layernorm_backward(const void* dy, int dy_dt, const void* h, int h_dt, const void* weight, int w_dt,
+                               const float* mean, const float* rstd, const void* dh, int64_t T, int d, void* dx,
+                               int dx_dt, float* dw, float* db, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* ------------------------------------------------------------------ MXFP4
  * OCP microscaling with E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their

@@ -40,6 +40,10 @@ EXPORTS = (
     "moe_wgrad_block_starts", "moe_wgrad_operands", "moe_wgrad_workspace_bytes", "moe_wgrad",
     "moe_add_rmsnorm", "moe_add_rmsnorm_backward_workspace_bytes", "moe_add_rmsnorm_backward",
     "mxfp4_quant_1x32", "mxfp4_dequant_1x32", "fp8_dequant_1x128", "grouped_gemm_mxfp4",
+    "moe_balance_loss_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
+    "moe_router_logits_backward_workspace_bytes", "moe_router_logits_backward",
+    "grouped_gemm_fp8_swiglu_zq", "moe_swiglu_backward_zq", "moe_wgrad_operands_zq",
+    "moe_add_layernorm", "moe_add_layernorm_backward_workspace_bytes", "moe_add_layernorm_backward",
 )
 
 
@@ -98,6 +102,18 @@ def load_library(path: str = LIB_PATH):
         "mxfp4_dequant_1x32": ([P, P, I64, I32, P, I32, P], I32),
         "fp8_dequant_1x128": ([P, P, I64, I32, P, I32, P], I32),
         "grouped_gemm_mxfp4": ([P, P, I64, P, P, I32, I64, P, P, I32, I32, I32, P, P, P, P], I32),
+        "moe_balance_loss_workspace_bytes": ([I64, I32], SZ),
+        "moe_balance_loss": ([P, P, P, I32, I64, I32, I32, F32, P, P, P, P, SZ, P], I32),
+        "moe_balance_loss_backward": ([P, P, P, I32, I64, I32, I32, F32, P, P, P, P], I32),
+        "moe_router_logits_backward_workspace_bytes": ([I64, I32, I32], SZ),
+        "moe_router_logits_backward": ([P, P, P, I64, I32, I32, P, P, P, P, P, SZ, P], I32),
+        "grouped_gemm_fp8_swiglu_zq": ([P, P, P, P, I32, I64, P, P, I32, I32, P, P, P, P, P, SZ, P], I32),
+        "moe_swiglu_backward_zq": ([P, P, P, I64, I32, P, P, P], I32),
+        "moe_wgrad_operands_zq": ([P, P, P, P, P, P, P, P, P, P, I32, I32, I64, I32, I32, I32, I64,
+                                   P, P, P, P, P, P, P, P, P], I32),
+        "moe_add_layernorm": ([P, I32, P, I32, P, P, I32, I64, I32, F32, P, P, P, P, P, P, P], I32),
+        "moe_add_layernorm_backward_workspace_bytes": ([I64, I32], SZ),
+        "moe_add_layernorm_backward": ([P, I32, P, I32, P, I32, P, P, P, I64, I32, P, I32, P, P, P, SZ, P], I32),
         "moe_wgrad": ([P, I32, I32, I32, I32, P, P, P, P, P, P, P, P, P, P, P, SZ, P], I32),
     }
     for name, (args, res) in sig.items():
@@ -544,6 +560,29 @@ def moe_wgrad(dh, topk_gate, slot_row, row_token, z, dh_row, u, group_offset, sh
     read back to the host: the buffers are sized by the bound
     ceil(R / 128) + G of the row-block count, so the whole chain can be
     captured in a graph."""
+    return _wgrad(dh, topk_gate, slot_row, row_token, z, None, dh_row, u, group_offset, shared_row0)
+
+
+def moe_wgrad_zq(dh, topk_gate, slot_row, row_token, z_q, z_scale, dh_row, u, group_offset, shared_row0=-1):
+    """As moe_wgrad, from z kept in 8 bits (grouped_gemm_fp8_swiglu_zq): z_q uint8 [R, 2I], z_scale f32
+    [R, 2I/128]; the operands come from moe_wgrad_operands_zq."""
+    if z_q.dim() != 2:
+        raise MoEError(f"z_q: shape {tuple(z_q.shape)}, expected two dimensions")
+    R, I2 = z_q.shape
+    _want(z_q, torch.uint8, (R, I2), "z_q")
+    _want(z_scale, torch.float32, (R, I2 // 128), "z_scale")
+    _want(dh_row, torch.float32, (R, I2 // 2), "dh_row")
+    T, d = dh.shape
+    K = topk_gate.shape[1]
+    _want(dh, torch.float32, (T, d), "dh")
+    _want(u, torch.bfloat16, (T, d), "u")
+    _want(topk_gate, torch.float32, (T, K), "topk_gate")
+    _want(slot_row, torch.int32, (T, K), "slot_row")
+    _want(row_token, torch.int32, (R,), "row_token")
+    return _wgrad(dh, topk_gate, slot_row, row_token, z_q, z_scale, dh_row, u, group_offset, shared_row0)
+
+
+def _wgrad(dh, topk_gate, slot_row, row_token, z, z_scale, dh_row, u, group_offset, shared_row0):
     T, d = dh.shape
     K = topk_gate.shape[1]
     R, I2 = z.shape
@@ -565,10 +604,12 @@ def moe_wgrad(dh, topk_gate, slot_row, row_token, z, dh_row, u, group_offset, sh
     L = load_library()
     kbs = torch.empty(G + 1, dtype=torch.int32, device=dev)
     _check(L.moe_wgrad_block_starts(_ptr(group_offset), G, _ptr(kbs), _stream()), "moe_wgrad_block_starts")
-    _check(L.moe_wgrad_operands(_ptr(dh), _ptr(topk_gate), _ptr(slot_row), _ptr(row_token), _ptr(z), _ptr(dh_row),
-                                _ptr(u), _ptr(group_offset), _ptr(kbs), G, n_kb, T, K, d, I, shared_row0,
-                                *(_ptr(bufs[k]) for k in ("dyT_q", "dyT_s", "hT_q", "hT_s", "dzT_q", "dzT_s",
-                                                           "xT_q", "xT_s")), _stream()), "moe_wgrad_operands")
+    name = "moe_wgrad_operands" if z_scale is None else "moe_wgrad_operands_zq"
+    zs = (z,) if z_scale is None else (z, z_scale)
+    _check(getattr(L, name)(*(_ptr(t) for t in (dh, topk_gate, slot_row, row_token, *zs, dh_row, u, group_offset, kbs)),
+                            G, n_kb, T, K, d, I, shared_row0,
+                            *(_ptr(bufs[k]) for k in ("dyT_q", "dyT_s", "hT_q", "hT_s", "dzT_q", "dzT_s",
+                                                       "xT_q", "xT_s")), _stream()), name)
     dw13 = _new((G, 2 * I, d), torch.float32, dh)
     dw2 = _new((G, d, I), torch.float32, dh)
     ws = _new((max(L.moe_wgrad_workspace_bytes(G, d, I), 256),), torch.uint8, dh)
@@ -790,3 +831,242 @@ def grouped_gemm_mxfp4(a_q, a_scale, group_offset, M_total, b_q, b_scale, epi=MO
     if st:
         _check(st, "grouped_gemm_mxfp4")
     return (out_q, out_scale) if epi == MOE_MX_SWIGLU_QUANT else out
+
+
+# ---------------------------------------------------------------- residual + layer norm
+LayerNorm = namedtuple("LayerNorm", "y h mean rstd q scale")
+
+
+def moe_add_layernorm(x, weight, eps, bias=None, residual=None, quant=False, h_out=None, y=None, q=None, scale=None,
+                      mean=None, rstd=None):
+    """h = x + residual, y = bf16((h - mean(h)) / sqrt(var(h) + eps) * weight + bias) and, with quant, the FP8
+    1x128 codes and scales of y.  x, residual bf16/f32 [T,d], weight and bias (or None) bf16/f32 [d]
+    -> LayerNorm(y bf16 [T,d], h of residual's type [T,d] or None, mean f32 [T], rstd f32 [T],
+    q uint8 [T,d] or None, scale f32 [T,d/128] or None).  h_out may be residual, or x of the same type; y may
+    be x or residual where that is bf16."""
+    T, d, xd, dev = _rows(x, "x")
+    shape = x.shape
+    px = _in(x, x.dtype, shape, "x", dev)
+    wd = _dt(weight, "weight")
+    pw = _in(weight, weight.dtype, (d,), "weight", dev)
+    pb = None if bias is None else _in(bias, weight.dtype, (d,), "bias", dev)
+    pr = ph = pq = ps = None
+    rd = MOE_F32
+    if residual is not None:
+        rd = _dt(residual, "residual")
+        pr = _in(residual, residual.dtype, shape, "residual", dev)
+        h_out, ph = _out(h_out, residual.dtype, shape, "h_out", dev)
+    elif h_out is not None:
+        raise MoEError("moe_add_layernorm: h_out without a residual")
+    y, py = _out(y, torch.bfloat16, shape, "y", dev)
+    mean, pm = _out(mean, torch.float32, (T,), "mean", dev)
+    rstd, prs = _out(rstd, torch.float32, (T,), "rstd", dev)
+    if quant:
+        q, pq = _out(q, torch.uint8, shape, "q", dev)
+        scale, ps = _out(scale, torch.float32, (T, d // 128), "scale", dev)
+    elif q is not None or scale is not None:
+        raise MoEError("moe_add_layernorm: q or scale without quant")
+    L = _lib or load_library()
+    st = L.moe_add_layernorm(px, xd, pr, rd, pw, pb, wd, T, d, eps, ph, py, pq, ps, pm, prs, _raw_stream(dev))
+    if st:
+        _check(st, "moe_add_layernorm")
+    return LayerNorm(y, h_out, mean, rstd, q, scale)
+
+
+def moe_add_layernorm_backward(dy, h, weight, mean, rstd, dh=None, bias_grad=True, dx=None, dw=None, db=None,
+                               dx_dtype=None, ws=None):
+    """dy, h bf16/f32 [T,d], weight bf16/f32 [d], mean, rstd f32 [T], dh (the gradient of h_out) or None
+    -> (dx [T,d] of dh's type, else dx_dtype, else dy's; dw f32 [d]; db f32 [d], None without bias_grad).
+    dx is the gradient of x and of residual alike."""
+    T, d, yd, dev = _rows(dy, "dy")
+    shape = dy.shape
+    if dx_dtype is None:
+        dx_dtype = dh.dtype if dh is not None else dx.dtype if dx is not None else dy.dtype
+    dx, pdx = _out(dx, dx_dtype, shape, "dx", dev)
+    dw, pdw = _out(dw, torch.float32, (d,), "dw", dev)
+    pdb = None
+    if bias_grad:
+        db, pdb = _out(db, torch.float32, (d,), "db", dev)
+    elif db is not None:
+        raise MoEError("moe_add_layernorm_backward: db without bias_grad")
+    L = _lib or load_library()
+    if ws is None:
+        ws_bytes = max(L.moe_add_layernorm_backward_workspace_bytes(T, d), 16)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        pws = ws.data_ptr()
+    else:
+        ws_bytes, pws = ws.numel() * ws.element_size(), _in(ws, ws.dtype, ws.shape, "ws", dev)
+    pdh = None if dh is None else _in(dh, dx_dtype, shape, "dh", dev)
+    st = L.moe_add_layernorm_backward(
+        _in(dy, dy.dtype, shape, "dy", dev), yd, _in(h, h.dtype, shape, "h", dev), _dt(h, "h"),
+        _in(weight, weight.dtype, (d,), "weight", dev), _dt(weight, "weight"),
+        _in(mean, torch.float32, (T,), "mean", dev), _in(rstd, torch.float32, (T,), "rstd", dev), pdh, T, d, pdx,
+        _dt(dx, "dx"), pdw, pdb, pws, ws_bytes, _raw_stream(dev))
+    if st:
+        _check(st, "moe_add_layernorm_backward")
+    return dx, dw, db
+
+
+# ---------------------------------------------------------------- balance loss over packed sequences
+BalanceLoss = namedtuple("BalanceLoss", "loss seq_count expert_count")
+
+
+def _scratch(ws, nbytes, dev):
+    """(tensor, address, bytes) of a call's scratch, allocated where none is given."""
+    if ws is None:
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        return ws, ws.data_ptr(), max(nbytes, 16)
+    return ws, _in(ws, ws.dtype, ws.shape, "ws", dev), ws.numel() * ws.element_size()
+
+
+def _sequences(scores, seq_start):
+    """(T, E, n_seq, address of seq_start, GPU) of a balance loss's arguments."""
+    if scores.dim() != 2:
+        raise MoEError(f"scores: shape {tuple(scores.shape)}, expected two dimensions")
+    T, E = scores.shape
+    dev = _current(scores, "scores")
+    if E > _INT_MAX:
+        _too_large("scores' columns", E)
+    if seq_start is None:
+        return T, E, 1, None, dev
+    if seq_start.dim() != 1 or seq_start.numel() < 2:
+        raise MoEError(f"seq_start: shape {tuple(seq_start.shape)}, expected [n_seq + 1] with a sequence at least")
+    n_seq = seq_start.numel() - 1
+    if n_seq > _INT_MAX:
+        _too_large("sequences", n_seq)
+    return T, E, n_seq, _in(seq_start, torch.int32, (n_seq + 1,), "seq_start", dev), dev
+
+
+def moe_balance_loss(scores, topk_idx, alpha, seq_start=None, loss=None, seq_count=None, expert_count=None, ws=None):
+    """The balance loss of each of the sequences [seq_start[q], seq_start[q+1]) of a packed batch, and the
+    experts' counts.  scores f32 [T,E], topk_idx i32 [T,K], seq_start i32 [n_seq+1] on the device (None: one
+    sequence of all T tokens) -> BalanceLoss(loss f32 [n_seq], seq_count i32 [n_seq,E], expert_count i32 [E])."""
+    T, E, n_seq, pstart, dev = _sequences(scores, seq_start)
+    if topk_idx.dim() != 2:
+        raise MoEError(f"topk_idx: shape {tuple(topk_idx.shape)}, expected two dimensions")
+    K = topk_idx.shape[1]
+    if K > _INT_MAX:
+        _too_large("topk_idx's columns", K)
+    loss, pl = _out(loss, torch.float32, (n_seq,), "loss", dev)
+    seq_count, pc = _out(seq_count, torch.int32, (n_seq, E), "seq_count", dev)
+    expert_count, pe = _out(expert_count, torch.int32, (E,), "expert_count", dev)
+    L = _lib or load_library()
+    ws, pws, ws_bytes = _scratch(ws, L.moe_balance_loss_workspace_bytes(T, n_seq), dev)
+    st = L.moe_balance_loss(_in(scores, torch.float32, (T, E), "scores", dev), _in(topk_idx, torch.int32, (T, K), "topk_idx", dev),
+                            pstart, n_seq, T, E, K, alpha, pl, pc, pe, pws, ws_bytes, _raw_stream(dev))
+    if st:
+        _check(st, "moe_balance_loss")
+    return BalanceLoss(loss, seq_count, expert_count)
+
+
+def moe_balance_loss_backward(scores, seq_count, K, alpha, seq_start=None, dloss=None, dlogits_in=None, dlogits=None):
+    """The balance loss's gradient with respect to the router's logits, f32 [T,E], added to dlogits_in (None:
+    zeros; may be dlogits itself).  seq_count as moe_balance_loss gave it, dloss f32 [n_seq] the gradient of
+    each sequence's loss (None: ones)."""
+    T, E, n_seq, pstart, dev = _sequences(scores, seq_start)
+    if not 0 < K <= _INT_MAX:
+        raise MoEError(f"moe_balance_loss_backward: K={K}")
+    pd = None if dloss is None else _in(dloss, torch.float32, (n_seq,), "dloss", dev)
+    pi = None if dlogits_in is None else _in(dlogits_in, torch.float32, (T, E), "dlogits_in", dev)
+    dlogits, po = _out(dlogits, torch.float32, (T, E), "dlogits", dev)
+    L = _lib or load_library()
+    st = L.moe_balance_loss_backward(_in(scores, torch.float32, (T, E), "scores", dev),
+                                     _in(seq_count, torch.int32, (n_seq, E), "seq_count", dev), pstart, n_seq, T, E, K,
+                                     alpha, pd, pi, po, _raw_stream(dev))
+    if st:
+        _check(st, "moe_balance_loss_backward")
+    return dlogits
+
+
+def moe_router_logits_backward(dlogits, u, centroids, du_in=None, de_in=None, du=None, de=None, want_du=True,
+                               want_de=True, ws=None):
+    """dlogits f32 [T,E], u bf16 [T,d], centroids bf16 [E,d] -> (du f32 [T,d] = du_in + dlogits . centroids,
+    de f32 [E,d] = de_in + dlogits^T . u); du may be du_in and de de_in.  None in the place of one that is not
+    wanted."""
+    if dlogits.dim() != 2 or u.dim() != 2:
+        raise MoEError(f"dlogits: {tuple(dlogits.shape)}, u: {tuple(u.shape)}, expected [T, E] and [T, d]")
+    T, E = dlogits.shape
+    d = u.shape[1]
+    if E > _INT_MAX or d > _INT_MAX:
+        _too_large("E or d", max(E, d))
+    dev = _current(dlogits, "dlogits")
+    pdu = pde = pws = None
+    ws_bytes = 0
+    if want_du:
+        du, pdu = _out(du, torch.float32, (T, d), "du", dev)
+    elif du is not None or du_in is not None:
+        raise MoEError("moe_router_logits_backward: du or du_in without want_du")
+    L = _lib or load_library()
+    if want_de:
+        de, pde = _out(de, torch.float32, (E, d), "de", dev)
+        ws, pws, ws_bytes = _scratch(ws, L.moe_router_logits_backward_workspace_bytes(T, d, E), dev)
+    elif de is not None or de_in is not None:
+        raise MoEError("moe_router_logits_backward: de or de_in without want_de")
+    pui = None if du_in is None else _in(du_in, torch.float32, (T, d), "du_in", dev)
+    pei = None if de_in is None else _in(de_in, torch.float32, (E, d), "de_in", dev)
+    st = L.moe_router_logits_backward(_in(dlogits, torch.float32, (T, E), "dlogits", dev),
+                                      _in(u, torch.bfloat16, (T, d), "u", dev),
+                                      _in(centroids, torch.bfloat16, (E, d), "centroids", dev), T, d, E, pui, pei, pdu, pde,
+                                      pws, ws_bytes, _raw_stream(dev))
+    if st:
+        _check(st, "moe_router_logits_backward")
+    return (du if want_du else None), (de if want_de else None)
+
+
+# ---------------------------------------------------------------- activations kept in 8 bits
+def grouped_gemm_fp8_swiglu_zq(a_q, a_scale, group_offset, M_total, b_q, b_scale, a_row_index=None, h_q=None,
+                               h_scale=None, z_q=None, z_scale=None, ws=None):
+    """grouped_gemm_fp8_blockscaled with MOE_EPI_SWIGLU_QUANT that keeps z in 8 bits
+    -> (h_q uint8 [M_total,N/2], h_scale f32 [M_total,N/256], z_q uint8 [M_total,N], z_scale f32 [M_total,N/128])."""
+    if b_q.dim() != 3 or a_q.dim() != 2:
+        raise MoEError(f"a_q: {tuple(a_q.shape)}, b_q: {tuple(b_q.shape)}, expected [*, K] and [G, N, K]")
+    G, N, K = b_q.shape
+    rows = a_q.shape[0]
+    if G > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
+        _too_large("G, N or K", max(G, N, K))
+    dev = _current(b_q, "b_q")
+    pi = None
+    if a_row_index is not None:
+        if a_row_index.dtype is not torch.int32 or a_row_index.numel() < M_total:
+            raise MoEError(f"a_row_index: {a_row_index.dtype} with {a_row_index.numel()} entries, "
+                           f"expected int32 with at least M_total = {M_total}")
+        pi = _in(a_row_index, torch.int32, a_row_index.shape, "a_row_index", dev)
+    elif rows < M_total:
+        raise MoEError(f"a_q holds {rows} rows, fewer than M_total = {M_total}")
+    if group_offset.dtype is not torch.int32 or group_offset.numel() < G + 1:
+        raise MoEError("group_offset must be int32 with G+1 entries")
+    h_q, phq = _out(h_q, torch.uint8, (M_total, N // 2), "h_q", dev)
+    h_scale, phs = _out(h_scale, torch.float32, (M_total, N // 256), "h_scale", dev)
+    z_q, pzq = _out(z_q, torch.uint8, (M_total, N), "z_q", dev)
+    z_scale, pzs = _out(z_scale, torch.float32, (M_total, N // 128), "z_scale", dev)
+    L = _lib or load_library()
+    ws, pws, ws_bytes = _scratch(ws, L.moe_gemm_workspace_bytes(G, M_total, N, K), dev)
+    st = L.grouped_gemm_fp8_swiglu_zq(
+        _in(a_q, torch.uint8, (rows, K), "a_q", dev), _in(a_scale, torch.float32, (rows, K // 128), "a_scale", dev), pi,
+        _in(group_offset, torch.int32, group_offset.shape, "group_offset", dev), G, M_total,
+        _in(b_q, torch.uint8, b_q.shape, "b_q", dev), _in(b_scale, torch.float32, (G, N // 128, K // 128), "b_scale", dev),
+        N, K, phq, phs, pzq, pzs, pws, ws_bytes, _raw_stream(dev))
+    if st:
+        _check(st, "grouped_gemm_fp8_swiglu_zq")
+    return h_q, h_scale, z_q, z_scale
+
+
+def moe_swiglu_backward_zq(z_q, z_scale, dh_row, dz_q=None, dz_scale=None):
+    """moe_swiglu_backward from z kept in 8 bits: z_q uint8 [R,2I], z_scale f32 [R,2I/128], dh_row f32 [R,I]
+    -> (dz_q uint8 [R,2I], dz_scale f32 [R,2I/128]), which may be z_q and z_scale themselves."""
+    if z_q.dim() != 2:
+        raise MoEError(f"z_q: shape {tuple(z_q.shape)}, expected two dimensions")
+    R, I2 = z_q.shape
+    if I2 > _INT_MAX:
+        _too_large("z_q's columns", I2)
+    dev = _current(z_q, "z_q")
+    dz_q, pq = _out(dz_q, torch.uint8, (R, I2), "dz_q", dev)
+    dz_scale, ps = _out(dz_scale, torch.float32, (R, I2 // 128), "dz_scale", dev)
+    L = _lib or load_library()
+    st = L.moe_swiglu_backward_zq(_in(z_q, torch.uint8, (R, I2), "z_q", dev),
+                                  _in(z_scale, torch.float32, (R, I2 // 128), "z_scale", dev),
+                                  _in(dh_row, torch.float32, (R, I2 // 2), "dh_row", dev), R, I2 // 2, pq, ps,
+                                  _raw_stream(dev))
+    if st:
+        _check(st, "moe_swiglu_backward_zq")
+    return dz_q, dz_scale

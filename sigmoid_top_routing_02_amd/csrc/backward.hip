@@ -175,6 +175,42 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(const float* __res
     }
 }
 
+// The same on z kept in 8 bits (codes [R, 2I], scales [R, 2I/128] in z's layout).
+__device__ __forceinline__ void decode8(const uint8_t* p, float s, float (&v)[8]) {
+    const uint2 c = *reinterpret_cast<const uint2*>(p);
+    const float4 a = e4m3_decode4(c.x), b = e4m3_decode4(c.y);
+    v[0] = a.x * s; v[1] = a.y * s; v[2] = a.z * s; v[3] = a.w * s;
+    v[4] = b.x * s; v[5] = b.y * s; v[6] = b.z * s; v[7] = b.w * s;
+}
+
+__global__ __launch_bounds__(256) void swiglu_backward_zq_kernel(const uint8_t* __restrict__ z_q,
+                                                                 const float* __restrict__ z_s,
+                                                                 const float* __restrict__ dh_row, int64_t R, int I,
+                                                                 uint8_t* __restrict__ dz_q, float* __restrict__ dz_s) {
+    const int nb = I / 128;
+    const int64_t total = R * nb * 16;
+    for (int64_t gi = (int64_t)blockIdx.x * 256 + threadIdx.x; gi - threadIdx.x < total;
+         gi += (int64_t)gridDim.x * 256) {
+        if (gi >= total) continue;          // whole 16-lane groups (total % 16 == 0)
+        const int64_t tile = gi >> 4;       // row * nb + h block: z's blocks of 256 and h's of 128 count alike
+        const int part = (int)(gi & 15);
+        float zg[8], zu[8], dh[8], dzg[8], dzu[8];
+        const uint8_t* zr = z_q + tile * 256 + part * 8;
+        decode8(zr, z_s[2 * tile], zg);
+        decode8(zr + 128, z_s[2 * tile + 1], zu);
+        load8_nt(dh_row + tile * 128 + part * 8, dh);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float sg = __builtin_amdgcn_rcpf(1.0f + __expf(-zg[i]));
+            dzu[i] = dh[i] * (zg[i] * sg);
+            dzg[i] = dh[i] * zu[i] * sg * (1.0f + zg[i] * (1.0f - sg));
+        }
+        uint8_t* qr = dz_q + tile * 256 + part * 8;
+        quant_tile8(dzg, part, qr, dz_s + 2 * tile);
+        quant_tile8(dzu, part, qr + 128, dz_s + 2 * tile + 1);
+    }
+}
+
 // du_t = dh_t + dx[shared_row0 + t] + sum_k dx[slot_row[t,k]] + sum_k dlogit_k e[idx[t,k]],
 // in that order, FP32; blocks of 128 threads x 4 columns of one token.
 template <int KMAX>
@@ -339,6 +375,16 @@ hipError_t launch_swiglu_backward(const float* z, const float* dh_row, int64_t R
     int64_t blocks = (threads + 255) / 256;
     if (blocks > 65536) blocks = 65536;
     hipLaunchKernelGGL(swiglu_backward_kernel, dim3((unsigned)blocks), dim3(256), 0, st, z, dh_row, R, I,
+                       dz_q, dz_s);
+    return hipGetLastError();
+}
+
+hipError_t launch_swiglu_backward_zq(const uint8_t* z_q, const float* z_s, const float* dh_row, int64_t R, int I,
+                                     uint8_t* dz_q, float* dz_s, hipStream_t st) {
+    const int64_t threads = R * (I / 128) * 16;
+    int64_t blocks = (threads + 255) / 256;
+    if (blocks > 65536) blocks = 65536;
+    hipLaunchKernelGGL(swiglu_backward_zq_kernel, dim3((unsigned)blocks), dim3(256), 0, st, z_q, z_s, dh_row, R, I,
                        dz_q, dz_s);
     return hipGetLastError();
 }

@@ -107,7 +107,227 @@ __global__ __launch_bounds__(256) void seq_balance_final_kernel(const BalancePar
     if (tid == 0) loss[q] = alpha * term[0];
 }
 
+// ---------------------------------------------------------------------------
+// The same loss over sequences of any lengths, with the counts that the gradient
+// and the bias update take, and its gradient with respect to the router's logits.
+// Sequence q holds the tokens [start[q], start[q+1]); with p = s / sum_j s_j,
+//     f_i = E n_i / (K L),  P_i = (1/L) sum_t p_ti,  loss_q = alpha sum_i f_i P_i,
+//     dlogit_ti = dloss_q alpha / L * p_ti (1 - s_ti) (f_i - sum_j f_j p_tj)
+// (the counts n are held fixed; s' = s (1 - s)).
+//
+// Forward.  Block c takes the tokens [c chunk, (c+1) chunk), one run of them for
+// each sequence that the chunk meets, and leaves the run's partial sums of p and
+// its counts as record c + q: along the chunks and sequences that meet, c + q grows
+// at every step, so no two runs share a record.  The chunk's counts over its runs
+// are kept too.  A second launch adds up each sequence's records, and the chunks'
+// counts.  Every order is fixed by the sizes and the starts.
+
+constexpr int RUN_WAVES = 16;
+constexpr int RUN_CHUNKS = 256;     // at most: one block per CU
+constexpr int RUN_LEAST = 64;       // tokens of a chunk at least
+
+// start[i], held inside [0, T]; without an array one sequence of all T tokens
+__device__ __forceinline__ int seq_start_at(const int32_t* __restrict__ start, int i, int n_seq, int T) {
+    if (!start) return i < n_seq ? 0 : T;
+    return min(max(start[i], 0), T);
+}
+
+// The first sequence that ends behind token t (n_seq if none does).
+__device__ __forceinline__ int seq_of(const int32_t* __restrict__ start, int n_seq, int T, int t) {
+    int lo = 0, hi = n_seq;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (seq_start_at(start, mid + 1, n_seq, T) > t) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+struct BalanceRun {                 // record of a run; [256] each, but a call's own E are in use
+    float p[256];
+    int32_t n[256];
+};
+
+// lane l of a wave holds the experts l + 64 j of a token
+__global__ __launch_bounds__(64 * RUN_WAVES) void balance_runs_kernel(
+    const float* __restrict__ s, const int32_t* __restrict__ idx, const int32_t* __restrict__ start, int n_seq, int T,
+    int E, int K, int chunk, BalanceRun* __restrict__ rec, int32_t* __restrict__ chunk_n) {
+    __shared__ int cnt[256];
+    __shared__ float psum[RUN_WAVES][256];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tb = blockIdx.x * chunk, te = min(T, tb + chunk);
+    int all = 0;                                      // thread = expert: counts over the chunk's runs
+    for (int q = seq_of(start, n_seq, T, tb); q < n_seq; ++q) {
+        const int rb = max(tb, seq_start_at(start, q, n_seq, T)), re = min(te, seq_start_at(start, q + 1, n_seq, T));
+        if (rb >= te) break;
+        if (rb >= re) {                               // an empty sequence has no record; nor have those behind it
+            q = max(q, seq_of(start, n_seq, T, rb) - 1);
+            continue;
+        }
+        if (tid < 256) cnt[tid] = 0;
+        __syncthreads();
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int t = rb + wave; t < re; t += RUN_WAVES) {
+            const float* row = s + (int64_t)t * E;
+            float v[4], sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = lane + 64 * j < E ? row[lane + 64 * j] : 0.0f;
+                sum += v[j];
+            }
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
+            if (sum != 0.0f) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[j] += v[j] / sum;
+            }
+            if (lane < K) {
+                const int e = idx[(int64_t)t * K + lane];
+                if ((unsigned)e < (unsigned)E) atomicAdd(&cnt[e], 1);      // integers: exact in any order
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) psum[wave][lane + 64 * j] = acc[j];
+        __syncthreads();
+        if (tid < E) {
+            float p = 0.0f;
+            for (int w = 0; w < RUN_WAVES; ++w) p += psum[w][tid];
+            rec[blockIdx.x + q].p[tid] = p;
+            rec[blockIdx.x + q].n[tid] = cnt[tid];
+            all += cnt[tid];
+        }
+        __syncthreads();
+    }
+    if (tid < E) chunk_n[blockIdx.x * 256 + tid] = all;
+}
+
+// One block per sequence, and one for the counts over all of them: thread = expert
+// and one of four parts of the records.
+__global__ __launch_bounds__(1024) void balance_sum_kernel(const BalanceRun* __restrict__ rec,
+                                                           const int32_t* __restrict__ chunk_n,
+                                                           const int32_t* __restrict__ start, int n_seq, int T, int E,
+                                                           int K, int chunk, float alpha, float* __restrict__ loss,
+                                                           int32_t* __restrict__ seq_count,
+                                                           int32_t* __restrict__ expert_count) {
+    __shared__ float ps[4][256];
+    __shared__ int ns[4][256];
+    const int e = threadIdx.x & 255, part = threadIdx.x >> 8, q = blockIdx.x;
+    if (q == n_seq) {
+        int n = 0;
+        if (e < E)
+            for (int c = part; c * chunk < T; c += 4) n += chunk_n[c * 256 + e];
+        ns[part][e] = n;
+        __syncthreads();
+        if (part == 0 && e < E) expert_count[e] = (ns[0][e] + ns[1][e]) + (ns[2][e] + ns[3][e]);
+        return;
+    }
+    const int b = seq_start_at(start, q, n_seq, T), L = max(seq_start_at(start, q + 1, n_seq, T) - b, 0);
+    float p = 0.0f;
+    int n = 0;
+    if (L > 0 && e < E) {
+        const int c0 = b / chunk, c1 = (b + L - 1) / chunk;
+        for (int c = c0 + part; c <= c1; c += 4) {
+            p += rec[c + q].p[e];
+            n += rec[c + q].n[e];
+        }
+    }
+    ps[part][e] = p;
+    ns[part][e] = n;
+    __syncthreads();
+    if (part == 0) {
+        p = (ps[0][e] + ps[1][e]) + (ps[2][e] + ps[3][e]);
+        n = (ns[0][e] + ns[1][e]) + (ns[2][e] + ns[3][e]);
+        if (e < E) seq_count[(int64_t)q * E + e] = n;
+        const float len = (float)max(L, 1), f = (float)E * (float)n / ((float)K * len);
+        ps[0][e] = f * (p / len);
+    }
+    __syncthreads();
+    for (int h = 128; h >= 1; h >>= 1) {
+        if (threadIdx.x < (unsigned)h) ps[0][threadIdx.x] += ps[0][threadIdx.x + h];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) loss[q] = alpha * ps[0][0];
+}
+
+// One wave per token.
+__global__ __launch_bounds__(256) void balance_backward_kernel(
+    const float* __restrict__ s, const int32_t* __restrict__ seq_count, const int32_t* __restrict__ start, int n_seq,
+    int T, int E, int K, float alpha, const float* __restrict__ dloss, const float* in, float* out) {
+    const int lane = threadIdx.x & 63;
+    for (int t = blockIdx.x * 4 + (threadIdx.x >> 6); t < T; t += gridDim.x * 4) {        // T <= 2^30
+        const int q = seq_of(start, n_seq, T, t);
+        const int b = q < n_seq ? seq_start_at(start, q, n_seq, T) : T;
+        const bool inside = t >= b;
+        float v[4], g[4], f[4] = {0.f, 0.f, 0.f, 0.f};
+        float sum = 0.0f, fp = 0.0f, coef = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = lane + 64 * j;
+            v[j] = e < E ? s[(int64_t)t * E + e] : 0.0f;
+            g[j] = in && e < E ? in[(int64_t)t * E + e] : 0.0f;
+            sum += v[j];
+        }
+        if (inside) {
+            const float len = (float)(seq_start_at(start, q + 1, n_seq, T) - b);
+            const float per = (float)E / ((float)K * len);
+            coef = (dloss ? dloss[q] : 1.0f) * alpha / len;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (lane + 64 * j < E) f[j] = per * (float)seq_count[(int64_t)q * E + lane + 64 * j];
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
+        float p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            p[j] = sum != 0.0f ? v[j] / sum : 0.0f;
+            fp = __builtin_fmaf(f[j], p[j], fp);
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) fp += __shfl_xor(fp, o, 64);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = lane + 64 * j;
+            if (e < E) out[(int64_t)t * E + e] = inside ? __builtin_fmaf(coef * p[j] * (1.0f - v[j]), f[j] - fp, g[j]) : g[j];
+        }
+    }
+}
+
+int balance_chunk(int64_t T) {
+    const int64_t c = (T + RUN_CHUNKS - 1) / RUN_CHUNKS;
+    return (int)(c < RUN_LEAST ? RUN_LEAST : c);
+}
+
 }  // namespace
+
+size_t balance_loss_ws_bytes(int64_t T, int n_seq) {
+    const int64_t chunk = balance_chunk(T);
+    const int64_t chunks = (T + chunk - 1) / chunk;
+    return (size_t)(chunks + n_seq) * sizeof(BalanceRun) + (size_t)chunks * 256 * sizeof(int32_t);
+}
+
+hipError_t launch_balance_loss(const float* s, const int32_t* idx, const int32_t* start, int n_seq, int64_t T, int E,
+                               int K, float alpha, float* loss, int32_t* seq_count, int32_t* expert_count, void* ws,
+                               hipStream_t st) {
+    BalanceRun* rec = static_cast<BalanceRun*>(ws);
+    const int chunk = balance_chunk(T), chunks = (int)((T + chunk - 1) / chunk);
+    int32_t* chunk_n = reinterpret_cast<int32_t*>(rec + chunks + n_seq);
+    if (T > 0)
+        hipLaunchKernelGGL(balance_runs_kernel, dim3(chunks), dim3(64 * RUN_WAVES), 0, st, s, idx, start, n_seq, (int)T, E,
+                           K, chunk, rec, chunk_n);
+    hipLaunchKernelGGL(balance_sum_kernel, dim3(n_seq + (expert_count ? 1 : 0)), dim3(1024), 0, st, rec, chunk_n, start,
+                       n_seq, (int)T, E, K, chunk, alpha, loss, seq_count, expert_count);
+    return hipGetLastError();
+}
+
+hipError_t launch_balance_loss_backward(const float* s, const int32_t* seq_count, const int32_t* start, int n_seq,
+                                        int64_t T, int E, int K, float alpha, const float* dloss, const float* in,
+                                        float* out, hipStream_t st) {
+    const int64_t blocks = (T + 3) / 4;
+    hipLaunchKernelGGL(balance_backward_kernel, dim3((unsigned)(blocks < (1 << 23) ? blocks : (1 << 23))), dim3(256), 0, st,
+                       s, seq_count, start, n_seq, (int)T, E, K, alpha, dloss, in, out);
+    return hipGetLastError();
+}
 
 size_t seq_balance_ws_bytes(int64_t n_seq, int L) {
     const int64_t nchunk = (L + BAL_CHUNK - 1) / BAL_CHUNK;

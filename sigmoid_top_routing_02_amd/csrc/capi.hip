@@ -30,11 +30,12 @@ int hip_status(hipError_t e, const char* what) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-#define REQUIRE_PTR(p)                                                               \
+#define REQUIRE_PTR_OF(who, p)                                                       \
     do {                                                                             \
-        if (!(p)) return fail(MOE_ERR_NULLPTR, "%s: %s is NULL", __func__, #p);      \
-        if (!aligned16(p)) return fail(MOE_ERR_ALIGN, "%s: %s is not 16-byte aligned", __func__, #p); \
+        if (!(p)) return fail(MOE_ERR_NULLPTR, "%s: %s is NULL", who, #p);           \
+        if (!aligned16(p)) return fail(MOE_ERR_ALIGN, "%s: %s is not 16-byte aligned", who, #p); \
     } while (0)
+#define REQUIRE_PTR(p) REQUIRE_PTR_OF(__func__, p)
 
 #define REQUIRE(cond, status, ...)                      \
     do {                                                \
@@ -42,6 +43,21 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
     } while (0)
 
 inline hipStream_t S(moe_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
+
+constexpr int64_t BALANCE_MAX_T = (int64_t)1 << 30;
+constexpr int BALANCE_MAX_SEQ = 1 << 20;
+constexpr int64_t LOGITS_MAX_T = (int64_t)1 << 24;
+constexpr int LOGITS_MAX_D = 65536;
+
+int balance_check(const char* who, const int32_t* seq_start, int n_seq, int64_t T, int E, int K) {
+    REQUIRE(T >= 0, MOE_ERR_SHAPE, "%s: T < 0", who);
+    REQUIRE(T <= BALANCE_MAX_T, MOE_ERR_UNSUPPORTED, "%s: T=%lld above 2^30", who, (long long)T);
+    REQUIRE(E >= 1 && E <= 256, MOE_ERR_UNSUPPORTED, "%s: E=%d outside [1, 256]", who, E);
+    REQUIRE(K >= 1 && K <= E && K <= 16, MOE_ERR_UNSUPPORTED, "%s: K=%d outside [1, min(E,16)]", who, K);
+    REQUIRE(n_seq >= 1 && n_seq <= BALANCE_MAX_SEQ, MOE_ERR_UNSUPPORTED, "%s: n_seq=%d outside [1, 2^20]", who, n_seq);
+    REQUIRE(seq_start || n_seq == 1, MOE_ERR_NULLPTR, "%s: %d sequences without seq_start", who, n_seq);
+    return MOE_OK;
+}
 
 inline size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -131,6 +147,84 @@ int moe_seq_balance_loss(const float* scores, const int32_t* topk_idx, int64_t T
     return hip_status(moe::launch_seq_balance_loss(scores, topk_idx, T / seq_len, E, K, seq_len, alpha,
                                                    loss, ws, S(stream)),
                       "balance loss launch");
+}
+
+size_t moe_balance_loss_workspace_bytes(int64_t T, int n_seq) {
+    if (T < 0 || T > BALANCE_MAX_T || n_seq < 1 || n_seq > BALANCE_MAX_SEQ) return 0;
+    return moe::balance_loss_ws_bytes(T, n_seq);
+}
+
+int moe_balance_loss(const float* scores, const int32_t* topk_idx, const int32_t* seq_start, int n_seq, int64_t T, int E,
+                     int K, float alpha, float* loss, int32_t* seq_count, int32_t* expert_count, void* ws,
+                     size_t ws_bytes, moe_stream_t stream) {
+    const int st = balance_check(__func__, seq_start, n_seq, T, E, K);
+    if (st != MOE_OK) return st;
+    REQUIRE_PTR(loss);
+    REQUIRE_PTR(seq_count);
+    if (seq_start) REQUIRE_PTR(seq_start);
+    if (expert_count) REQUIRE_PTR(expert_count);
+    if (T > 0) {
+        REQUIRE_PTR(scores);
+        REQUIRE_PTR(topk_idx);
+    }
+    REQUIRE_PTR(ws);
+    REQUIRE(ws_bytes >= moe::balance_loss_ws_bytes(T, n_seq), MOE_ERR_WORKSPACE,
+            "moe_balance_loss: workspace of %zu bytes, %zu needed", ws_bytes, moe::balance_loss_ws_bytes(T, n_seq));
+    return hip_status(moe::launch_balance_loss(scores, topk_idx, seq_start, n_seq, T, E, K, alpha, loss, seq_count,
+                                               expert_count, ws, S(stream)),
+                      "balance loss launch");
+}
+
+int moe_balance_loss_backward(const float* scores, const int32_t* seq_count, const int32_t* seq_start, int n_seq,
+                              int64_t T, int E, int K, float alpha, const float* dloss, const float* dlogits_in,
+                              float* dlogits, moe_stream_t stream) {
+    const int st = balance_check(__func__, seq_start, n_seq, T, E, K);
+    if (st != MOE_OK || T == 0) return st;
+    REQUIRE_PTR(scores);
+    REQUIRE_PTR(seq_count);
+    if (seq_start) REQUIRE_PTR(seq_start);
+    if (dloss) REQUIRE_PTR(dloss);
+    if (dlogits_in) REQUIRE_PTR(dlogits_in);
+    REQUIRE_PTR(dlogits);
+    return hip_status(moe::launch_balance_loss_backward(scores, seq_count, seq_start, n_seq, T, E, K, alpha, dloss,
+                                                        dlogits_in, dlogits, S(stream)),
+                      "balance loss backward launch");
+}
+
+size_t moe_router_logits_backward_workspace_bytes(int64_t T, int d, int E) {
+    if (T < 0 || T > LOGITS_MAX_T || d < 128 || d % 128 || d > LOGITS_MAX_D || E < 1 || E > 256) return 0;
+    return moe::router_logits_backward_ws_bytes(T, d, E);
+}
+
+int moe_router_logits_backward(const float* dlogits, const void* u_bf16, const void* centroids_bf16, int64_t T, int d,
+                               int E, const float* du_in, const float* de_in, float* du, float* de, void* ws,
+                               size_t ws_bytes, moe_stream_t stream) {
+    REQUIRE(T >= 0, MOE_ERR_SHAPE, "moe_router_logits_backward: T < 0");
+    REQUIRE(T <= LOGITS_MAX_T, MOE_ERR_UNSUPPORTED, "moe_router_logits_backward: T=%lld above 2^24", (long long)T);
+    REQUIRE(d > 0 && d % 128 == 0, MOE_ERR_SHAPE, "moe_router_logits_backward: d=%d not a positive multiple of 128", d);
+    REQUIRE(d <= LOGITS_MAX_D, MOE_ERR_UNSUPPORTED, "moe_router_logits_backward: d=%d above 65536", d);
+    REQUIRE(E >= 1 && E <= 256, MOE_ERR_UNSUPPORTED, "moe_router_logits_backward: E=%d outside [1, 256]", E);
+    REQUIRE(du || de, MOE_ERR_NULLPTR, "moe_router_logits_backward: neither du nor de asked for");
+    REQUIRE((du || !du_in) && (de || !de_in), MOE_ERR_NULLPTR, "moe_router_logits_backward: du_in without du or de_in without de");
+    if (du && T > 0) {
+        REQUIRE_PTR(du);
+        REQUIRE_PTR(centroids_bf16);
+        if (du_in) REQUIRE_PTR(du_in);
+    }
+    if (de) {
+        REQUIRE_PTR(de);
+        if (T > 0) REQUIRE_PTR(u_bf16);
+        if (de_in) REQUIRE_PTR(de_in);
+        REQUIRE_PTR(ws);
+        REQUIRE(ws_bytes >= moe::router_logits_backward_ws_bytes(T, d, E), MOE_ERR_WORKSPACE,
+                "moe_router_logits_backward: workspace %zu < %zu bytes", ws_bytes,
+                moe::router_logits_backward_ws_bytes(T, d, E));
+    }
+    if (T > 0) REQUIRE_PTR(dlogits);
+    return hip_status(moe::launch_router_logits_backward(dlogits, static_cast<const uint16_t*>(u_bf16),
+                                                         static_cast<const uint16_t*>(centroids_bf16), T, d, E, du_in,
+                                                         de_in, du, de, ws, S(stream)),
+                      "router logits backward launch");
 }
 
 size_t moe_dispatch_workspace_bytes(int64_t T, int E) {
@@ -281,7 +375,7 @@ int grouped_gemm_fp8_blockscaled(const uint8_t* a_q, const float* a_scale,
     REQUIRE(ws_bytes >= moe::gemm_ws_bytes(G, M_total, N, K), MOE_ERR_WORKSPACE,
             "grouped_gemm: workspace %zu < %zu bytes", ws_bytes, moe::gemm_ws_bytes(G, M_total, N, K));
     return hip_status(moe::launch_grouped_gemm(a_q, a_scale, a_row_index, group_offset, G, M_total,
-                                               b_q, b_scale, N, K, epi, out, out_q, out_scale, ws,
+                                               b_q, b_scale, N, K, epi, out, out_q, out_scale, nullptr, nullptr, ws,
                                                S(stream)),
                       "grouped gemm launch");
 }
@@ -302,7 +396,25 @@ int grouped_gemm_fp8_blockscaled_noalloc(const uint8_t* a_q, const float* a_scal
     const hipError_t e = moe::gemm_static_scratch(&scratch);
     if (e != hipSuccess) return hip_status(e, "grouped_gemm_noalloc: static scratch address");
     return hip_status(moe::launch_grouped_gemm(a_q, a_scale, a_row_index, group_offset, G, M_total,
-                                               b_q, b_scale, N, K, epi, out, out_q, out_scale, scratch,
+                                               b_q, b_scale, N, K, epi, out, out_q, out_scale, nullptr, nullptr, scratch,
+                                               S(stream)),
+                      "grouped gemm launch");
+}
+
+int grouped_gemm_fp8_swiglu_zq(const uint8_t* a_q, const float* a_scale, const int32_t* a_row_index,
+                               const int32_t* group_offset, int G, int64_t M_total, const uint8_t* b_q,
+                               const float* b_scale, int N, int K, uint8_t* h_q, float* h_scale, uint8_t* z_q,
+                               float* z_scale, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    const int st = gemm_check_args(a_q, a_scale, a_row_index, group_offset, G, M_total, b_q, b_scale, N, K,
+                                   MOE_EPI_SWIGLU_QUANT, nullptr, h_q, h_scale);
+    if (st != MOE_OK || M_total == 0) return st;
+    REQUIRE_PTR(z_q);
+    REQUIRE_PTR(z_scale);
+    REQUIRE_PTR(ws);
+    REQUIRE(ws_bytes >= moe::gemm_ws_bytes(G, M_total, N, K), MOE_ERR_WORKSPACE,
+            "grouped_gemm: workspace %zu < %zu bytes", ws_bytes, moe::gemm_ws_bytes(G, M_total, N, K));
+    return hip_status(moe::launch_grouped_gemm(a_q, a_scale, a_row_index, group_offset, G, M_total, b_q, b_scale, N, K,
+                                               moe::EPI_SWIGLU_QUANT_ZQ, nullptr, h_q, h_scale, z_q, z_scale, ws,
                                                S(stream)),
                       "grouped gemm launch");
 }
@@ -460,6 +572,22 @@ int moe_swiglu_backward(const float* z, const float* dh_row, int64_t R, int I, u
                       "SwiGLU backward launch");
 }
 
+int moe_swiglu_backward_zq(const uint8_t* z_q, const float* z_scale, const float* dh_row, int64_t R, int I,
+                           uint8_t* dz_q, float* dz_scale, moe_stream_t stream) {
+    REQUIRE(R >= 0, MOE_ERR_SHAPE, "moe_swiglu_backward_zq: R < 0");
+    REQUIRE(I > 0 && I % 128 == 0, MOE_ERR_SHAPE, "moe_swiglu_backward_zq: I=%d not a positive multiple of 128", I);
+    REQUIRE(R < ((int64_t)1 << 31) && I <= 65536, MOE_ERR_UNSUPPORTED, "moe_swiglu_backward_zq: R=%lld, I=%d",
+            (long long)R, I);
+    if (R == 0) return MOE_OK;
+    REQUIRE_PTR(z_q);
+    REQUIRE_PTR(z_scale);
+    REQUIRE_PTR(dh_row);
+    REQUIRE_PTR(dz_q);
+    REQUIRE_PTR(dz_scale);
+    return hip_status(moe::launch_swiglu_backward_zq(z_q, z_scale, dh_row, R, I, dz_q, dz_scale, S(stream)),
+                      "SwiGLU backward launch");
+}
+
 int moe_router_backward(const float* dh, const float* dx, int64_t shared_row0, const int32_t* slot_row,
                         const float* dlogit, const int32_t* topk_idx, const void* centroids_bf16,
                         const void* u_bf16, const float* row_dlogit, const int32_t* row_token,
@@ -498,40 +626,66 @@ int moe_wgrad_block_starts(const int32_t* group_offset, int G, int32_t* kb_start
     return hip_status(moe::launch_wgrad_block_starts(group_offset, G, kb_start, S(stream)), "kb_start launch");
 }
 
+// moe_wgrad_operands and, with z_q, moe_wgrad_operands_zq
+static int wgrad_operands(const char* who, const float* dh, const float* topk_gate, const int32_t* slot_row,
+                          const int32_t* row_token, const float* z, const uint8_t* z_q, const float* z_scale,
+                          const float* dh_row, const void* u_bf16, const int32_t* group_offset,
+                          const int32_t* kb_start, int G, int n_kb, int64_t T, int K, int d, int I,
+                          int64_t shared_row0, uint8_t* dyT_q, float* dyT_scale, uint8_t* hT_q, float* hT_scale,
+                          uint8_t* dzT_q, float* dzT_scale, uint8_t* xT_q, float* xT_scale, moe_stream_t stream) {
+    REQUIRE(G >= 1 && G <= 65535, MOE_ERR_UNSUPPORTED, "%s: G=%d outside [1, 65535]", who, G);
+    REQUIRE(n_kb >= 0 && n_kb <= 65535, MOE_ERR_UNSUPPORTED, "%s: n_kb=%d outside [0, 65535]", who, n_kb);
+    REQUIRE(K >= 1 && K <= 16, MOE_ERR_UNSUPPORTED, "%s: K=%d outside [1, 16]", who, K);
+    REQUIRE(d > 0 && d % 128 == 0 && I > 0 && I % 128 == 0, MOE_ERR_SHAPE,
+            "%s: d=%d, I=%d must be positive multiples of 128", who, d, I);
+    REQUIRE(T >= 0, MOE_ERR_SHAPE, "%s: T < 0", who);
+    if (n_kb == 0) return MOE_OK;
+    REQUIRE_PTR_OF(who, dh);
+    REQUIRE_PTR_OF(who, topk_gate);
+    REQUIRE_PTR_OF(who, slot_row);
+    REQUIRE_PTR_OF(who, row_token);
+    if (z_q) {
+        REQUIRE_PTR_OF(who, z_q);
+        REQUIRE_PTR_OF(who, z_scale);
+    } else {
+        REQUIRE_PTR_OF(who, z);
+    }
+    REQUIRE_PTR_OF(who, dh_row);
+    REQUIRE_PTR_OF(who, u_bf16);
+    REQUIRE_PTR_OF(who, group_offset);
+    REQUIRE_PTR_OF(who, kb_start);
+    REQUIRE_PTR_OF(who, dyT_q);
+    REQUIRE_PTR_OF(who, dyT_scale);
+    REQUIRE_PTR_OF(who, hT_q);
+    REQUIRE_PTR_OF(who, hT_scale);
+    REQUIRE_PTR_OF(who, dzT_q);
+    REQUIRE_PTR_OF(who, dzT_scale);
+    REQUIRE_PTR_OF(who, xT_q);
+    REQUIRE_PTR_OF(who, xT_scale);
+    return hip_status(moe::launch_wgrad_operands(dh, topk_gate, slot_row, row_token, z, z_q, z_scale, dh_row,
+                                                 static_cast<const uint16_t*>(u_bf16), shared_row0, K, d, I,
+                                                 group_offset, kb_start, G, n_kb, dyT_q, dyT_scale, hT_q, hT_scale,
+                                                 dzT_q, dzT_scale, xT_q, xT_scale, S(stream)),
+                      "wgrad operand launch");
+}
+
 int moe_wgrad_operands(const float* dh, const float* topk_gate, const int32_t* slot_row, const int32_t* row_token,
                        const float* z, const float* dh_row, const void* u_bf16, const int32_t* group_offset,
                        const int32_t* kb_start, int G, int n_kb, int64_t T, int K, int d, int I,
                        int64_t shared_row0, uint8_t* dyT_q, float* dyT_scale, uint8_t* hT_q, float* hT_scale,
                        uint8_t* dzT_q, float* dzT_scale, uint8_t* xT_q, float* xT_scale, moe_stream_t stream) {
-    REQUIRE(G >= 1 && G <= 65535, MOE_ERR_UNSUPPORTED, "moe_wgrad_operands: G=%d outside [1, 65535]", G);
-    REQUIRE(n_kb >= 0 && n_kb <= 65535, MOE_ERR_UNSUPPORTED, "moe_wgrad_operands: n_kb=%d outside [0, 65535]", n_kb);
-    REQUIRE(K >= 1 && K <= 16, MOE_ERR_UNSUPPORTED, "moe_wgrad_operands: K=%d outside [1, 16]", K);
-    REQUIRE(d > 0 && d % 128 == 0 && I > 0 && I % 128 == 0, MOE_ERR_SHAPE,
-            "moe_wgrad_operands: d=%d, I=%d must be positive multiples of 128", d, I);
-    REQUIRE(T >= 0, MOE_ERR_SHAPE, "moe_wgrad_operands: T < 0");
-    if (n_kb == 0) return MOE_OK;
-    REQUIRE_PTR(dh);
-    REQUIRE_PTR(topk_gate);
-    REQUIRE_PTR(slot_row);
-    REQUIRE_PTR(row_token);
-    REQUIRE_PTR(z);
-    REQUIRE_PTR(dh_row);
-    REQUIRE_PTR(u_bf16);
-    REQUIRE_PTR(group_offset);
-    REQUIRE_PTR(kb_start);
-    REQUIRE_PTR(dyT_q);
-    REQUIRE_PTR(dyT_scale);
-    REQUIRE_PTR(hT_q);
-    REQUIRE_PTR(hT_scale);
-    REQUIRE_PTR(dzT_q);
-    REQUIRE_PTR(dzT_scale);
-    REQUIRE_PTR(xT_q);
-    REQUIRE_PTR(xT_scale);
-    return hip_status(moe::launch_wgrad_operands(dh, topk_gate, slot_row, row_token, z, dh_row,
-                                                 static_cast<const uint16_t*>(u_bf16), shared_row0, K, d, I,
-                                                 group_offset, kb_start, G, n_kb, dyT_q, dyT_scale, hT_q, hT_scale,
-                                                 dzT_q, dzT_scale, xT_q, xT_scale, S(stream)),
-                      "wgrad operand launch");
+    return wgrad_operands(__func__, dh, topk_gate, slot_row, row_token, z, nullptr, nullptr, dh_row, u_bf16, group_offset, kb_start, G, n_kb, T, K, d, I,
+                          shared_row0, dyT_q, dyT_scale, hT_q, hT_scale, dzT_q, dzT_scale, xT_q, xT_scale, stream);
+}
+
+int moe_wgrad_operands_zq(const float* dh, const float* topk_gate, const int32_t* slot_row, const int32_t* row_token,
+                       const uint8_t* z_q, const float* z_scale, const float* dh_row, const void* u_bf16, const int32_t* group_offset,
+                       const int32_t* kb_start, int G, int n_kb, int64_t T, int K, int d, int I,
+                       int64_t shared_row0, uint8_t* dyT_q, float* dyT_scale, uint8_t* hT_q, float* hT_scale,
+                       uint8_t* dzT_q, float* dzT_scale, uint8_t* xT_q, float* xT_scale, moe_stream_t stream) {
+    if (n_kb > 0) REQUIRE_PTR(z_q);
+    return wgrad_operands(__func__, dh, topk_gate, slot_row, row_token, nullptr, z_q, z_scale, dh_row, u_bf16, group_offset, kb_start, G, n_kb, T, K, d, I,
+                          shared_row0, dyT_q, dyT_scale, hT_q, hT_scale, dzT_q, dzT_scale, xT_q, xT_scale, stream);
 }
 
 size_t moe_wgrad_workspace_bytes(int G, int d, int I) {
@@ -642,6 +796,77 @@ int moe_add_rmsnorm_backward(const void* dy, int dy_dt, const void* h, int h_dt,
     a.dx = dx; a.dx_f32 = dx_dt == MOE_F32;
     a.part = static_cast<float*>(ws);
     return hip_status(moe::launch_add_rmsnorm_backward(a, dw, S(stream)), "add rmsnorm backward launch");
+}
+
+int moe_add_layernorm(const void* x, int x_dt, const void* residual, int res_dt, const void* weight, const void* bias,
+                      int w_dt, int64_t T, int d, float eps, void* h_out, void* y_bf16, uint8_t* q, float* scale,
+                      float* mean, float* rstd, moe_stream_t stream) {
+    REQUIRE(T >= 0, MOE_ERR_SHAPE, "moe_add_layernorm: T < 0");
+    REQUIRE(d >= 1, MOE_ERR_SHAPE, "moe_add_layernorm: d=%d not positive", d);
+    REQUIRE(d <= 16384, MOE_ERR_UNSUPPORTED, "moe_add_layernorm: d=%d above 16384", d);
+    REQUIRE(is_dtype(x_dt) && is_dtype(w_dt) && (!residual || is_dtype(res_dt)), MOE_ERR_UNSUPPORTED,
+            "moe_add_layernorm: dtypes %d, %d, %d", x_dt, res_dt, w_dt);
+    REQUIRE(eps >= 0.0f, MOE_ERR_UNSUPPORTED, "moe_add_layernorm: eps=%g is negative or NaN", (double)eps);
+    REQUIRE((q == nullptr) == (scale == nullptr), MOE_ERR_NULLPTR,
+            "moe_add_layernorm: q and scale must both be given or both be NULL");
+    REQUIRE(!q || d % 128 == 0, MOE_ERR_SHAPE, "moe_add_layernorm: d=%d not a multiple of 128, as q needs", d);
+    REQUIRE(!h_out || residual || T == 0, MOE_ERR_NULLPTR, "moe_add_layernorm: h_out without a residual");
+    if (T == 0) return MOE_OK;
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(weight);
+    if (bias) REQUIRE_PTR(bias);
+    if (residual) REQUIRE_PTR(residual);
+    if (h_out) REQUIRE_PTR(h_out);
+    if (y_bf16) REQUIRE_PTR(y_bf16);
+    if (q) REQUIRE_PTR(q);
+    if (scale) REQUIRE_PTR(scale);
+    if (mean) REQUIRE_PTR(mean);
+    if (rstd) REQUIRE_PTR(rstd);
+    moe::AddLayernormArgs a{};
+    a.x = x; a.x_f32 = x_dt == MOE_F32;
+    a.res = residual; a.res_f32 = res_dt == MOE_F32;
+    a.w = weight; a.b = bias; a.w_f32 = w_dt == MOE_F32;
+    a.T = T; a.d = d; a.eps = eps;
+    a.h = h_out; a.y = y_bf16; a.q = q; a.scale = scale; a.mean = mean; a.rstd = rstd;
+    return hip_status(moe::launch_add_layernorm(a, S(stream)), "add layernorm launch");
+}
+
+size_t moe_add_layernorm_backward_workspace_bytes(int64_t T, int d) {
+    return T >= 1 && d >= 1 && d <= 16384 ? moe::add_layernorm_backward_ws_bytes(T, d) : 0;
+}
+
+int moe_add_layernorm_backward(const void* dy, int dy_dt, const void* h, int h_dt, const void* weight, int w_dt,
+                               const float* mean, const float* rstd, const void* dh, int64_t T, int d, void* dx,
+                               int dx_dt, float* dw, float* db, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    REQUIRE(T >= 0, MOE_ERR_SHAPE, "moe_add_layernorm_backward: T < 0");
+    REQUIRE(d >= 1, MOE_ERR_SHAPE, "moe_add_layernorm_backward: d=%d not positive", d);
+    REQUIRE(d <= 16384, MOE_ERR_UNSUPPORTED, "moe_add_layernorm_backward: d=%d above 16384", d);
+    REQUIRE(is_dtype(dy_dt) && is_dtype(h_dt) && is_dtype(w_dt) && is_dtype(dx_dt), MOE_ERR_UNSUPPORTED,
+            "moe_add_layernorm_backward: dtypes %d, %d, %d, %d", dy_dt, h_dt, w_dt, dx_dt);
+    REQUIRE_PTR(dw);
+    if (db) REQUIRE_PTR(db);
+    if (T > 0) {
+        REQUIRE_PTR(dy);
+        REQUIRE_PTR(h);
+        REQUIRE_PTR(weight);
+        REQUIRE_PTR(mean);
+        REQUIRE_PTR(rstd);
+        REQUIRE_PTR(dx);
+        REQUIRE_PTR(ws);
+        if (dh) REQUIRE_PTR(dh);
+        REQUIRE(ws_bytes >= moe::add_layernorm_backward_ws_bytes(T, d), MOE_ERR_WORKSPACE,
+                "moe_add_layernorm_backward: workspace %zu < %zu bytes", ws_bytes,
+                moe::add_layernorm_backward_ws_bytes(T, d));
+    }
+    moe::AddLayernormBackwardArgs a{};
+    a.dy = dy; a.dy_f32 = dy_dt == MOE_F32;
+    a.h = h; a.h_f32 = h_dt == MOE_F32;
+    a.w = weight; a.w_f32 = w_dt == MOE_F32;
+    a.mean = mean; a.rstd = rstd; a.dh = dh; a.T = T; a.d = d;
+    a.dx = dx; a.dx_f32 = dx_dt == MOE_F32;
+    a.part = static_cast<float*>(ws);
+    a.bias_grad = db != nullptr;
+    return hip_status(moe::launch_add_layernorm_backward(a, dw, db, S(stream)), "add layernorm backward launch");
 }
 
 int mxfp4_quant_1x32(const void* x, int in_dt, int64_t rows, int cols, uint8_t* q, uint8_t* scale,
@@ -822,10 +1047,10 @@ int moe_layer_forward(const void* u_bf16, const void* centroids_bf16, const floa
     e = moe::launch_quant_1x128(u_bf16, 0, T, d, w.uq, w.us, st);
     if (e != hipSuccess) return hip_status(e, "quant launch");
     e = moe::launch_grouped_gemm(w.uq, w.us, w.row_token, w.go, G, R, pk.w13q, pk.w13s, 2 * I, d,
-                                 moe::EPI_SWIGLU_QUANT, nullptr, w.hq, w.hs, w.gws, st);
+                                 moe::EPI_SWIGLU_QUANT, nullptr, w.hq, w.hs, nullptr, nullptr, w.gws, st);
     if (e != hipSuccess) return hip_status(e, "gemm1 launch");
     e = moe::launch_grouped_gemm(w.hq, w.hs, nullptr, w.go, G, R, pk.w2q, pk.w2s, d, I,
-                                 moe::EPI_STORE_F32, w.y, nullptr, nullptr, w.gws, st);
+                                 moe::EPI_STORE_F32, w.y, nullptr, nullptr, nullptr, nullptr, w.gws, st);
     if (e != hipSuccess) return hip_status(e, "gemm2 launch");
     e = moe::launch_combine(static_cast<const uint16_t*>(u_bf16), w.y, 1, T * K, w.gate, w.slot_row,
                             T, K, d, out, st);

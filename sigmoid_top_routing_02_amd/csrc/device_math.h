@@ -82,6 +82,13 @@ __device__ __forceinline__ uint32_t e4m3_encode4(float a, float b, float c, floa
     return e4m3_nan_fix(w, d, 3);
 }
 
+// The values of four E4M3 codes (exact; NaN codes give NaN).
+__device__ __forceinline__ float4 e4m3_decode4(uint32_t w) {
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    return make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+
 // 1x128 / 128x128 scale rule: inv multiplies the data, scale dequantises.
 __device__ __forceinline__ void tile_scale(float amax, float& inv, float& scale) {
     const float iv = 448.0f / amax;

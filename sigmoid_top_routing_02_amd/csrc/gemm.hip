@@ -35,7 +35,8 @@
 // Epilogues: FP32 store; SwiGLU (B rows interleaved gate/up per 128-row
 // block, so one N tile holds the gate and up columns of the same 128 h
 // columns); SwiGLU + 1x128 E4M3 re-quantisation of h, whose row maximum over
-// the tile's 128 h columns is reduced across the N-waves in LDS.
+// the tile's 128 h columns is reduced across the N-waves in LDS; the same with the
+// tile itself, z, kept for the backward in FP32 or as E4M3 with 1x128 scales.
 #include <atomic>
 #include <type_traits>
 
@@ -115,6 +116,9 @@ struct GemmArgs {
     const int32_t* kb_start;
     int group_rows;
     int b_cs;
+    // EPI_SWIGLU_QUANT_ZQ: z [M_total, N] in 8 bits with its scales [M_total, N/128]
+    uint8_t* z_q;
+    float* z_s;
 };
 
 // The three pipeline stages are separate LDS objects and every access names
@@ -611,6 +615,13 @@ __global__ __launch_bounds__(NT) void grouped_gemm_kernel(GemmArgs p) {
     float* const amax_s = reinterpret_cast<float*>(g_b2);               // [WAVES_N][BM] row maxima
     float* const scale_s = amax_s + WAVES_N * BM;                        // [BM] row scales
     char* const qtile = a_buf<2, BM>();                                  // [BM][128] codes
+    // z in 8 bits: the maxima of h, gate and up [3][WAVES_N][BM] where the codes
+    // [BM][256] come to lie, chunk c of 16 of row r at c ^ (r & 15), and the scales
+    // [3][BM] in the stage's scale buffer.
+    constexpr bool ZQ = EPI == EPI_SWIGLU_QUANT_ZQ;
+    char* const ztile = g_b2;
+    float* const zscale_s = g_sa2;
+    static_assert(!ZQ || (3 * BM <= 64 * NWAVES && 3 * WAVES_N * BM * 4 <= B_BYTES && BM * 256 <= B_BYTES), "z's scratch");
     auto swiglu_compute = [&]() {
         if constexpr (EPI != EPI_STORE_F32) {
 #pragma unroll
@@ -661,6 +672,92 @@ __global__ __launch_bounds__(NT) void grouped_gemm_kernel(GemmArgs p) {
                     if (wn == 0 && kb == 0) scale_s[r] = sc;
                 }
                 __syncthreads();
+            }
+        }
+    };
+    auto zq_compute = [&]() {
+        if constexpr (ZQ) {
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi) {
+                float m[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int ni = 0; ni < HALF; ++ni)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float x[3] = {h[mi][ni][j], acc[mi][ni][j], acc[mi][ni + HALF][j]};
+#pragma unroll
+                        for (int w = 0; w < 3; ++w) {
+                            const float a = __builtin_fabsf(x[w]);
+                            m[w] = a > m[w] ? a : m[w];
+                        }
+                    }
+#pragma unroll
+                for (int w = 0; w < 3; ++w) {
+#pragma unroll
+                    for (int o = 16; o < 64; o <<= 1) {
+                        const float other = __shfl_xor(m[w], o, 64);
+                        m[w] = other > m[w] ? other : m[w];
+                    }
+                    if (kb == 0) amax_s[(w * WAVES_N + wn) * BM + sa_row + mi * 16] = m[w];
+                }
+            }
+            __syncthreads();
+            float inv[MI][3];
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                for (int w = 0; w < 3; ++w) {
+                    const int r = sa_row + mi * 16;
+                    float amax = amax_s[w * WAVES_N * BM + r];
+#pragma unroll
+                    for (int v = 1; v < WAVES_N; ++v) {
+                        const float a = amax_s[(w * WAVES_N + v) * BM + r];
+                        amax = a > amax ? a : amax;
+                    }
+                    float sc;
+                    tile_scale(amax, inv[mi][w], sc);
+                    if (wn == 0 && kb == 0) zscale_s[w * BM + r] = sc;
+                }
+            __syncthreads();                   // the maxima are read before codes overwrite them
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi) {
+                const int r = sa_row + mi * 16;
+#pragma unroll
+                for (int ni = 0; ni < HALF; ++ni)
+                    *reinterpret_cast<uint32_t*>(qtile + r * 128 + wn * HC + ni * 16 + 4 * kb) =
+                        e4m3_encode4(h[mi][ni][0] * inv[mi][0], h[mi][ni][1] * inv[mi][0], h[mi][ni][2] * inv[mi][0],
+                                     h[mi][ni][3] * inv[mi][0]);
+#pragma unroll
+                for (int ni = 0; ni < NI; ++ni) {
+                    const float iv = inv[mi][ni < HALF ? 1 : 2];
+                    const int chunk = ncol<EPI, C>(wn, ni) / 16 ^ (r & 15);
+                    *reinterpret_cast<uint32_t*>(ztile + r * 256 + chunk * 16 + 4 * kb) =
+                        e4m3_encode4(acc[mi][ni][0] * iv, acc[mi][ni][1] * iv, acc[mi][ni][2] * iv, acc[mi][ni][3] * iv);
+                }
+            }
+            __syncthreads();
+        }
+    };
+    auto zq_store = [&](const Tile& T) {
+        if constexpr (ZQ) {
+            const int I = p.N / 2, h0 = T.n0 / 2;
+            for (int c = tid; c < BM * 8; c += NT) {
+                const int r = c >> 3, part = c & 7;
+                if (r < T.rows)
+                    *reinterpret_cast<uint4*>(p.out_q + (int64_t)(T.m0 + r) * I + h0 + part * 16) =
+                        *reinterpret_cast<const uint4*>(qtile + r * 128 + part * 16);
+            }
+            for (int c = tid; c < BM * 16; c += NT) {
+                const int r = c >> 4, part = c & 15;
+                if (r < T.rows)
+                    *reinterpret_cast<uint4*>(p.z_q + (int64_t)(T.m0 + r) * p.N + T.n0 + part * 16) =
+                        *reinterpret_cast<const uint4*>(ztile + r * 256 + (part ^ (r & 15)) * 16);
+            }
+            if (tid < BM && tid < T.rows) {
+                p.out_s[(int64_t)(T.m0 + tid) * (I / 128) + h0 / 128] = zscale_s[tid];
+                float* zs = p.z_s + (int64_t)(T.m0 + tid) * (p.N / 128) + T.n0 / 128;
+                zs[0] = zscale_s[BM + tid];
+                zs[1] = zscale_s[2 * BM + tid];
             }
         }
     };
@@ -757,6 +854,7 @@ __global__ __launch_bounds__(NT) void grouped_gemm_kernel(GemmArgs p) {
             load_rows(nxt);
         }
         swiglu_compute();
+        zq_compute();
         if (t_nxt >= 0) {
             setup(nxt);
             issue(IC<0>{}, 0);
@@ -765,6 +863,7 @@ __global__ __launch_bounds__(NT) void grouped_gemm_kernel(GemmArgs p) {
         }
         store_f32(cur);
         swiglu_store(cur);
+        zq_store(cur);
         if (t_nxt < 0) break;
         __syncthreads();   // stage-2 scratch and the tile's LDS reads are done before slice 2 lands
         cur = nxt;
@@ -1495,7 +1594,7 @@ size_t gemm_ws_bytes(int G, int64_t M_total, int N, int K) {
 hipError_t launch_grouped_gemm(const uint8_t* a_q, const float* a_s, const int32_t* a_rows,
                                const int32_t* group_offset, int G, int64_t M_total,
                                const uint8_t* b_q, const float* b_s, int N, int K, int epi,
-                               float* out, uint8_t* out_q, float* out_s, void* ws,
+                               float* out, uint8_t* out_q, float* out_s, uint8_t* z_q, float* z_s, void* ws,
                                hipStream_t st) {
     int32_t* ts = static_cast<int32_t*>(ws);
     int4* tiles = reinterpret_cast<int4*>(static_cast<char*>(ws) + tile_list_offset(G));
@@ -1517,6 +1616,8 @@ hipError_t launch_grouped_gemm(const uint8_t* a_q, const float* a_s, const int32
     }
     GemmArgs p{a_q, a_sT, (uint32_t)(M_total * 4), a_rows, group_offset, ts, ts + G + 1, tiles, G, b_q, b_s, N, K,
                out, out_q, out_s};
+    p.z_q = z_q;
+    p.z_s = z_s;
     const int64_t blocks = list_bound;
     // one block per CU (its ~150 KB of LDS admit one), a multiple of the 8 XCDs
     const int64_t persistent = ((int64_t)cu_count_for_current_device() + 7) / 8 * 8;
@@ -1528,14 +1629,16 @@ hipError_t launch_grouped_gemm(const uint8_t* a_q, const float* a_s, const int32
     // measured 5% faster on the expert down-projection (K = 2048) and 1-5%
     // slower on tiles of 32 or more slices and on 32-row tiles.  It needs four
     // slices to fetch the next tile's rows ahead, and one tile's rows of the
-    // output below 2 GiB (its out-of-range store offsets have bit 31 set).
-    const bool ring = bm == 128 && ns >= RING_MIN_SLICES && ns <= 16 &&
+    // output below 2 GiB (its out-of-range store offsets have bit 31 set), and has
+    // no epilogue for z in 8 bits.
+    const bool ring = bm == 128 && epi != EPI_SWIGLU_QUANT_ZQ && ns >= RING_MIN_SLICES && ns <= 16 &&
                       (int64_t)128 * N * 4 < ((int64_t)1 << 31);
     if (bm == 32) {
         switch (epi) {
             case EPI_STORE_F32: MOE_LAUNCH(grouped_gemm_kernel, EPI_STORE_F32, 32); break;
             case EPI_SWIGLU_F32: MOE_LAUNCH(grouped_gemm_kernel, EPI_SWIGLU_F32, 32); break;
             case EPI_SWIGLU_QUANT_Z: MOE_LAUNCH(grouped_gemm_kernel, EPI_SWIGLU_QUANT_Z, 32); break;
+            case EPI_SWIGLU_QUANT_ZQ: MOE_LAUNCH(grouped_gemm_kernel, EPI_SWIGLU_QUANT_ZQ, 32); break;
             default: MOE_LAUNCH(grouped_gemm_kernel, EPI_SWIGLU_QUANT, 32); break;
         }
     } else if (ring) {
@@ -1550,6 +1653,7 @@ hipError_t launch_grouped_gemm(const uint8_t* a_q, const float* a_s, const int32
             case EPI_STORE_F32: MOE_LAUNCH(grouped_gemm_kernel, EPI_STORE_F32, 128); break;
             case EPI_SWIGLU_F32: MOE_LAUNCH(grouped_gemm_kernel, EPI_SWIGLU_F32, 128); break;
             case EPI_SWIGLU_QUANT_Z: MOE_LAUNCH(grouped_gemm_kernel, EPI_SWIGLU_QUANT_Z, 128); break;
+            case EPI_SWIGLU_QUANT_ZQ: MOE_LAUNCH(grouped_gemm_kernel, EPI_SWIGLU_QUANT_ZQ, 128); break;
             default: MOE_LAUNCH(grouped_gemm_kernel, EPI_SWIGLU_QUANT, 128); break;
         }
     }

@@ -33,14 +33,14 @@ hipError_t launch_quant_128x128(const float* w, int64_t rows, int cols, uint8_t*
                                 int row_mul, int row_add, hipStream_t st);
 
 // gemm.hip
-enum { EPI_STORE_F32 = 0, EPI_SWIGLU_F32 = 1, EPI_SWIGLU_QUANT = 2, EPI_SWIGLU_QUANT_Z = 3 };
+enum { EPI_STORE_F32 = 0, EPI_SWIGLU_F32 = 1, EPI_SWIGLU_QUANT = 2, EPI_SWIGLU_QUANT_Z = 3, EPI_SWIGLU_QUANT_ZQ = 4 };
 size_t gemm_ws_bytes(int G, int64_t M_total, int N, int K);
 // device address of the static scratch array (MOE_GEMM_SCRATCH_BYTES) on the current device
 hipError_t gemm_static_scratch(void** ptr);
 hipError_t launch_grouped_gemm(const uint8_t* a_q, const float* a_s, const int32_t* a_rows,
                                const int32_t* group_offset, int G, int64_t M_total,
                                const uint8_t* b_q, const float* b_s, int N, int K, int epi,
-                               float* out, uint8_t* out_q, float* out_s, void* ws,
+                               float* out, uint8_t* out_q, float* out_s, uint8_t* z_q, float* z_s, void* ws,
                                hipStream_t st);
 // K-grouped FP32-store GEMM: G groups of `rows` A rows; group g's inner
 // dimension is the 128-blocks [kb_start[g], kb_start[g+1]) (device array), its
@@ -59,6 +59,9 @@ hipError_t launch_gate_backward(const float* dh, const float* y, int64_t shared_
                                 float* row_dlogit, hipStream_t st);
 hipError_t launch_swiglu_backward(const float* z, const float* dh_row, int64_t R, int I, uint8_t* dz_q,
                                   float* dz_s, hipStream_t st);
+// the same on z kept in 8 bits: codes [R, 2I], scales [R, 2I/128]
+hipError_t launch_swiglu_backward_zq(const uint8_t* z_q, const float* z_s, const float* dh_row, int64_t R, int I,
+                                     uint8_t* dz_q, float* dz_s, hipStream_t st);
 hipError_t launch_du(const float* dh, const float* dx, int64_t shared_row0, const int32_t* slot_row,
                      const float* dlogit, const int32_t* idx, const uint16_t* e, int64_t T, int K, int d,
                      float* du, hipStream_t st);
@@ -72,10 +75,10 @@ hipError_t launch_dispatch_check(const int32_t* count, const int32_t* group_offs
                                  const int32_t* row_token, const int32_t* slot_row, int64_t T, int K, int E,
                                  int include_shared, uint32_t* status, hipStream_t st);
 
-// wgrad.hip
+// wgrad.hip: z in FP32, or (z null) its codes and scales
 hipError_t launch_wgrad_operands(const float* dh, const float* gate, const int32_t* slot_row,
-                                 const int32_t* row_token, const float* z, const float* dh_row,
-                                 const uint16_t* u, int64_t shared_row0, int K, int d, int I,
+                                 const int32_t* row_token, const float* z, const uint8_t* z_q, const float* z_s,
+                                 const float* dh_row, const uint16_t* u, int64_t shared_row0, int K, int d, int I,
                                  const int32_t* go, const int32_t* kb_start, int G, int n_kb,
                                  uint8_t* dyT_q, float* dyT_s, uint8_t* hT_q, float* hT_s, uint8_t* dzT_q,
                                  float* dzT_s, uint8_t* xT_q, float* xT_s, hipStream_t st);
@@ -91,6 +94,21 @@ hipError_t launch_wgrad_gemms(const int32_t* kb_start, int G, int d, int I, cons
 size_t seq_balance_ws_bytes(int64_t n_seq, int L);
 hipError_t launch_seq_balance_loss(const float* s, const int32_t* idx, int64_t n_seq, int E, int K,
                                    int L, float alpha, float* loss, void* ws, hipStream_t st);
+
+// ragged sequences: T >= 0, start may be null (then n_seq = 1)
+size_t balance_loss_ws_bytes(int64_t T, int n_seq);
+hipError_t launch_balance_loss(const float* s, const int32_t* idx, const int32_t* start, int n_seq, int64_t T, int E,
+                               int K, float alpha, float* loss, int32_t* seq_count, int32_t* expert_count, void* ws,
+                               hipStream_t st);
+hipError_t launch_balance_loss_backward(const float* s, const int32_t* seq_count, const int32_t* start, int n_seq,
+                                        int64_t T, int E, int K, float alpha, const float* dloss, const float* in,
+                                        float* out, hipStream_t st);
+
+// logits.hip: null du_in / de_in: nothing to add to; null du / de: not asked for
+size_t router_logits_backward_ws_bytes(int64_t T, int d, int E);
+hipError_t launch_router_logits_backward(const float* dlogits, const uint16_t* u, const uint16_t* e, int64_t T, int d,
+                                         int E, const float* du_in, const float* de_in, float* du, float* de, void* ws,
+                                         hipStream_t st);
 
 // accum_probe.hip
 hipError_t launch_accum_probe(const uint8_t* a_q, const uint8_t* b_q, int M, int N, int K,
@@ -124,6 +142,38 @@ struct AddRmsnormBackwardArgs {
 };
 size_t add_rmsnorm_backward_ws_bytes(int64_t T, int d);
 hipError_t launch_add_rmsnorm_backward(const AddRmsnormBackwardArgs& a, float* dw, hipStream_t st);
+
+// layernorm.hip, as norm.hip
+struct AddLayernormArgs {
+    const void* x; bool x_f32;
+    const void* res; bool res_f32;      // h has its type
+    const void* w; const void* b; bool w_f32;
+    int64_t T;
+    int d;
+    float eps;
+    void* h;
+    void* y;                            // bf16
+    uint8_t* q;
+    float* scale;
+    float* mean;
+    float* rstd;
+};
+hipError_t launch_add_layernorm(const AddLayernormArgs& a, hipStream_t st);
+struct AddLayernormBackwardArgs {
+    const void* dy; bool dy_f32;
+    const void* h; bool h_f32;
+    const void* w; bool w_f32;
+    const float* mean;
+    const float* rstd;
+    const void* dh;                     // of dx's type
+    int64_t T;
+    int d;
+    void* dx; bool dx_f32;
+    float* part;                        // add_layernorm_backward_ws_bytes: partial rows of dw, then of db
+    bool bias_grad;
+};
+size_t add_layernorm_backward_ws_bytes(int64_t T, int d);
+hipError_t launch_add_layernorm_backward(const AddLayernormBackwardArgs& a, float* dw, float* db, hipStream_t st);
 
 // mxfp4.hip: n_blocks blocks of 32 consecutive values
 hipError_t launch_mxfp4_quant(const void* x, int in_is_f32, int64_t n_blocks, uint8_t* q, uint8_t* scale,

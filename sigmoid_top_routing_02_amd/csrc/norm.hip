@@ -13,116 +13,11 @@
 //
 // Both are bound by HBM: a row is read once, kept in registers between its
 // reduction and its use, and written once.
-#include "device_math.h"
 #include "kernels.h"
-#include "streaming.h"
+#include "rows.h"
 
 namespace moe {
 namespace {
-
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-    const v2bf v = {(__bf16)a, (__bf16)b};          // round to nearest even, NaN stays NaN
-    return __builtin_bit_cast(uint32_t, v);
-}
-
-// A row of d values lies in the NV * 8 registers of each of its threads as 8
-// consecutive values at ((v * tpr) + t) * 8, t of tpr threads.  VEC: d % 8 == 0, so
-// that each such 8 lie on 16 bytes and in the row or past it; otherwise the vector
-// accesses are to addresses of the values' own alignment, which this GPU takes, and
-// the row's last up to 7 values are accessed one by one (32768 rows of bf16 values
-// with residual: 999 wide 59 us against 84 with one value an access throughout, 4095
-// wide 305 against 494, but 100 wide 22 against 16; the backward of 131072 rows, 999
-// wide, 345 against 766).
-__device__ __forceinline__ int col_of(int v, int t, int tpr) { return (v * tpr + t) * 8; }
-
-template <bool VEC> struct Aligned {                     // four words
-    typedef uint32_t bf16 __attribute__((ext_vector_type(4)));
-    typedef float f32 __attribute__((ext_vector_type(4)));
-};
-template <> struct Aligned<false> {
-    typedef uint32_t bf16 __attribute__((ext_vector_type(4), aligned(2)));
-    typedef float f32 __attribute__((ext_vector_type(4), aligned(4)));
-};
-
-// 8 values of a row (zero past its end).  f32 is uniform over the launch.
-template <bool VEC>
-__device__ __forceinline__ void load8(const void* p, bool f32, int64_t row_off, int v, int t, int tpr, int d,
-                                      float (&x)[8]) {
-    const int c = col_of(v, t, tpr);
-    if (VEC ? c < d : c + 8 <= d) {
-        if (f32) {
-            const auto* q = reinterpret_cast<const typename Aligned<VEC>::f32*>(static_cast<const float*>(p) + row_off + c);
-            const v4f a = q[0], b = q[1];
-            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-        } else {
-            const v4u a = *reinterpret_cast<const typename Aligned<VEC>::bf16*>(static_cast<const uint16_t*>(p) + row_off + c);
-            x[0] = bf16_lo(a.x); x[1] = bf16_hi(a.x); x[2] = bf16_lo(a.y); x[3] = bf16_hi(a.y);
-            x[4] = bf16_lo(a.z); x[5] = bf16_hi(a.z); x[6] = bf16_lo(a.w); x[7] = bf16_hi(a.w);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            x[j] = VEC || c + j >= d ? 0.0f
-                   : f32             ? static_cast<const float*>(p)[row_off + c + j]
-                                     : bf16_to_f32(static_cast<const uint16_t*>(p)[row_off + c + j]);
-    }
-}
-
-// (not through put(): a template's argument drops the vector types' lower alignment)
-template <bool VEC, bool NT>
-__device__ __forceinline__ void store8(void* p, bool f32, int64_t row_off, int v, int t, int tpr, int d,
-                                       const float (&x)[8]) {
-    const int c = col_of(v, t, tpr);
-    if (VEC ? c < d : c + 8 <= d) {
-        if (f32) {
-            typedef typename Aligned<VEC>::f32 V;
-            V* q = reinterpret_cast<V*>(static_cast<float*>(p) + row_off + c);
-            const V a = {x[0], x[1], x[2], x[3]}, b = {x[4], x[5], x[6], x[7]};
-            if constexpr (NT) {
-                __builtin_nontemporal_store(a, q);
-                __builtin_nontemporal_store(b, q + 1);
-            } else {
-                q[0] = a;
-                q[1] = b;
-            }
-        } else {
-            typedef typename Aligned<VEC>::bf16 V;
-            V* q = reinterpret_cast<V*>(static_cast<uint16_t*>(p) + row_off + c);
-            const V a = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
-            if constexpr (NT) __builtin_nontemporal_store(a, q);
-            else *q = a;
-        }
-    } else if (!VEC) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (c + j >= d) continue;
-            if (f32) static_cast<float*>(p)[row_off + c + j] = x[j];
-            else static_cast<uint16_t*>(p)[row_off + c + j] = (uint16_t)pack_bf16(x[j], 0.0f);
-        }
-    }
-}
-
-// Sum over the threads of one row: the wave by shuffles, the waves through LDS
-// (two buffers in turn, so one barrier per row is enough).  Same order on every
-// run.
-template <bool WAVE_ROW>
-__device__ __forceinline__ float row_sum(float s, float (*part)[16], int flip) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
-    if constexpr (WAVE_ROW) return s;
-    const int nw = (int)blockDim.x >> 6;
-    if ((threadIdx.x & 63) == 0) part[flip][threadIdx.x >> 6] = s;
-    // a barrier for LDS alone: loads and stores under way go on
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    s = part[flip][0];
-    for (int i = 1; i < nw; ++i) s += part[flip][i];
-    return s;
-}
 
 // A block is one row (WAVE_ROW: each of its four waves is one); only a grid that
 // would pass the largest one makes it take more.  16384 rows of 7168 bf16 values
@@ -177,34 +72,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_kernel(AddR
             for (int j = 0; j < 8; ++j) y[j] = h[v][j] * rstd * w[v][j];
             if (a.y) store8<VEC, true>(a.y, false, off, v, t, tpr, d, y);
             if constexpr (VEC) {
-                if (a.q) {                            // d % 128 == 0: 16 lanes are one tile, all in the row or none
-                    const int c = col_of(v, t, tpr);
-                    float amax = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        const uint32_t b = pack_bf16(y[j], y[j + 1]);
-                        y[j] = bf16_lo(b);
-                        y[j + 1] = bf16_hi(b);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float m = __builtin_fabsf(y[j]);
-                        amax = m > amax ? m : amax;
-                    }
-#pragma unroll
-                    for (int o = 1; o < 16; o <<= 1) {
-                        const float m = __shfl_xor(amax, o, 64);
-                        amax = m > amax ? m : amax;
-                    }
-                    float inv, sc;
-                    tile_scale(amax, inv, sc);
-                    if (c < d) {
-                        put<true>(reinterpret_cast<v2u*>(a.q + off + c),
-                                v2u{e4m3_encode4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                                    e4m3_encode4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv)});
-                        if ((t & 15) == 0) a.scale[row * (d / 128) + c / 128] = sc;
-                    }
-                }
+                if (a.q) store_quant8(a.q, a.scale, row, d, col_of(v, t, tpr), t, y);
             }
         }
     }
@@ -284,54 +152,6 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void add_rmsnorm_backward_ke
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) store8<VEC, false>(a.part, true, (int64_t)blockIdx.x * d, v, t, tpr, d, dw[v]);
-}
-
-// The sum in pairs, pairs of pairs and so on: a term goes through log2 N roundings.
-template <int N>
-__device__ __forceinline__ float pairwise(const float (&x)[N]) {
-    float s[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = x[i];
-#pragma unroll
-    for (int n = N / 2; n > 0; n /= 2)
-#pragma unroll
-        for (int i = 0; i < n; ++i) s[i] = s[2 * i] + s[2 * i + 1];
-    return s[0];
-}
-
-// dw[c] = sum of the partial rows, pairwise: 16 threads take every 16th row of a
-// column, eight loads at a time, then their sums are added (512 rows of 7168: 6 us,
-// in which two blocks read every line, the 64 bytes of a row that one takes being half).
-// Added one after the other they took the same time and left dw 1.2 to 2.1 times the
-// error (32768 rows of 2048 FP32 values: 2.4e-7 of it, now 1.2e-7).
-constexpr int MOST_PARTIAL_ROWS = 2048;                  // of backward_most
-__global__ __launch_bounds__(256) void dw_reduce_kernel(const float* __restrict__ part, int rows, int d,
-                                                        float* __restrict__ dw) {
-    __shared__ float sum[16][17];
-    const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4;
-    const int c = blockIdx.x * 16 + cl;
-    float s[MOST_PARTIAL_ROWS / 128];
-#pragma unroll
-    for (int k = 0; k < MOST_PARTIAL_ROWS / 128; ++k) {
-        s[k] = 0.0f;
-        if (k * 128 < rows && c < d) {
-            const int r = k * 128 + rl;
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = part[(int64_t)min(r + 16 * i, rows - 1) * d + c];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = r + 16 * i < rows ? x[i] : 0.0f;
-            s[k] = pairwise(x);
-        }
-    }
-    sum[rl][cl] = pairwise(s);
-    __syncthreads();
-    if (rl == 0 && c < d) {
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = sum[i][cl];
-        dw[c] = pairwise(x);
-    }
 }
 
 // A row of up to `narrow` values is one wave, four to a block; a wider one is a
@@ -430,7 +250,7 @@ hipError_t launch_add_rmsnorm_backward(const AddRmsnormBackwardArgs& a, float* d
         if (e != hipSuccess) return e;
         rows = backward_blocks(a.T, a.d);
     }
-    hipLaunchKernelGGL(dw_reduce_kernel, dim3((a.d + 15) / 16), dim3(256), 0, st, a.part, rows, a.d, dw);
+    hipLaunchKernelGGL(dw_reduce_kernel, dim3((a.d + 15) / 16), dim3(256), 0, st, a.part, rows, a.d, dw, nullptr);
     return hipGetLastError();
 }
 

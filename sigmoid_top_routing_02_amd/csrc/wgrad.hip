@@ -35,7 +35,9 @@ struct WgradSrc {
     const float* gate;        // [T, K]
     const int32_t* slot_row;  // [T, K]
     const int32_t* row_token; // [R]
-    const float* z;           // [R, 2I]
+    const float* z;           // [R, 2I], or
+    const uint8_t* z_q;       // its codes [R, 2I]
+    const float* z_s;         // and scales [R, 2I/128]
     const float* dh_row;      // [R, I]
     const uint16_t* u;        // [T, d] bf16
     int64_t shared_row0;
@@ -59,7 +61,28 @@ __device__ __forceinline__ float row_weight(const WgradSrc& s, int64_t r, int64_
     return hit >= 0 ? s.gate[t * s.K + hit] : 0.0f;
 }
 
-template <int SRC, bool BLOCK_SCALE>
+// z's 4 values at column `at` of row r, from FP32 or (ZQ) from 8 bits
+template <bool ZQ> struct Z4 {
+    float4 v;
+    __device__ __forceinline__ void load(const WgradSrc& s, int64_t r, int at) {
+        v = *reinterpret_cast<const float4*>(s.z + r * 2 * s.I + at);
+    }
+    __device__ __forceinline__ float4 get() const { return v; }
+};
+template <> struct Z4<true> {
+    uint32_t c;
+    float sc;
+    __device__ __forceinline__ void load(const WgradSrc& s, int64_t r, int at) {
+        c = *reinterpret_cast<const uint32_t*>(s.z_q + r * 2 * s.I + at);
+        sc = s.z_s[r * (2 * s.I / 128) + (at >> 7)];
+    }
+    __device__ __forceinline__ float4 get() const {
+        const float4 x = e4m3_decode4(c);
+        return make_float4(x.x * sc, x.y * sc, x.z * sc, x.w * sc);
+    }
+};
+
+template <int SRC, bool BLOCK_SCALE, bool ZQ = false>
 __global__ __launch_bounds__(256) void wgrad_operand_kernel(WgradSrc s, const int32_t* __restrict__ go,
                                                             const int32_t* __restrict__ kb_start, int G, int C,
                                                             uint8_t* __restrict__ out_q, float* __restrict__ out_s) {
@@ -110,7 +133,8 @@ __global__ __launch_bounds__(256) void wgrad_operand_kernel(WgradSrc s, const in
         constexpr int NB = (SRC == SRC_DY || SRC == SRC_X) ? 16 : 8;
 #pragma unroll
         for (int b = 0; b < 16; b += NB) {
-            float4 la[NB], lb[NB], lc[NB];
+            float4 la[NB], lc[NB];
+            Z4<ZQ> za[NB], zb[NB];
             uint2 lx[NB];
 #pragma unroll
             for (int jj = 0; jj < NB; ++jj) {
@@ -121,14 +145,13 @@ __global__ __launch_bounds__(256) void wgrad_operand_kernel(WgradSrc s, const in
                 } else if constexpr (SRC == SRC_X) {
                     lx[jj] = *reinterpret_cast<const uint2*>(s.u + s_tok[i] * s.d + c);
                 } else if constexpr (SRC == SRC_H) {
-                    const float* zr = s.z + rl * 2 * s.I + (c >> 7) * 256 + (c & 127);
-                    la[jj] = *reinterpret_cast<const float4*>(zr);
-                    lb[jj] = *reinterpret_cast<const float4*>(zr + 128);
+                    const int at = (c >> 7) * 256 + (c & 127);
+                    za[jj].load(s, rl, at);
+                    zb[jj].load(s, rl, at + 128);
                 } else {
                     const int j = c >> 8, w = c & 255, ic = j * 128 + (w & 127);
-                    const float* zr = s.z + rl * 2 * s.I + j * 256 + (w & 127);
-                    la[jj] = *reinterpret_cast<const float4*>(zr);
-                    lb[jj] = *reinterpret_cast<const float4*>(zr + 128);
+                    za[jj].load(s, rl, j * 256 + (w & 127));
+                    zb[jj].load(s, rl, j * 256 + (w & 127) + 128);
                     lc[jj] = *reinterpret_cast<const float4*>(s.dh_row + rl * s.I + ic);
                 }
             }
@@ -146,13 +169,13 @@ __global__ __launch_bounds__(256) void wgrad_operand_kernel(WgradSrc s, const in
                         const uint2 x = lx[jj];
                         v[0] = bf16_lo(x.x); v[1] = bf16_hi(x.x); v[2] = bf16_lo(x.y); v[3] = bf16_hi(x.y);
                     } else if constexpr (SRC == SRC_H) {
-                        const float4 zg = la[jj], zu = lb[jj];
+                        const float4 zg = za[jj].get(), zu = zb[jj].get();
                         const float g4[4] = {zg.x, zg.y, zg.z, zg.w}, u4[4] = {zu.x, zu.y, zu.z, zu.w};
 #pragma unroll
                         for (int q = 0; q < 4; ++q) v[q] = g4[q] * sigm(g4[q]) * u4[q];
                     } else {
                         const int w = c & 255;
-                        const float4 zg = la[jj], zu = lb[jj], dh = lc[jj];
+                        const float4 zg = za[jj].get(), zu = zb[jj].get(), dh = lc[jj];
                         const float g4[4] = {zg.x, zg.y, zg.z, zg.w}, u4[4] = {zu.x, zu.y, zu.z, zu.w};
                         const float d4[4] = {dh.x, dh.y, dh.z, dh.w};
 #pragma unroll
@@ -266,18 +289,20 @@ hipError_t launch_wgrad_gemms(const int32_t* kb_start, int G, int d, int I, cons
 }
 
 hipError_t launch_wgrad_operands(const float* dh, const float* gate, const int32_t* slot_row,
-                                 const int32_t* row_token, const float* z, const float* dh_row,
-                                 const uint16_t* u, int64_t shared_row0, int K, int d, int I,
+                                 const int32_t* row_token, const float* z, const uint8_t* z_q, const float* z_s,
+                                 const float* dh_row, const uint16_t* u, int64_t shared_row0, int K, int d, int I,
                                  const int32_t* go, const int32_t* kb_start, int G, int n_kb,
                                  uint8_t* dyT_q, float* dyT_s, uint8_t* hT_q, float* hT_s, uint8_t* dzT_q,
                                  float* dzT_s, uint8_t* xT_q, float* xT_s, hipStream_t st) {
-    WgradSrc s{dh, gate, slot_row, row_token, z, dh_row, u, shared_row0, K, d, I};
+    WgradSrc s{dh, gate, slot_row, row_token, z, z_q, z_s, dh_row, u, shared_row0, K, d, I};
     hipLaunchKernelGGL((wgrad_operand_kernel<SRC_DY, false>), dim3((unsigned)n_kb, (unsigned)(d / 128)), dim3(256),
                        0, st, s, go, kb_start, G, d, dyT_q, dyT_s);
-    hipLaunchKernelGGL((wgrad_operand_kernel<SRC_H, true>), dim3((unsigned)(I / 128), (unsigned)n_kb), dim3(256),
-                       0, st, s, go, kb_start, G, I, hT_q, hT_s);
-    hipLaunchKernelGGL((wgrad_operand_kernel<SRC_DZ, false>), dim3((unsigned)(2 * I / 128), (unsigned)n_kb),
-                       dim3(256), 0, st, s, go, kb_start, G, 2 * I, dzT_q, dzT_s);
+    const auto h_kernel = z ? wgrad_operand_kernel<SRC_H, true> : wgrad_operand_kernel<SRC_H, true, true>;
+    const auto dz_kernel = z ? wgrad_operand_kernel<SRC_DZ, false> : wgrad_operand_kernel<SRC_DZ, false, true>;
+    hipLaunchKernelGGL(h_kernel, dim3((unsigned)(I / 128), (unsigned)n_kb), dim3(256), 0, st, s, go, kb_start, G, I, hT_q,
+                       hT_s);
+    hipLaunchKernelGGL(dz_kernel, dim3((unsigned)(2 * I / 128), (unsigned)n_kb), dim3(256), 0, st, s, go, kb_start, G,
+                       2 * I, dzT_q, dzT_s);
     hipLaunchKernelGGL((wgrad_operand_kernel<SRC_X, true>), dim3((unsigned)n_kb, (unsigned)(d / 128)), dim3(256),
                        0, st, s, go, kb_start, G, d, xT_q, xT_s);
     return hipGetLastError();
