@@ -184,10 +184,12 @@ int moe_balance_loss_backward(const float* scores, const int32_t* seq_count, con
  * dlogits FP32 [T,E], u bf16 [T,d], centroids (e) bf16 [E,d]; du_in, du FP32 [T,d] and
  * de_in, de FP32 [E,d]; du_in or de_in NULL: zeros; du or de NULL: not asked for (not
  * both).  du may be du_in itself and de de_in, so that the sums go on from
- * moe_router_backward's outputs in place.  The products are exact and summed in FP32
- * in an order that depends on T, d and E alone.  Infinite values of u or the centroids
- * give NaN.  ws: scratch of moe_router_logits_backward_workspace_bytes(T, d, E) bytes
- * (no setup needed; may be NULL when de is).
+ * moe_router_backward's outputs in place.  Every product is exact (each logit is taken
+ * as the sum of three bf16 that it is) and they are summed in FP32 in an order that
+ * depends on T, d and E alone; what is under the smallest normal FP32 number counts as
+ * zero, and infinite values of u or the centroids may give NaN.  ws: scratch of
+ * moe_router_logits_backward_workspace_bytes(T, d, E) bytes (no setup needed; may be
+ * NULL when T = 0): 6 bytes for each logit, and partial sums of de.
  * Limits: 0 <= T <= 2^24, d % 128 == 0, d <= 65536, 1 <= E <= 256.
  */
 size_t moe_router_logits_backward_workspace_bytes(int64_t T, int d, int E);   /* 0 outside the limits */

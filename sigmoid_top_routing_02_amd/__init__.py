@@ -990,8 +990,7 @@ def moe_router_logits_backward(dlogits, u, centroids, du_in=None, de_in=None, du
     if E > _INT_MAX or d > _INT_MAX:
         _too_large("E or d", max(E, d))
     dev = _current(dlogits, "dlogits")
-    pdu = pde = pws = None
-    ws_bytes = 0
+    pdu = pde = None
     if want_du:
         du, pdu = _out(du, torch.float32, (T, d), "du", dev)
     elif du is not None or du_in is not None:
@@ -999,9 +998,9 @@ def moe_router_logits_backward(dlogits, u, centroids, du_in=None, de_in=None, du
     L = _lib or load_library()
     if want_de:
         de, pde = _out(de, torch.float32, (E, d), "de", dev)
-        ws, pws, ws_bytes = _scratch(ws, L.moe_router_logits_backward_workspace_bytes(T, d, E), dev)
     elif de is not None or de_in is not None:
         raise MoEError("moe_router_logits_backward: de or de_in without want_de")
+    ws, pws, ws_bytes = _scratch(ws, L.moe_router_logits_backward_workspace_bytes(T, d, E), dev)
     pui = None if du_in is None else _in(du_in, torch.float32, (T, d), "du_in", dev)
     pei = None if de_in is None else _in(de_in, torch.float32, (E, d), "de_in", dev)
     st = L.moe_router_logits_backward(_in(dlogits, torch.float32, (T, E), "dlogits", dev),

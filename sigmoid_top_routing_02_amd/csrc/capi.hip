@@ -215,12 +215,15 @@ int moe_router_logits_backward(const float* dlogits, const void* u_bf16, const v
         REQUIRE_PTR(de);
         if (T > 0) REQUIRE_PTR(u_bf16);
         if (de_in) REQUIRE_PTR(de_in);
+    }
+    if (T > 0) {
+        REQUIRE_PTR(dlogits);
         REQUIRE_PTR(ws);
         REQUIRE(ws_bytes >= moe::router_logits_backward_ws_bytes(T, d, E), MOE_ERR_WORKSPACE,
                 "moe_router_logits_backward: workspace %zu < %zu bytes", ws_bytes,
                 moe::router_logits_backward_ws_bytes(T, d, E));
     }
-    if (T > 0) REQUIRE_PTR(dlogits);
+    if (T == 0 && !de) return MOE_OK;
     return hip_status(moe::launch_router_logits_backward(dlogits, static_cast<const uint16_t*>(u_bf16),
                                                          static_cast<const uint16_t*>(centroids_bf16), T, d, E, du_in,
                                                          de_in, du, de, ws, S(stream)),
