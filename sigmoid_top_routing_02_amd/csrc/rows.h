@@ -95,6 +95,37 @@ __device__ __forceinline__ void store8(void* p, bool f32, int64_t row_off, int v
     }
 }
 
+// Sums and maxima over lanes without LDS: within 16 lanes by DPP (neighbours, pairs,
+// halves, all 16 mirrored), then over the wave's four sixteens by lane swaps.  Every
+// lane gets the same bits.  (A row of LDS shuffles is six times their latency.)
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float sum16(float s) {
+    s += dpp<0xB1>(s);                                // quad_perm 1 0 3 2
+    s += dpp<0x4E>(s);                                // quad_perm 2 3 0 1
+    s += dpp<0x141>(s);                               // row_half_mirror
+    return s + dpp<0x140>(s);                         // row_mirror
+}
+__device__ __forceinline__ float wave_sum(float s) {
+    s = sum16(s);
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(s), __float_as_uint(s), false, false);
+    s = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(s), __float_as_uint(s), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+__device__ __forceinline__ float max16(float m) {     // a NaN counts as less than anything
+    float o = dpp<0xB1>(m);
+    m = o > m ? o : m;
+    o = dpp<0x4E>(m);
+    m = o > m ? o : m;
+    o = dpp<0x141>(m);
+    m = o > m ? o : m;
+    o = dpp<0x140>(m);
+    return o > m ? o : m;
+}
+
 // y rounded to bf16 and its 1x128 E4M3 tiles: 8 values at column c of a row of d,
 // d % 128 == 0, so that 16 lanes are one tile, all in the row or none.
 __device__ __forceinline__ void store_quant8(uint8_t* q, float* scale, int64_t row, int d, int c, int t, float (&y)[8]) {
@@ -110,11 +141,7 @@ __device__ __forceinline__ void store_quant8(uint8_t* q, float* scale, int64_t r
         const float m = __builtin_fabsf(y[j]);
         amax = m > amax ? m : amax;
     }
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) {
-        const float m = __shfl_xor(amax, o, 64);
-        amax = m > amax ? m : amax;
-    }
+    amax = max16(amax);
     float inv, sc;
     tile_scale(amax, inv, sc);
     if (c < d) {
@@ -142,27 +169,21 @@ __device__ __forceinline__ float row_sum(float s, float (*part)[16], int flip) {
     return s;
 }
 
-// Two such sums at once.
+// Two such sums at once, the waves' by wave_sum.
 template <bool WAVE_ROW>
 __device__ __forceinline__ void row_sum2(float& a, float& b, float (*part)[16]) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        a += __shfl_xor(a, o, 64);
-        b += __shfl_xor(b, o, 64);
-    }
+    a = wave_sum(a);
+    b = wave_sum(b);
     if constexpr (WAVE_ROW) return;
-    const int nw = (int)blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0) {
         part[0][threadIdx.x >> 6] = a;
         part[1][threadIdx.x >> 6] = b;
     }
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    a = part[0][0];
-    b = part[1][0];
-    for (int i = 1; i < nw; ++i) {
-        a += part[0][i];
-        b += part[1][i];
-    }
+    const int w = threadIdx.x & 15;                   // 16 lanes hold one wave's each
+    const bool in = w < (int)blockDim.x >> 6;
+    a = sum16(in ? part[0][w] : 0.0f);
+    b = sum16(in ? part[1][w] : 0.0f);
 }
 
 // The sum in pairs, pairs of pairs and so on: a term goes through log2 N roundings.
