@@ -21,6 +21,8 @@
 // block per sequence adds the chunks in order and reduces the E terms by a
 // fixed tree.
 #include "kernels.h"
+#include "lanes.h"
+#include "streaming.h"
 
 namespace moe {
 namespace {
@@ -148,13 +150,48 @@ struct BalanceRun {                 // record of a run; [256] each, but a call's
     int32_t n[256];
 };
 
-// lane l of a wave holds the experts l + 64 j of a token
+// LPT lanes hold a token, 4 of its experts each: 4 l to 4 l + 3 (VEC: E % 4 == 0), or
+// l + LPT j.
+template <int LPT, bool VEC>
+__device__ __forceinline__ int expert_of(int l, int j) { return VEC ? 4 * l + j : l + LPT * j; }
+
+template <int LPT, bool VEC>
+__device__ __forceinline__ void load_experts(const float* row, int l, int E, bool in, float (&v)[4]) {
+    if constexpr (VEC) {
+        const float4 x = in && 4 * l < E ? *reinterpret_cast<const float4*>(row + 4 * l) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = in && l + LPT * j < E ? row[l + LPT * j] : 0.0f;
+    }
+}
+
+template <int LPT>
+__device__ __forceinline__ float token_sum(float s) {
+    return LPT == 16 ? sum16(s) : wave_sum(s);
+}
+
+// A token's shares p = v / sum v from its reciprocal (0 where the sum is): sums under
+// 2^-64 are scaled up first, so that the reciprocal stays finite.
+template <int LPT>
+__device__ __forceinline__ void shares(const float (&v)[4], float (&p)[4]) {
+    const float sum = token_sum<LPT>((v[0] + v[1]) + (v[2] + v[3]));
+    const float up = __builtin_fabsf(sum) < 0x1p-64f ? 0x1p64f : 1.0f;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / (sum * up);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = v[j] * up * inv;
+}
+
+constexpr int AT_ONCE = 4;          // tokens whose loads go out together
+
+template <int LPT, bool VEC>
 __global__ __launch_bounds__(64 * RUN_WAVES) void balance_runs_kernel(
     const float* __restrict__ s, const int32_t* __restrict__ idx, const int32_t* __restrict__ start, int n_seq, int T,
     int E, int K, int chunk, BalanceRun* __restrict__ rec, int32_t* __restrict__ chunk_n) {
+    constexpr int GROUPS = 64 * RUN_WAVES / LPT, WIDE = 4 * LPT;
     __shared__ int cnt[256];
-    __shared__ float psum[RUN_WAVES][256];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ float psum[GROUPS][WIDE];
+    const int tid = threadIdx.x, l = tid % LPT, grp = tid / LPT;
     const int tb = blockIdx.x * chunk, te = min(T, tb + chunk);
     int all = 0;                                      // thread = expert: counts over the chunk's runs
     for (int q = seq_of(start, n_seq, T, tb); q < n_seq; ++q) {
@@ -166,39 +203,54 @@ __global__ __launch_bounds__(64 * RUN_WAVES) void balance_runs_kernel(
         }
         if (tid < 256) cnt[tid] = 0;
         __syncthreads();
+        for (int64_t i = (int64_t)rb * K + tid; i < (int64_t)re * K; i += 64 * RUN_WAVES) {
+            const int e = idx[i];
+            if ((unsigned)e < (unsigned)E) atomicAdd(&cnt[e], 1);          // integers: exact in any order
+        }
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int t = rb + wave; t < re; t += RUN_WAVES) {
-            const float* row = s + (int64_t)t * E;
-            float v[4], sum = 0.0f;
+        for (int t = rb + grp; t < re; t += AT_ONCE * GROUPS) {
+            float v[AT_ONCE][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[j] = lane + 64 * j < E ? row[lane + 64 * j] : 0.0f;
-                sum += v[j];
-            }
+            for (int k = 0; k < AT_ONCE; ++k)
+                load_experts<LPT, VEC>(s + (int64_t)(t + k * GROUPS) * E, l, E, t + k * GROUPS < re, v[k]);
 #pragma unroll
-            for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
-            if (sum != 0.0f) {
+            for (int k = 0; k < AT_ONCE; ++k) {
+                float p[4];
+                shares<LPT>(v[k], p);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[j] += v[j] / sum;
-            }
-            if (lane < K) {
-                const int e = idx[(int64_t)t * K + lane];
-                if ((unsigned)e < (unsigned)E) atomicAdd(&cnt[e], 1);      // integers: exact in any order
+                for (int j = 0; j < 4; ++j) acc[j] += p[j];
             }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) psum[wave][lane + 64 * j] = acc[j];
+        for (int j = 0; j < 4; ++j) psum[grp][expert_of<LPT, VEC>(l, j)] = acc[j];
         __syncthreads();
         if (tid < E) {
-            float p = 0.0f;
-            for (int w = 0; w < RUN_WAVES; ++w) p += psum[w][tid];
-            rec[blockIdx.x + q].p[tid] = p;
+            float p[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int g = 0; g < GROUPS; g += 4)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[i] += psum[g + i][tid];
+            rec[blockIdx.x + q].p[tid] = (p[0] + p[1]) + (p[2] + p[3]);
             rec[blockIdx.x + q].n[tid] = cnt[tid];
             all += cnt[tid];
         }
         __syncthreads();
     }
     if (tid < E) chunk_n[blockIdx.x * 256 + tid] = all;
+}
+
+// The sum of x(c) for c = c0 + part, c0 + part + 4, .. up to c1, in that order, 16 loads
+// at a time.
+template <typename V, typename Load>
+__device__ __forceinline__ V every_fourth(int c0, int c1, int part, Load&& x) {
+    V s = 0;
+    for (int c = c0 + part; c <= c1; c += 64) {
+        V v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = x(min(c + 4 * i, c1));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s += c + 4 * i <= c1 ? v[i] : (V)0;
+    }
+    return s;
 }
 
 // One block per sequence, and one for the counts over all of them: thread = expert
@@ -213,10 +265,8 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const BalanceRun* __r
     __shared__ int ns[4][256];
     const int e = threadIdx.x & 255, part = threadIdx.x >> 8, q = blockIdx.x;
     if (q == n_seq) {
-        int n = 0;
-        if (e < E)
-            for (int c = part; c * chunk < T; c += 4) n += chunk_n[c * 256 + e];
-        ns[part][e] = n;
+        ns[part][e] = e < E ? every_fourth<int>(0, (T + chunk - 1) / chunk - 1, part,
+                                                [&](int c) { return chunk_n[c * 256 + e]; }) : 0;
         __syncthreads();
         if (part == 0 && e < E) expert_count[e] = (ns[0][e] + ns[1][e]) + (ns[2][e] + ns[3][e]);
         return;
@@ -226,69 +276,78 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const BalanceRun* __r
     int n = 0;
     if (L > 0 && e < E) {
         const int c0 = b / chunk, c1 = (b + L - 1) / chunk;
-        for (int c = c0 + part; c <= c1; c += 4) {
-            p += rec[c + q].p[e];
-            n += rec[c + q].n[e];
-        }
+        p = every_fourth<float>(c0, c1, part, [&](int c) { return rec[c + q].p[e]; });
+        n = every_fourth<int>(c0, c1, part, [&](int c) { return rec[c + q].n[e]; });
     }
     ps[part][e] = p;
     ns[part][e] = n;
     __syncthreads();
-    if (part == 0) {
-        p = (ps[0][e] + ps[1][e]) + (ps[2][e] + ps[3][e]);
-        n = (ns[0][e] + ns[1][e]) + (ns[2][e] + ns[3][e]);
-        if (e < E) seq_count[(int64_t)q * E + e] = n;
-        const float len = (float)max(L, 1), f = (float)E * (float)n / ((float)K * len);
-        ps[0][e] = f * (p / len);
-    }
+    if (part) return;
+    p = (ps[0][e] + ps[1][e]) + (ps[2][e] + ps[3][e]);
+    n = (ns[0][e] + ns[1][e]) + (ns[2][e] + ns[3][e]);
+    if (e < E) seq_count[(int64_t)q * E + e] = n;
+    const float len = (float)max(L, 1), f = (float)E * (float)n / ((float)K * len);
+    const float term = wave_sum(f * (p / len));      // four waves are left
+    __shared__ float wave_term[4];
+    if ((e & 63) == 0) wave_term[e >> 6] = term;
     __syncthreads();
-    for (int h = 128; h >= 1; h >>= 1) {
-        if (threadIdx.x < (unsigned)h) ps[0][threadIdx.x] += ps[0][threadIdx.x + h];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) loss[q] = alpha * ps[0][0];
+    if (e == 0) loss[q] = alpha * ((wave_term[0] + wave_term[1]) + (wave_term[2] + wave_term[3]));
 }
 
-// One wave per token.
+// LPT lanes go through EACH consecutive tokens: their sequence is looked for once and
+// followed from there, its f kept as long as it lasts.
+constexpr int EACH = 8;
+
+template <int LPT, bool VEC, bool NT>
 __global__ __launch_bounds__(256) void balance_backward_kernel(
     const float* __restrict__ s, const int32_t* __restrict__ seq_count, const int32_t* __restrict__ start, int n_seq,
     int T, int E, int K, float alpha, const float* __restrict__ dloss, const float* in, float* out) {
-    const int lane = threadIdx.x & 63;
-    for (int t = blockIdx.x * 4 + (threadIdx.x >> 6); t < T; t += gridDim.x * 4) {        // T <= 2^30
-        const int q = seq_of(start, n_seq, T, t);
-        const int b = q < n_seq ? seq_start_at(start, q, n_seq, T) : T;
-        const bool inside = t >= b;
-        float v[4], g[4], f[4] = {0.f, 0.f, 0.f, 0.f};
-        float sum = 0.0f, fp = 0.0f, coef = 0.0f;
+    constexpr int GROUPS = 256 / LPT;
+    typedef float v4f __attribute__((ext_vector_type(4)));
+    const int l = threadIdx.x % LPT;
+    const int64_t first = ((int64_t)blockIdx.x * GROUPS + threadIdx.x / LPT) * EACH;
+    if (first >= T) return;                           // whole groups of lanes
+    const int t0 = (int)first, te = min(T, t0 + EACH);
+    int q = -1, qb = 0, qe = 0;                       // the sequence that holds the last token looked at, or none yet
+    float f[4], coef = 0.0f;
+    for (int tt = t0; tt < te; tt += AT_ONCE) {
+        float v[AT_ONCE][4], g[AT_ONCE][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int e = lane + 64 * j;
-            v[j] = e < E ? s[(int64_t)t * E + e] : 0.0f;
-            g[j] = in && e < E ? in[(int64_t)t * E + e] : 0.0f;
-            sum += v[j];
+        for (int k = 0; k < AT_ONCE; ++k) {
+            load_experts<LPT, VEC>(s + (int64_t)(tt + k) * E, l, E, tt + k < te, v[k]);
+            load_experts<LPT, VEC>(in + (int64_t)(tt + k) * E, l, E, in && tt + k < te, g[k]);
         }
-        if (inside) {
-            const float len = (float)(seq_start_at(start, q + 1, n_seq, T) - b);
-            const float per = (float)E / ((float)K * len);
-            coef = (dloss ? dloss[q] : 1.0f) * alpha / len;
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            const int t = tt + k;
+            if (t >= te) break;
+            if (q < 0 || (t >= qe && q < n_seq)) {
+                q = seq_of(start, n_seq, T, t);
+                qb = q < n_seq ? seq_start_at(start, q, n_seq, T) : T;
+                qe = q < n_seq ? seq_start_at(start, q + 1, n_seq, T) : T;
+                const float len = (float)max(qe - qb, 1), per = (float)E / ((float)K * len);
+                coef = q < n_seq ? (dloss ? dloss[q] : 1.0f) * alpha / len : 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int e = expert_of<LPT, VEC>(l, j);
+                    f[j] = q < n_seq && e < E ? per * (float)seq_count[(int64_t)q * E + e] : 0.0f;
+                }
+            }
+            float p[4], o[4];
+            shares<LPT>(v[k], p);
+            const float fp = token_sum<LPT>(__builtin_fmaf(f[3], p[3], f[2] * p[2]) + __builtin_fmaf(f[1], p[1], f[0] * p[0]));
+            const bool inside = t >= qb;              // qb = T behind the last sequence
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (lane + 64 * j < E) f[j] = per * (float)seq_count[(int64_t)q * E + lane + 64 * j];
-        }
+                o[j] = inside ? __builtin_fmaf(coef * p[j] * (1.0f - v[k][j]), f[j] - fp, g[k][j]) : g[k][j];
+            float* const row = out + (int64_t)t * E;
+            if constexpr (VEC) {
+                if (4 * l < E) put<NT>(reinterpret_cast<v4f*>(row + 4 * l), v4f{o[0], o[1], o[2], o[3]});
+            } else {
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
-        float p[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            p[j] = sum != 0.0f ? v[j] / sum : 0.0f;
-            fp = __builtin_fmaf(f[j], p[j], fp);
-        }
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) fp += __shfl_xor(fp, o, 64);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int e = lane + 64 * j;
-            if (e < E) out[(int64_t)t * E + e] = inside ? __builtin_fmaf(coef * p[j] * (1.0f - v[j]), f[j] - fp, g[j]) : g[j];
+                for (int j = 0; j < 4; ++j)
+                    if (l + LPT * j < E) put<NT>(row + l + LPT * j, o[j]);
+            }
         }
     }
 }
@@ -312,9 +371,11 @@ hipError_t launch_balance_loss(const float* s, const int32_t* idx, const int32_t
     BalanceRun* rec = static_cast<BalanceRun*>(ws);
     const int chunk = balance_chunk(T), chunks = (int)((T + chunk - 1) / chunk);
     int32_t* chunk_n = reinterpret_cast<int32_t*>(rec + chunks + n_seq);
+    const auto runs = E > 64 ? E % 4 ? balance_runs_kernel<64, false> : balance_runs_kernel<64, true>
+                             : E % 4 ? balance_runs_kernel<16, false> : balance_runs_kernel<16, true>;
     if (T > 0)
-        hipLaunchKernelGGL(balance_runs_kernel, dim3(chunks), dim3(64 * RUN_WAVES), 0, st, s, idx, start, n_seq, (int)T, E,
-                           K, chunk, rec, chunk_n);
+        hipLaunchKernelGGL(runs, dim3(chunks), dim3(64 * RUN_WAVES), 0, st, s, idx, start, n_seq, (int)T, E, K, chunk, rec,
+                           chunk_n);
     hipLaunchKernelGGL(balance_sum_kernel, dim3(n_seq + (expert_count ? 1 : 0)), dim3(1024), 0, st, rec, chunk_n, start,
                        n_seq, (int)T, E, K, chunk, alpha, loss, seq_count, expert_count);
     return hipGetLastError();
@@ -323,9 +384,15 @@ hipError_t launch_balance_loss(const float* s, const int32_t* idx, const int32_t
 hipError_t launch_balance_loss_backward(const float* s, const int32_t* seq_count, const int32_t* start, int n_seq,
                                         int64_t T, int E, int K, float alpha, const float* dloss, const float* in,
                                         float* out, hipStream_t st) {
-    const int64_t blocks = (T + 3) / 4;
-    hipLaunchKernelGGL(balance_backward_kernel, dim3((unsigned)(blocks < (1 << 23) ? blocks : (1 << 23))), dim3(256), 0, st,
-                       s, seq_count, start, n_seq, (int)T, E, K, alpha, dloss, in, out);
+    const int lanes = E > 64 ? 64 : 16;
+    const int64_t each = (int64_t)EACH * 256 / lanes;
+    const bool nt = streamed(T * E * 4);
+    const auto kernel = E > 64 ? E % 4 ? nt ? balance_backward_kernel<64, false, true> : balance_backward_kernel<64, false, false>
+                                       : nt ? balance_backward_kernel<64, true, true> : balance_backward_kernel<64, true, false>
+                               : E % 4 ? nt ? balance_backward_kernel<16, false, true> : balance_backward_kernel<16, false, false>
+                                       : nt ? balance_backward_kernel<16, true, true> : balance_backward_kernel<16, true, false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((T + each - 1) / each)), dim3(256), 0, st, s, seq_count, start, n_seq, (int)T, E,
+                       K, alpha, dloss, in, out);
     return hipGetLastError();
 }
 

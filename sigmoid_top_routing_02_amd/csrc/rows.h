@@ -3,6 +3,7 @@
 #pragma once
 
 #include "device_math.h"
+#include "lanes.h"
 #include "streaming.h"
 
 namespace moe {
@@ -93,37 +94,6 @@ __device__ __forceinline__ void store8(void* p, bool f32, int64_t row_off, int v
             else static_cast<uint16_t*>(p)[row_off + c + j] = (uint16_t)pack_bf16(x[j], 0.0f);
         }
     }
-}
-
-// Sums and maxima over lanes without LDS: within 16 lanes by DPP (neighbours, pairs,
-// halves, all 16 mirrored), then over the wave's four sixteens by lane swaps.  Every
-// lane gets the same bits.  (A row of LDS shuffles is six times their latency.)
-template <int CTRL>
-__device__ __forceinline__ float dpp(float x) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
-}
-__device__ __forceinline__ float sum16(float s) {
-    s += dpp<0xB1>(s);                                // quad_perm 1 0 3 2
-    s += dpp<0x4E>(s);                                // quad_perm 2 3 0 1
-    s += dpp<0x141>(s);                               // row_half_mirror
-    return s + dpp<0x140>(s);                         // row_mirror
-}
-__device__ __forceinline__ float wave_sum(float s) {
-    s = sum16(s);
-    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(s), __float_as_uint(s), false, false);
-    s = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(s), __float_as_uint(s), false, false);
-    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-__device__ __forceinline__ float max16(float m) {     // a NaN counts as less than anything
-    float o = dpp<0xB1>(m);
-    m = o > m ? o : m;
-    o = dpp<0x4E>(m);
-    m = o > m ? o : m;
-    o = dpp<0x141>(m);
-    m = o > m ? o : m;
-    o = dpp<0x140>(m);
-    return o > m ? o : m;
 }
 
 // y rounded to bf16 and its 1x128 E4M3 tiles: 8 values at column c of a row of d,
