@@ -134,13 +134,21 @@ __device__ __forceinline__ int seq_start_at(const int32_t* __restrict__ start, i
     return min(max(start[i], 0), T);
 }
 
-// The first sequence that ends behind token t (n_seq if none does).
+// The first sequence that ends behind token t (n_seq if none does): LPT lanes, who all
+// want the same, look at LPT ends at a time.
+template <int LPT>
 __device__ __forceinline__ int seq_of(const int32_t* __restrict__ start, int n_seq, int T, int t) {
+    const int l = threadIdx.x % LPT, shift = (threadIdx.x & 63) / LPT * LPT;
     int lo = 0, hi = n_seq;
     while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (seq_start_at(start, mid + 1, n_seq, T) > t) hi = mid;
-        else lo = mid + 1;
+        const int step = (hi - lo + LPT - 1) / LPT, at = lo + (l + 1) * step - 1;
+        const uint64_t ends = __ballot(at >= hi || seq_start_at(start, at + 1, n_seq, T) > t) >> shift;
+        const uint64_t mine = LPT == 64 ? ends : ends & 0xFFFFull;
+        if (!mine) return hi;
+        const int first = __builtin_ctzll(mine);
+        hi = min(hi, lo + (first + 1) * step - 1);    // the answer at most, as that one ends behind t
+        lo = lo + first * step;
+        if (step == 1) return lo;
     }
     return lo;
 }
@@ -194,11 +202,11 @@ __global__ __launch_bounds__(64 * RUN_WAVES) void balance_runs_kernel(
     const int tid = threadIdx.x, l = tid % LPT, grp = tid / LPT;
     const int tb = blockIdx.x * chunk, te = min(T, tb + chunk);
     int all = 0;                                      // thread = expert: counts over the chunk's runs
-    for (int q = seq_of(start, n_seq, T, tb); q < n_seq; ++q) {
+    for (int q = seq_of<64>(start, n_seq, T, tb); q < n_seq; ++q) {
         const int rb = max(tb, seq_start_at(start, q, n_seq, T)), re = min(te, seq_start_at(start, q + 1, n_seq, T));
         if (rb >= te) break;
         if (rb >= re) {                               // an empty sequence has no record; nor have those behind it
-            q = max(q, seq_of(start, n_seq, T, rb) - 1);
+            q = max(q, seq_of<64>(start, n_seq, T, rb) - 1);
             continue;
         }
         if (tid < 256) cnt[tid] = 0;
@@ -296,7 +304,7 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const BalanceRun* __r
 
 // LPT lanes go through EACH consecutive tokens: their sequence is looked for once and
 // followed from there, its f kept as long as it lasts.
-constexpr int EACH = 8;
+constexpr int EACH = 4;
 
 template <int LPT, bool VEC, bool NT>
 __global__ __launch_bounds__(256) void balance_backward_kernel(
@@ -322,7 +330,7 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(
             const int t = tt + k;
             if (t >= te) break;
             if (q < 0 || (t >= qe && q < n_seq)) {
-                q = seq_of(start, n_seq, T, t);
+                q = seq_of<LPT>(start, n_seq, T, t);
                 qb = q < n_seq ? seq_start_at(start, q, n_seq, T) : T;
                 qe = q < n_seq ? seq_start_at(start, q + 1, n_seq, T) : T;
                 const float len = (float)max(qe - qb, 1), per = (float)E / ((float)K * len);
