@@ -109,41 +109,19 @@ struct LogitsDuArgs {
     float* out;
 };
 
-// The stages are separate LDS objects, so that the compiler sees that reads of one do
-// not wait for the DMA into another.
-__shared__ __attribute__((aligned(1024))) char g_stage0[64 * 1024];
-__shared__ __attribute__((aligned(1024))) char g_stage1[64 * 1024];
-
-template <int ST>
-__device__ __forceinline__ char* stage() {
-    if constexpr (ST == 0) return g_stage0;
-    else return g_stage1;
-}
-
 template <int V> struct IC { static constexpr int value = V; };
 
 constexpr int DU_STEP = 64;             // columns
 __shared__ __attribute__((aligned(1024))) char g_e0[256 * DU_STEP * 2];
 __shared__ __attribute__((aligned(1024))) char g_e1[256 * DU_STEP * 2];
-__shared__ __attribute__((aligned(1024))) char g_in0[4 * CHUNK * DU_STEP * 4];
-__shared__ __attribute__((aligned(1024))) char g_in1[4 * CHUNK * DU_STEP * 4];
-__shared__ __attribute__((aligned(1024))) char g_in2[4 * CHUNK * DU_STEP * 4];
 
-template <int SLOT>
-__device__ __forceinline__ char* in_slot() {
-    if constexpr (SLOT == 0) return g_in0;
-    else if constexpr (SLOT == 1) return g_in1;
-    else return g_in2;
-}
-
-// du: a wave (one to a SIMD) holds the fragments of its 32 tokens for all experts in
-// registers and goes through the columns 64 at a time; the block's four waves share
-// each step's centroids in LDS, sent for a step ahead.  du_in comes by DMA too, two
-// steps ahead, and is added, and the sums stored, a step after their products, spread
-// between the next step's matrix instructions: no wait is for memory that has not had
-// a step's time.
+// du: a wave holds the fragments of its 32 tokens for all experts in registers and goes
+// through the columns, the block's four waves sharing 64 columns' centroids at a time
+// in LDS, sent for a step ahead; 32 columns are multiplied, added to du_in and stored at
+// a time.  Two blocks share a CU, so that one multiplies while the other waits for
+// du_in or for its stores to go out.
 template <int EP, bool ADD, bool NT>
-__global__ __launch_bounds__(256, 1) void logits_du_kernel(LogitsDuArgs a) {
+__global__ __launch_bounds__(256, 2) void logits_du_kernel(LogitsDuArgs a) {
     constexpr int KS = EP / 16;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -152,7 +130,7 @@ __global__ __launch_bounds__(256, 1) void logits_du_kernel(LogitsDuArgs a) {
     const int64_t chunk = (int64_t)blockIdx.x * 4 + wave;
     const int64_t t0 = chunk * CHUNK;
     const int rows = t0 < a.T ? (int)(a.T - t0 < CHUNK ? a.T - t0 : CHUNK) : 0;
-    const int first = blockIdx.y * a.steps, steps = min(a.steps, a.d / DU_STEP - first);
+    const int s0 = blockIdx.y * a.steps, s1 = min(s0 + a.steps, a.d / DU_STEP);
 
     const auto e_rsrc = make_rsrc(a.e, (uint32_t)a.E * (uint32_t)a.d * 2u);
     const int dr = lane >> 3;                       // DMA: row of 8 and chunk of 8
@@ -161,28 +139,17 @@ __global__ __launch_bounds__(256, 1) void logits_du_kernel(LogitsDuArgs a) {
         char* const to = decltype(st)::value ? g_e1 : g_e0;
 #pragma unroll
         for (int j = 0; j < EP / 32; ++j)
-            lds_dma16(e_rsrc, dma_off + (uint32_t)(j * 32) * (uint32_t)a.d * 2u, (uint32_t)(first + s) * (DU_STEP * 2u),
+            lds_dma16(e_rsrc, dma_off, (uint32_t)(j * 32) * (uint32_t)a.d * 2u + (uint32_t)s * (DU_STEP * 2u),
                       to + (j * 4 + wave) * 1024);
     };
     // rows past the last token are out of the descriptors' range
-    const uint32_t records = (uint32_t)rows * (uint32_t)a.d * 4u;
+    const uint32_t records = (uint32_t)rows * (uint32_t)a.d * 4u, row4 = (uint32_t)a.d * 4u;
     const auto in_rsrc = make_rsrc(ADD ? a.in + t0 * a.d : a.out, ADD ? records : 0u);
     const auto out_rsrc = make_rsrc(a.out + t0 * a.d, records);
-    // the wave's 32 rows of 256 bytes, four to a DMA; chunks of rows 4 apart are swapped
-    // by 128 bytes, so that the two halves of a wave read different banks
-    auto send_in = [&](auto slot, int s) {          // 8 DMAs
-        if constexpr (ADD) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t r = (uint32_t)(4 * j + (lane >> 4)), c = (uint32_t)((lane & 15) ^ ((j & 1) << 3));
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(in_rsrc, (lds_void*)(in_slot<decltype(slot)::value>() + (wave * 8 + j) * 1024), 16,
-                                                         r * (uint32_t)a.d * 4u + c * 16u, (uint32_t)(first + s) * (DU_STEP * 4u), 0,
-                                                         NT ? 2 : 0);
-            }
-        }
-    };
-    send(IC<0>{}, 0);
-    send_in(IC<0>{}, 0);
+    // result i of 16 of the lane's column lane % 32: row 8 (i / 4) + 4 half + i % 4
+    const uint32_t out_off = (uint32_t)(4 * half) * row4 + (uint32_t)(lane & 31) * 4u;
+    auto at = [&](int i) { return out_off + (uint32_t)(8 * (i / 4) + i % 4) * row4; };
+    send(IC<0>{}, s0);
     v8bf x[3][KS];
     {
         const int t = lane & 31;
@@ -193,108 +160,49 @@ __global__ __launch_bounds__(256, 1) void logits_du_kernel(LogitsDuArgs a) {
             for (int k = 0; k < KS; ++k)
                 x[w][k] = *reinterpret_cast<const v8bf*>(p + w * CHUNK * EP * 2 + ((2 * k + half) ^ swizzle<EP * 2>(t)) * 16);
     }
-    // result i of 16 of the lane's column lane % 32: row 8 (i / 4) + 4 half + i % 4
-    const uint32_t row4 = (uint32_t)a.d * 4u;
-    const uint32_t out_off = (uint32_t)(4 * half) * row4 + (uint32_t)(lane & 31) * 4u;
-    const int in_off = wave * 8192 + half * 1024 + (((lane & 31) * 4) ^ (half << 7));
     // the lane's part of a transposing read: row i16 / 4 of 4, 8 bytes of its column;
-    // the second column tile starts 64 bytes on
+    // the second 32 columns start 64 bytes on
     const int read_off = (8 * (g >> 1) + (i16 >> 2)) * 128 +
                          ((2 * (g & 1) + ((i16 & 3) >> 1)) ^ swizzle<128>(i16 >> 2)) * 16 + (i16 & 1) * 8;
-    v16f acc[2][2];
-    // result j of 32 of a step: du_in from its slot, and the sum's store
-    auto add_in = [&](auto slot, int j) -> float {
-        const int n = j / 16, i = j % 16;
-        if constexpr (ADD)
-            return *reinterpret_cast<const float*>(in_slot<decltype(slot)::value>() + (in_off ^ (n * 128)) +
-                                                   (8 * (i / 4) + i % 4) * 256);
-        else return 0.0f;
-    };
-    auto store = [&](float o, int j, int s) {
-        const int n = j / 16, i = j % 16;
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, o), out_rsrc,
-                                              out_off + (uint32_t)(8 * (i / 4) + i % 4) * row4 + n * 128,
-                                              (first + s) * (DU_STEP * 4), NT ? 2 : 0);
-    };
-    constexpr int PER = 32 / KS;                    // results that are finished with every 16 experts
-    // step s, the AT-th of six that go round: stage AT % 2, du_in's slot AT % 3
-    auto step = [&](auto at, auto first, int s) {
-        constexpr int AT = decltype(at)::value, ST = AT % 2;
-        constexpr bool FIRST = decltype(first)::value;
-        if (s + 1 < steps) {
-            send(IC<1 - ST>{}, s + 1);
-            send_in(IC<(AT + 1) % 3>{}, s + 1);
-        }
-        const char* const b = ST ? g_e1 : g_e0;
-        v8bf f[2][2];
-        float in[2][PER];
-        auto read = [&](int k) {
-            f[k & 1][0] = column8(b + read_off + k * 2048, 512);
-            f[k & 1][1] = column8(b + (read_off ^ 64) + k * 2048, 512);
-            if constexpr (!FIRST) {
+    auto columns32 = [&](const char* b, int col) {  // col: the first of them
+        float old[16];
+        if constexpr (ADD) {
 #pragma unroll
-                for (int j = 0; j < PER; ++j) in[k & 1][j] = add_in(IC<(AT + 2) % 3>{}, k * PER + j);
-            }
-        };
-        __builtin_amdgcn_sched_barrier(0);
-        read(0);
-        acc[ST][0] = v16f{};
-        acc[ST][1] = v16f{};
+            for (int i = 0; i < 16; ++i)
+                old[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(in_rsrc, at(i), col * 4, NT ? 2 : 0));
+        }
+        v8bf f[2];
+        f[0] = column8(b, 512);
+        v16f acc = {};
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
             __builtin_amdgcn_sched_barrier(0);
-            if (k + 1 < KS) read(k + 1);            // a whole round of products ahead
+            if (k + 1 < KS) f[(k + 1) & 1] = column8(b + (k + 1) * 2048, 512);   // a round of products ahead
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int w = 0; w < 3; ++w)
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-                    acc[ST][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[w][k], f[k & 1][n], acc[ST][n], 0, 0, 0);
-            if constexpr (!FIRST) {
-#pragma unroll
-                for (int j = 0; j < PER; ++j)
-                    store(in[k & 1][j] + acc[1 - ST][(k * PER + j) / 16][(k * PER + j) % 16], k * PER + j, s - 1);
-            }
+            for (int w = 0; w < 3; ++w) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[w][k], f[k & 1], acc, 0, 0, 0);
         }
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    // Before step s: its centroids and du_in of step s - 1 have landed, and the wave's
-    // reads of the other stage are done.  What was sent for after them may be out:
-    // du_in of step s (8 DMAs) and the 32 stores of step s - 2.
-    constexpr int IN = ADD ? 8 : 0;
-    auto wait = [&](auto out) {
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(out)::value) : "memory");
-    };
-    auto last = [&](auto at) {                      // the results of the last step, AT of six
-        constexpr int AT = decltype(at)::value;
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-        for (int j = 0; j < 32; ++j) store(add_in(IC<AT % 3>{}, j) + acc[AT % 2][j / 16][j % 16], j, steps - 1);
+        for (int i = 0; i < 16; ++i) {
+            const float o = ADD ? old[i] + acc[i] : acc[i];
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, o), out_rsrc, at(i), col * 4, NT ? 2 : 0);
+        }
+    };
+    auto step = [&](auto st, int s) {
+        constexpr int ST = decltype(st)::value;
+        if (s + 1 < s1) send(IC<1 - ST>{}, s + 1);
+        __builtin_amdgcn_sched_barrier(0);          // before the stores that the wait below leaves out
+        const char* const b = ST ? g_e1 : g_e0;
+        columns32(b + read_off, s * DU_STEP);
+        columns32(b + (read_off ^ 64), s * DU_STEP + 32);
+        // the next stage has landed (32 stores at least were sent for after it: as many may be out) and
+        // this one is read
+        asm volatile("s_waitcnt vmcnt(32) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     };
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    step(IC<0>{}, IC<1>{}, 0);
-    if (steps == 1) return last(IC<0>{});
-    wait(IC<IN>{});
-    step(IC<1>{}, IC<0>{}, 1);
-    for (int s = 2;; s += 6) {
-        if (s == steps) return last(IC<1>{});
-        wait(IC<IN + 32>{});
-        step(IC<2>{}, IC<0>{}, s);
-        if (s + 1 == steps) return last(IC<2>{});
-        wait(IC<IN + 32>{});
-        step(IC<3>{}, IC<0>{}, s + 1);
-        if (s + 2 == steps) return last(IC<3>{});
-        wait(IC<IN + 32>{});
-        step(IC<4>{}, IC<0>{}, s + 2);
-        if (s + 3 == steps) return last(IC<4>{});
-        wait(IC<IN + 32>{});
-        step(IC<5>{}, IC<0>{}, s + 3);
-        if (s + 4 == steps) return last(IC<5>{});
-        wait(IC<IN + 32>{});
-        step(IC<0>{}, IC<0>{}, s + 4);
-        if (s + 5 == steps) return last(IC<0>{});
-        wait(IC<IN + 32>{});
-        step(IC<1>{}, IC<0>{}, s + 5);
+    for (int s = s0; s < s1; s += 2) {
+        step(IC<0>{}, s);
+        if (s + 1 < s1) step(IC<1>{}, s + 1);
     }
 }
 
@@ -305,6 +213,17 @@ struct LogitsDeArgs {
     int d, E, chunks;                   // chunks of 32 tokens that a block takes
     float* part;                        // [blockIdx.y][E][d]
 };
+
+// The stages are separate LDS objects, so that the compiler sees that reads of one do
+// not wait for the DMA into another.
+__shared__ __attribute__((aligned(1024))) char g_stage0[64 * 1024];
+__shared__ __attribute__((aligned(1024))) char g_stage1[64 * 1024];
+
+template <int ST>
+__device__ __forceinline__ char* stage() {
+    if constexpr (ST == 0) return g_stage0;
+    else return g_stage1;
+}
 
 // de: a block takes all experts (EP = 64 WE) by 256 columns over some of the tokens, a
 // wave 64 experts by 32 WE columns; x's planes and u's rows come by DMA 32 tokens at
@@ -431,7 +350,7 @@ void split_and_du(const float* x, const uint16_t* e, int64_t T, int d, int E, co
     if (!out) return;
     const int64_t blocks = (token_chunks(T) + 3) / 4;
     const int steps = d / 64;
-    int64_t split = (256 + blocks - 1) / blocks;
+    int64_t split = (512 + blocks - 1) / blocks;
     split = split < steps ? split : steps;
     const int each = (int)((steps + split - 1) / split);
     const LogitsDuArgs a{planes, e, T, d, E, each, in, out};
