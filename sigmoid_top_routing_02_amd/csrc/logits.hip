@@ -24,6 +24,7 @@
 namespace moe {
 namespace {
 
+typedef int v4i __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -45,11 +46,21 @@ __device__ __forceinline__ int swizzle(int r) {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
 }
-// 16 bytes a lane, global -> LDS at lds + 16 lane (lds is wave-uniform); past the
-// descriptor's range zeros are written
-__device__ __forceinline__ void lds_dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, char* lds) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, voff, soff, 0, 0);
+__device__ __forceinline__ uint32_t uni(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
+// 16 bytes a lane, global -> LDS at lds + 16 lane (lds and soff are wave-uniform); past
+// the `bytes` at base zeros are written.  Stages are addressed at run time, so the DMA
+// is assembly: the compiler would make every read of LDS wait for all of them.  The
+// waits are the explicit ones.  (A write of m0 needs one wait state before its use.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void lds_dma16(const void* base, uint32_t bytes, uint32_t voff, uint32_t soff_, uint32_t lds_) {
+    const uint64_t at = reinterpret_cast<uint64_t>(base);
+    const v4i r = {(int)uni((uint32_t)at), (int)uni((uint32_t)(at >> 32) & 0xFFFFu), (int)uni(bytes), 0x00020000};
+    const uint32_t soff = uni(soff_), lds = uni(lds_);
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :: "v"(voff), "s"(r), "s"(soff), "s"(lds) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // A fragment of 8 values down a column: rows k, k + 1, .. k + 7 of which the lane's
 // 16 neighbours read 4 rows at p and 4 at p + rows4 (the bytes of 4 rows).
@@ -100,56 +111,60 @@ __global__ __launch_bounds__(256) void logits_split_kernel(const float* __restri
             make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
 }
 
-struct LogitsDuArgs {
+// Both products in one launch, blocks of four waves, two to a CU.
+struct LogitsArgs {
     const char* planes;
+    const uint16_t* u;
     const uint16_t* e;
     int64_t T;
-    int d, E, steps;                    // steps of 64 columns that a block takes
-    const float* in;
-    float* out;
+    int d, E;
+    int de_blocks;                      // the first blocks
+    int de_parts, de_chunks;            // parts of the tokens, and 32-token chunks in each
+    float* part;                        // [de_parts][E][d]
+    int du_split, du_steps;             // blocks along d, and steps of 64 columns in each
+    const float* du_in;
+    float* du;
 };
+
+constexpr int LDS_BYTES = 80 * 1024;    // of a block: half a CU's
 
 template <int V> struct IC { static constexpr int value = V; };
 
-constexpr int DU_STEP = 64;             // columns
-__shared__ __attribute__((aligned(1024))) char g_e0[256 * DU_STEP * 2];
-__shared__ __attribute__((aligned(1024))) char g_e1[256 * DU_STEP * 2];
-
 // du: a wave holds the fragments of its 32 tokens for all experts in registers and goes
 // through the columns, the block's four waves sharing 64 columns' centroids at a time
-// in LDS, sent for a step ahead; 32 columns are multiplied, added to du_in and stored at
-// a time.  Two blocks share a CU, so that one multiplies while the other waits for
-// du_in or for its stores to go out.
+// in LDS (two stages, sent for a step ahead); 32 columns are multiplied, added to du_in
+// and stored at a time.
 template <int EP, bool ADD, bool NT>
-__global__ __launch_bounds__(256, 2) void logits_du_kernel(LogitsDuArgs a) {
-    constexpr int KS = EP / 16;
+__device__ __forceinline__ void du_block(const LogitsArgs& a, int block, char* lds) {
+    constexpr int KS = EP / 16, STEP = 64, STAGE = EP * STEP * 2;
+    static_assert(2 * STAGE <= LDS_BYTES, "two stages");
     const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = (int)uni(tid >> 6);
     const int g = lane >> 4, i16 = lane & 15, half = lane >> 5;
     const int64_t chunks = (a.T + CHUNK - 1) / CHUNK;
-    const int64_t chunk = (int64_t)blockIdx.x * 4 + wave;
+    const int64_t chunk = (int64_t)(block / a.du_split) * 4 + wave;
     const int64_t t0 = chunk * CHUNK;
     const int rows = t0 < a.T ? (int)(a.T - t0 < CHUNK ? a.T - t0 : CHUNK) : 0;
-    const int s0 = blockIdx.y * a.steps, s1 = min(s0 + a.steps, a.d / DU_STEP);
+    const int s0 = block % a.du_split * a.du_steps, s1 = min(s0 + a.du_steps, a.d / STEP);
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(lds);
 
-    const auto e_rsrc = make_rsrc(a.e, (uint32_t)a.E * (uint32_t)a.d * 2u);
     const int dr = lane >> 3;                       // DMA: row of 8 and chunk of 8
     const uint32_t dma_off = (uint32_t)(wave * 8 + dr) * (uint32_t)a.d * 2u + (uint32_t)((lane & 7) ^ swizzle<128>(dr)) * 16u;
-    auto send = [&](auto st, int s) {               // EP / 32 DMAs
-        char* const to = decltype(st)::value ? g_e1 : g_e0;
+    auto send = [&](int st, int s) {                // EP / 32 DMAs
 #pragma unroll
         for (int j = 0; j < EP / 32; ++j)
-            lds_dma16(e_rsrc, dma_off, (uint32_t)(j * 32) * (uint32_t)a.d * 2u + (uint32_t)s * (DU_STEP * 2u),
-                      to + (j * 4 + wave) * 1024);
+            lds_dma16(a.e, (uint32_t)a.E * (uint32_t)a.d * 2u, dma_off,
+                      (uint32_t)(j * 32) * (uint32_t)a.d * 2u + (uint32_t)s * (STEP * 2u),
+                      lds0 + (uint32_t)(st * STAGE + (j * 4 + wave) * 1024));
     };
     // rows past the last token are out of the descriptors' range
     const uint32_t records = (uint32_t)rows * (uint32_t)a.d * 4u, row4 = (uint32_t)a.d * 4u;
-    const auto in_rsrc = make_rsrc(ADD ? a.in + t0 * a.d : a.out, ADD ? records : 0u);
-    const auto out_rsrc = make_rsrc(a.out + t0 * a.d, records);
+    const auto in_rsrc = make_rsrc(ADD ? a.du_in + t0 * a.d : a.du, ADD ? records : 0u);
+    const auto out_rsrc = make_rsrc(a.du + t0 * a.d, records);
     // result i of 16 of the lane's column lane % 32: row 8 (i / 4) + 4 half + i % 4
     const uint32_t out_off = (uint32_t)(4 * half) * row4 + (uint32_t)(lane & 31) * 4u;
     auto at = [&](int i) { return out_off + (uint32_t)(8 * (i / 4) + i % 4) * row4; };
-    send(IC<0>{}, s0);
+    send(0, s0);
     v8bf x[3][KS];
     {
         const int t = lane & 31;
@@ -188,132 +203,128 @@ __global__ __launch_bounds__(256, 2) void logits_du_kernel(LogitsDuArgs a) {
             __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, o), out_rsrc, at(i), col * 4, NT ? 2 : 0);
         }
     };
-    auto step = [&](auto st, int s) {
-        constexpr int ST = decltype(st)::value;
-        if (s + 1 < s1) send(IC<1 - ST>{}, s + 1);
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    for (int s = s0; s < s1; ++s) {
+        const int st = (s - s0) & 1;
+        if (s + 1 < s1) send(1 - st, s + 1);
         __builtin_amdgcn_sched_barrier(0);          // before the stores that the wait below leaves out
-        const char* const b = ST ? g_e1 : g_e0;
-        columns32(b + read_off, s * DU_STEP);
-        columns32(b + (read_off ^ 64), s * DU_STEP + 32);
+        columns32(lds + st * STAGE + read_off, s * STEP);
+        columns32(lds + st * STAGE + (read_off ^ 64), s * STEP + 32);
         // the next stage has landed (32 stores at least were sent for after it: as many may be out) and
         // this one is read
         asm volatile("s_waitcnt vmcnt(32) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    };
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    for (int s = s0; s < s1; s += 2) {
-        step(IC<0>{}, s);
-        if (s + 1 < s1) step(IC<1>{}, s + 1);
     }
 }
 
-struct LogitsDeArgs {
-    const char* planes;
-    const uint16_t* u;
-    int64_t T;
-    int d, E, chunks;                   // chunks of 32 tokens that a block takes
-    float* part;                        // [blockIdx.y][E][d]
-};
-
-// The stages are separate LDS objects, so that the compiler sees that reads of one do
-// not wait for the DMA into another.
-__shared__ __attribute__((aligned(1024))) char g_stage0[64 * 1024];
-__shared__ __attribute__((aligned(1024))) char g_stage1[64 * 1024];
-
-template <int ST>
-__device__ __forceinline__ char* stage() {
-    if constexpr (ST == 0) return g_stage0;
-    else return g_stage1;
-}
-
-// de: a block takes all experts (EP = 64 WE) by 256 columns over some of the tokens, a
-// wave 64 experts by 32 WE columns; x's planes and u's rows come by DMA 32 tokens at
-// a time into two stages.
-template <int WE>
-__global__ __launch_bounds__(512, 2) void logits_de_kernel(LogitsDeArgs a) {
-    constexpr int EP = 64 * WE, A_BYTES = 3 * CHUNK * EP * 2, NT = WE;
+// de: a block takes 128 experts (all of EP = 64) by 256 columns over some of the tokens,
+// a wave 64 experts by 128 (64) columns.  x's planes and u's rows come by DMA, 16 tokens
+// to a stage and three stages ahead; fragments are read a step ahead of their products.
+template <int EP>
+__device__ __forceinline__ void de_block(const LogitsArgs& a, int block, char* lds) {
+    constexpr int TE = EP < 128 ? EP : 128, WE = TE / 64, WN = 4 / WE, NT = 8 / WN;
+    constexpr int TOKENS = 16, SEGMENT = TOKENS * TE * 2, A_BYTES = 3 * SEGMENT, STAGE = A_BYTES + TOKENS * 512;
+    constexpr int SENT = STAGE / 1024;              // DMAs of a stage, over four waves
+    static_assert(4 * STAGE <= LDS_BYTES, "four stages");
     const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = (int)uni(tid >> 6);
     const int we = wave % WE, wn = wave / WE;
     const int g = lane >> 4, i16 = lane & 15;
-    const int n0 = blockIdx.x * 256;
+    // blocks 8 apart, on one XCD, take the same columns and tokens for the other experts
+    constexpr int TILES = EP / TE;
+    const int at = block / (8 * TILES) * 8 + block % 8, e0 = block / 8 % TILES * TE;
+    const int columns = (a.d + 255) / 256;
+    if (at >= columns * a.de_parts) return;
+    const int n0 = at % columns * 256, part = at / columns;
     const int64_t chunks = (a.T + CHUNK - 1) / CHUNK;
-    const int64_t c0 = (int64_t)blockIdx.y * a.chunks, c1 = c0 + a.chunks < chunks ? c0 + a.chunks : chunks;
+    const int64_t c0 = (int64_t)part * a.de_chunks, c1 = c0 + a.de_chunks < chunks ? c0 + a.de_chunks : chunks;
+    const int steps = (int)(c1 - c0) * (CHUNK / TOKENS);
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(lds);
 
-    auto send = [&](auto st, int64_t c) {
-        char* const to = stage<decltype(st)::value>();
-        const auto x_rsrc = make_rsrc(a.planes + c * A_BYTES, A_BYTES);
+    // a plane's row of EP experts is swizzled over all of it; its e0 to e0 + TE are whole
+    // 256-byte quarters of that, or all
+    auto send = [&](int s) {
+        const uint32_t to = lds0 + (uint32_t)(s & 3) * STAGE;
+        const int64_t t0 = c0 * CHUNK + (int64_t)s * TOKENS;
+        const int rows = (int)(a.T - t0 < 0 ? 0 : a.T - t0 < TOKENS ? a.T - t0 : TOKENS);
+        const char* planes = a.planes + (c0 + s / 2) * (3 * CHUNK * EP * 2) + (s & 1) * (TOKENS * EP * 2) + e0 * 2;
+        const uint16_t* u = a.u + t0 * a.d;
 #pragma unroll
-        for (int j = 0; j < (A_BYTES / 1024 + 7) / 8; ++j) {
-            const int k = j * 8 + wave;
-            if (k < A_BYTES / 1024) lds_dma16(x_rsrc, (uint32_t)lane * 16u, (uint32_t)k * 1024u, to + k * 1024);
-        }
-        const int64_t t0 = c * CHUNK;
-        const int rows = (int)(a.T - t0 < CHUNK ? a.T - t0 : CHUNK);
-        const auto u_rsrc = make_rsrc(a.u + t0 * a.d, (uint32_t)rows * (uint32_t)a.d * 2u);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {                // two rows of 512 bytes a time; rows past T are out of range
-            const int k = j * 8 + wave, r = 2 * k + (lane >> 5);
-            const int at = ((lane & 31) ^ swizzle<512>(r)) * 16 + n0 * 2;
-            // columns past d: the row's own last ones, whose results are not stored
-            lds_dma16(u_rsrc, (uint32_t)r * (uint32_t)a.d * 2u + (uint32_t)min(at, a.d * 2 - 16), 0u, to + A_BYTES + k * 1024);
+        for (int j = 0; j < (SENT + 3) / 4; ++j) {
+            const int k = j * 4 + wave;
+            if (k < A_BYTES / 1024) {
+                constexpr int ROWS = 1024 / (TE * 2), PER = SEGMENT / 1024, CHUNKS = TE / 8;   // rows a DMA, DMAs a plane
+                const uint32_t r = (uint32_t)((k % PER) * ROWS + lane / CHUNKS);
+                lds_dma16(planes, 3 * CHUNK * EP * 2, r * (EP * 2) + (uint32_t)(lane % CHUNKS) * 16u,
+                          (uint32_t)(k / PER) * (CHUNK * EP * 2), to + (uint32_t)k * 1024u);
+            } else if (k < SENT) {                   // two rows of 512 bytes; rows past T are out of range
+                const int r = 2 * (k - A_BYTES / 1024) + (lane >> 5);
+                // columns past d: the row's own last ones, whose results are not stored
+                const int c = min(((lane & 31) ^ swizzle<512>(r)) * 16 + n0 * 2, a.d * 2 - 16);
+                lds_dma16(u, (uint32_t)rows * (uint32_t)a.d * 2u, (uint32_t)r * (uint32_t)a.d * 2u + (uint32_t)c, 0u,
+                          to + (uint32_t)k * 1024u);
+            }
         }
     };
     v16f acc[2][NT] = {};
     const int row = 8 * (g >> 1) + (i16 >> 2), in16 = 2 * (g & 1) + ((i16 & 3) >> 1);
-    const int a_off = row * EP * 2 + ((we * 8 + in16) ^ swizzle<EP * 2>(i16 >> 2)) * 16 + (i16 & 1) * 8;
+    const int a_off = row * TE * 2 + ((we * 8 + in16) ^ swizzle<EP * 2>(i16 >> 2)) * 16 + (i16 & 1) * 8;
     const int b_off = A_BYTES + row * 512 + ((wn * NT * 4 + in16) ^ swizzle<512>(i16 >> 2)) * 16 + (i16 & 1) * 8;
     struct Fragments { v8bf x[3][2], b[NT]; };
-    auto read = [&](auto st, int k, Fragments& f) {  // 16 tokens of the chunk's 32
-        const char* const s = stage<decltype(st)::value>();
+    auto read = [&](int s, Fragments& f) {
+        const char* const from = lds + (s & 3) * STAGE;
 #pragma unroll
         for (int w = 0; w < 3; ++w)
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
-                f.x[w][m] = column8(s + (a_off ^ (m * 64)) + (w * CHUNK + k * 16) * EP * 2, 4 * EP * 2);
+            for (int m = 0; m < 2; ++m) f.x[w][m] = column8(from + (a_off ^ (m * 64)) + w * SEGMENT, 4 * TE * 2);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) f.b[n] = column8(s + (b_off ^ (n * 64)) + k * 16 * 512, 4 * 512);
+        for (int n = 0; n < NT; ++n) f.b[n] = column8(from + (b_off ^ (n * 64)), 4 * 512);
     };
-    auto multiply = [&](const Fragments& f) {
+    Fragments f[2];
+    // Stage s + 1 has landed where at most the two after it are out, SENT / 4 DMAs of a wave
+    // each at least; behind the barrier stage s, whose reads are done, takes s + 4.
+    auto step = [&](int s, const Fragments& now, Fragments& next) {
+        if (s + 3 < steps) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * (SENT / 4)) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (s + 4 < steps) send(s + 4);
+        if (s + 1 < steps) read(s + 1, next);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int w = 0; w < 3; ++w)
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.x[w][m], f.b[n], acc[m][n], 0, 0, 0);
+                    acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now.x[w][m], now.b[n], acc[m][n], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
     };
-    // Reads run half a chunk ahead of the products: the second half's while the first
-    // half is multiplied, the next chunk's first half's, behind the wait for its DMA,
-    // while the second half is.
-    Fragments f0, f1;
-    auto step = [&](auto st, int64_t c) {
-        constexpr int ST = decltype(st)::value;
-        read(st, 1, f1);
-        multiply(f0);
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (c + 2 < c1) send(st, c + 2);
-        if (c + 1 < c1) read(IC<1 - ST>{}, 0, f0);
-        multiply(f1);
-    };
-    send(IC<0>{}, c0);
+    for (int s = 0; s < 4 && s < steps; ++s) send(s);
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    if (c0 + 1 < c1) send(IC<1>{}, c0 + 1);
-    read(IC<0>{}, 0, f0);
-    for (int64_t c = c0; c < c1; c += 2) {
-        step(IC<0>{}, c);
-        if (c + 1 < c1) step(IC<1>{}, c + 1);
+    read(0, f[0]);
+    for (int s = 0; s < steps; s += 2) {            // steps is even
+        step(s, f[0], f[1]);
+        step(s + 1, f[1], f[0]);
     }
-    float* const part = a.part + (int64_t)blockIdx.y * a.E * a.d;
+    float* const out = a.part + (int64_t)part * a.E * a.d;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int e = we * 64 + m * 32 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4;
+                const int e = e0 + we * 64 + m * 32 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4;
                 const int col = n0 + (wn * NT + n) * 32 + (lane & 31);
-                if (e < a.E && col < a.d) part[(int64_t)e * a.d + col] = acc[m][n][i];
+                if (e < a.E && col < a.d) out[(int64_t)e * a.d + col] = acc[m][n][i];
             }
+}
+
+// de's blocks go first, one to a CU, and du's beside them: while du waits for memory, de
+// multiplies.
+template <int EP, bool ADD, bool NT>
+__global__ __launch_bounds__(256, 2) void logits_kernel(LogitsArgs a) {
+    __shared__ __attribute__((aligned(1024))) char lds[LDS_BYTES];
+    const int block = blockIdx.x;
+    if (block < a.de_blocks) de_block<EP>(a, block, lds);
+    else du_block<EP, ADD, NT>(a, block - a.de_blocks, lds);
 }
 
 // de = de_in + the parts in order; n = E d values, a multiple of 4
@@ -333,68 +344,69 @@ int64_t token_chunks(int64_t T) { return (T + CHUNK - 1) / CHUNK; }
 
 size_t plane_bytes(int64_t T, int E) { return (size_t)token_chunks(T) * 3 * CHUNK * padded_experts(E) * 2; }
 
-// Chunks that a block of logits_de_kernel takes.
-int de_chunks(int64_t T, int d) {
-    const int64_t blocks = (d + 255) / 256, chunks = token_chunks(T), parts = 256 / blocks < 1 ? 1 : 256 / blocks;
+// 32-token chunks that a block of de takes: about one block to a CU, and four chunks at
+// least.
+int de_chunks(int64_t T, int d, int E) {
+    const int64_t blocks = (int64_t)((d + 255) / 256) * (padded_experts(E) > 128 ? 2 : 1);
+    const int64_t chunks = token_chunks(T), parts = 256 / blocks < 1 ? 1 : 256 / blocks;
     const int64_t each = (chunks + parts - 1) / parts;
     return (int)(each < 4 ? 4 : each);
 }
 
-int de_parts(int64_t T, int d) { return (int)((token_chunks(T) + de_chunks(T, d) - 1) / de_chunks(T, d)); }
+int de_parts(int64_t T, int d, int E) {
+    const int each = de_chunks(T, d, E);
+    return (int)((token_chunks(T) + each - 1) / each);
+}
 
 template <int EP>
-void split_and_du(const float* x, const uint16_t* e, int64_t T, int d, int E, const float* in, float* out, char* planes,
-                  hipStream_t st) {
-    hipLaunchKernelGGL((logits_split_kernel<EP>), dim3((unsigned)(token_chunks(T) * CHUNK * (EP / 8) / 256)), dim3(256), 0,
-                       st, x, T, E, planes);
-    if (!out) return;
-    const int64_t blocks = (token_chunks(T) + 3) / 4;
-    const int steps = d / 64;
-    int64_t split = (512 + blocks - 1) / blocks;
-    split = split < steps ? split : steps;
-    const int each = (int)((steps + split - 1) / split);
-    const LogitsDuArgs a{planes, e, T, d, E, each, in, out};
-    const dim3 grid((unsigned)blocks, (unsigned)((steps + each - 1) / each));
-    const bool nt = streamed(T * d * 4);
-    if (in) {
-        if (nt) hipLaunchKernelGGL((logits_du_kernel<EP, true, true>), grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((logits_du_kernel<EP, true, false>), grid, dim3(256), 0, st, a);
-    } else {
-        if (nt) hipLaunchKernelGGL((logits_du_kernel<EP, false, true>), grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((logits_du_kernel<EP, false, false>), grid, dim3(256), 0, st, a);
+void launch_all(const float* x, LogitsArgs& a, bool de, hipStream_t st) {
+    hipLaunchKernelGGL((logits_split_kernel<EP>), dim3((unsigned)(token_chunks(a.T) * CHUNK * (EP / 8) / 256)), dim3(256), 0,
+                       st, x, a.T, a.E, const_cast<char*>(a.planes));
+    const int64_t tiles = (int64_t)((a.d + 255) / 256) * a.de_parts;
+    a.de_blocks = de ? (int)((tiles + 7) / 8 * 8 * (EP > 128 ? 2 : 1)) : 0;
+    int64_t du_blocks = 0;
+    if (a.du) {
+        const int64_t along = (token_chunks(a.T) + 3) / 4;
+        const int steps = a.d / 64;
+        int64_t split = (512 + along - 1) / along;
+        split = split < steps ? split : steps;
+        a.du_steps = (int)((steps + split - 1) / split);
+        a.du_split = (steps + a.du_steps - 1) / a.du_steps;
+        du_blocks = along * a.du_split;
     }
+    const dim3 grid((unsigned)(a.de_blocks + du_blocks));
+    const bool nt = streamed(a.T * a.d * 4);
+    const auto kernel = a.du_in ? nt ? logits_kernel<EP, true, true> : logits_kernel<EP, true, false>
+                                : nt ? logits_kernel<EP, false, true> : logits_kernel<EP, false, false>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, a);
 }
 
 }  // namespace
 
 size_t router_logits_backward_ws_bytes(int64_t T, int d, int E) {
-    return T == 0 ? 16 : plane_bytes(T, E) + (size_t)de_parts(T, d) * E * d * sizeof(float);
+    return T == 0 ? 16 : plane_bytes(T, E) + (size_t)de_parts(T, d, E) * E * d * sizeof(float);
 }
 
 hipError_t launch_router_logits_backward(const float* dlogits, const uint16_t* u, const uint16_t* e, int64_t T, int d,
                                          int E, const float* du_in, const float* de_in, float* du, float* de, void* ws,
                                          hipStream_t st) {
-    char* planes = static_cast<char*>(ws);
-    float* part = reinterpret_cast<float*>(planes + plane_bytes(T, E));
-    int parts = 0;
+    LogitsArgs a{};
     if (T > 0) {
+        a.planes = static_cast<const char*>(ws);
+        a.u = u; a.e = e; a.T = T; a.d = d; a.E = E;
+        a.de_parts = de_parts(T, d, E);
+        a.de_chunks = de_chunks(T, d, E);
+        a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + plane_bytes(T, E));
+        a.du_in = du_in; a.du = du;
         const int ep = padded_experts(E);
-        if (ep == 64) split_and_du<64>(dlogits, e, T, d, E, du_in, du, planes, st);
-        else if (ep == 128) split_and_du<128>(dlogits, e, T, d, E, du_in, du, planes, st);
-        else split_and_du<256>(dlogits, e, T, d, E, du_in, du, planes, st);
-        if (de) {
-            parts = de_parts(T, d);
-            const LogitsDeArgs a{planes, u, T, d, E, de_chunks(T, d), part};
-            const dim3 grid((d + 255) / 256, parts);
-            if (ep == 64) hipLaunchKernelGGL((logits_de_kernel<1>), grid, dim3(512), 0, st, a);
-            else if (ep == 128) hipLaunchKernelGGL((logits_de_kernel<2>), grid, dim3(512), 0, st, a);
-            else hipLaunchKernelGGL((logits_de_kernel<4>), grid, dim3(512), 0, st, a);
-        }
+        if (ep == 64) launch_all<64>(dlogits, a, de != nullptr, st);
+        else if (ep == 128) launch_all<128>(dlogits, a, de != nullptr, st);
+        else launch_all<256>(dlogits, a, de != nullptr, st);
     }
     if (de) {
         const int64_t n = (int64_t)E * d;
-        hipLaunchKernelGGL(logits_sum_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, part, parts, n, de_in,
-                           de);
+        hipLaunchKernelGGL(logits_sum_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, a.part, a.de_parts, n,
+                           de_in, de);
     }
     return hipGetLastError();
 }
