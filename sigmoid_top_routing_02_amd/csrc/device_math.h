@@ -82,6 +82,29 @@ __device__ __forceinline__ uint32_t e4m3_encode4(float a, float b, float c, floa
     return e4m3_nan_fix(w, d, 3);
 }
 
+// The same codes of 4 N values that a tile's scale has been applied to: no larger by
+// magnitude than 448 (1 + 2^-22), or NaN.  These need no clamp (the conversion rounds
+// them to 448), and a sum, which a NaN passes into, tells for all of them at once
+// whether any NaN needs its sign.
+template <int N>
+__device__ __forceinline__ void e4m3_encode_scaled(const float (&v)[4 * N], uint32_t (&w)[N]) {
+    float any = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        any += (v[4 * i] + v[4 * i + 1]) + (v[4 * i + 2] + v[4 * i + 3]);
+        w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
+        w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], (int)w[i], true);
+    }
+    if (any != any) {
+#pragma unroll
+        for (int i = 0; i < 4 * N; ++i) w[i / 4] = e4m3_nan_fix(w[i / 4], v[i], i % 4);
+    }
+}
+// The larger of m >= 0 and |x|, m if x is NaN, in one instruction.
+__device__ __forceinline__ float max_abs(float m, float x) {
+    return __builtin_amdgcn_fmed3f(m, __builtin_fabsf(x), __builtin_inff());
+}
+
 // The values of four E4M3 codes (exact; NaN codes give NaN).
 __device__ __forceinline__ float4 e4m3_decode4(uint32_t w) {
     typedef float v2f __attribute__((ext_vector_type(2)));

@@ -37,4 +37,12 @@ __device__ __forceinline__ float max16(float m) {     // a NaN counts as less th
     return o > m ? o : m;
 }
 
+// the largest of lanes l, l ^ 16, l ^ 32 and l ^ 48 (of no NaN)
+__device__ __forceinline__ float max_of_rows(float m) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+    m = __uint_as_float(a[0]) > __uint_as_float(a[1]) ? __uint_as_float(a[0]) : __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+    return __uint_as_float(b[0]) > __uint_as_float(b[1]) ? __uint_as_float(b[0]) : __uint_as_float(b[1]);
+}
+
 }  // namespace moe

@@ -61,7 +61,10 @@ __device__ __forceinline__ float row_weight(const WgradSrc& s, int64_t r, int64_
     return hit >= 0 ? s.gate[t * s.K + hit] : 0.0f;
 }
 
-// z's 4 values at column `at` of row r, from FP32 or (ZQ) from 8 bits
+// z's 4 values at column `at` of row r, from FP32 or (ZQ) from 8 bits: of the 147456
+// rows of a 16384-token layer with I = 2048 the operand h^T takes 394 us from 8 bits and
+// 517 from FP32, dz^T 893 and 1104 (of dz^T's sources dh, read by the blocks of both
+// halves, is the larger part by then).
 template <bool ZQ> struct Z4 {
     float4 v;
     __device__ __forceinline__ void load(const WgradSrc& s, int64_t r, int at) {
