@@ -47,8 +47,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, ui
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
 }
 __device__ __forceinline__ uint32_t uni(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
-// 16 bytes a lane, global -> LDS at lds + 16 lane (lds and soff are wave-uniform); past
-// the `bytes` at base zeros are written.  Stages are addressed at run time, so the DMA
+// 16 bytes a lane, global -> LDS at lds + 16 lane (lds and soff are wave-uniform).  Where
+// voff is past the `bytes` at base, zeros are written: rows, which may be, go into voff,
+// and soff takes what stays inside a row, so that it does not matter whether the range
+// check counts it.  Stages are addressed at run time, so the DMA
 // is assembly: the compiler would make every read of LDS wait for all of them.  The
 // waits are the explicit ones.  (A write of m0 needs one wait state before its use.)
 #pragma clang diagnostic push
@@ -153,12 +155,13 @@ __device__ __forceinline__ void du_block(const LogitsArgs& a, int block, char* l
     auto send = [&](int st, int s) {                // EP / 32 DMAs
 #pragma unroll
         for (int j = 0; j < EP / 32; ++j)
-            lds_dma16(a.e, (uint32_t)a.E * (uint32_t)a.d * 2u, dma_off,
-                      (uint32_t)(j * 32) * (uint32_t)a.d * 2u + (uint32_t)s * (STEP * 2u),
-                      lds0 + (uint32_t)(st * STAGE + (j * 4 + wave) * 1024));
+            lds_dma16(a.e, (uint32_t)a.E * (uint32_t)a.d * 2u, dma_off + (uint32_t)(j * 32) * (uint32_t)a.d * 2u,
+                      (uint32_t)s * (STEP * 2u), lds0 + (uint32_t)(st * STAGE + (j * 4 + wave) * 1024));
     };
-    // rows past the last token are out of the descriptors' range
+    // rows past the last token are out of the descriptors' range (of a wave that has none
+    // too, whose offset along the row is kept at zero)
     const uint32_t records = (uint32_t)rows * (uint32_t)a.d * 4u, row4 = (uint32_t)a.d * 4u;
+    const uint32_t along = rows > 0 ? 4u : 0u;
     const auto in_rsrc = make_rsrc(ADD ? a.du_in + t0 * a.d : a.du, ADD ? records : 0u);
     const auto out_rsrc = make_rsrc(a.du + t0 * a.d, records);
     // result i of 16 of the lane's column lane % 32: row 8 (i / 4) + 4 half + i % 4
@@ -184,7 +187,7 @@ __device__ __forceinline__ void du_block(const LogitsArgs& a, int block, char* l
         if constexpr (ADD) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                old[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(in_rsrc, at(i), col * 4, NT ? 2 : 0));
+                old[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(in_rsrc, at(i), col * along, NT ? 2 : 0));
         }
         v8bf f[2];
         f[0] = column8(b, 512);
@@ -200,7 +203,7 @@ __device__ __forceinline__ void du_block(const LogitsArgs& a, int block, char* l
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float o = ADD ? old[i] + acc[i] : acc[i];
-            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, o), out_rsrc, at(i), col * 4, NT ? 2 : 0);
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, o), out_rsrc, at(i), col * along, NT ? 2 : 0);
         }
     };
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");

@@ -380,6 +380,33 @@ def test_logits_no_tokens_one_output_and_in_place():
     assert got[0] is a and got[1] is b and torch.equal(a, want[0]) and torch.equal(b, want[1])
 
 
+@pytest.mark.parametrize("T,d,E", [(1, 128, 1), (45, 256, 33), (97, 384, 70), (130, 128, 129), (161, 256, 200)])
+def test_logits_operands_inside_a_buffer(T, d, E):
+    """Nothing around the operands is read (there are NaN) and nothing around the outputs written."""
+    dev()
+    pad = 1 << 16                                    # values, on each side
+
+    def inside(x):
+        big = torch.full((x.numel() + 2 * pad,), float("nan"), dtype=x.dtype, device="cuda")
+        view = big[pad:pad + x.numel()].view(x.shape)
+        view.copy_(x)
+        return big, view
+
+    dl, u, e = _operands(T, d, E, seed=T)
+    add = _rand(_gen(1), T, d), _rand(_gen(2), E, d)
+    want = moe.moe_router_logits_backward(dl, u, e, du_in=add[0], de_in=add[1])
+    (_, dl), (_, u), (_, e), (_, du_in), (_, de_in) = (inside(x) for x in (dl, u, e, *add))
+    outs = [inside(torch.zeros_like(x)) for x in want]
+    ws_bytes = moe.load_library().moe_router_logits_backward_workspace_bytes(T, d, E)
+    room, ws = inside(torch.zeros(ws_bytes // 4 + 1, device="cuda"))
+    moe.moe_router_logits_backward(dl, u, e, du_in=du_in, de_in=de_in, du=outs[0][1], de=outs[1][1],
+                                   ws=ws.view(torch.uint8).view(-1))
+    torch.cuda.synchronize()
+    for (big, view), x in zip([*outs, (room, ws)], [*want, None]):
+        assert x is None or torch.equal(view, x)
+        assert torch.isnan(big[:pad]).all() and torch.isnan(big[pad + view.numel():]).all()
+
+
 def test_logits_against_differences():
     """L = <g, u . e^T> is linear in u and in e: its differences are its gradient."""
     dev()
