@@ -203,6 +203,8 @@ __global__ __launch_bounds__(MAXT, NV == 2 ? 4 : 1) void add_layernorm_kernel(Ad
     }
 }
 
+// Bound by HBM: 8192 rows of 7168 bf16 values with dh 91 to 96 us (4.9 to 5.2 TB/s), and
+// 7 for the partial rows.
 // AHEAD: a row's dy and h are sent for before the last one's reduction and kept packed.
 // IN_LDS: the sums over the rows are kept there, where a row of more than 8192 values
 // leaves a thread no registers for them (4096 rows of 16384 bf16 values
