@@ -119,6 +119,32 @@ def test_long(T, E, K):
     assert all(torch.equal(a, b) for a, b in zip(r, again))
 
 
+def test_past_32_bit_offsets():
+    """The last tokens of 8 GiB of scores: their counts and gradients as of those tokens alone, bit for bit."""
+    dev()
+    T, E, K, last = 2 ** 23 + 77, 256, 2, 100
+    block, picks = _inputs(4096, E, K, seed=5)
+    scores = block.repeat(-(-T // 4096), 1)[:T]
+    idx = picks.repeat(-(-T // 4096), 1)[:T].contiguous()
+    say("  inputs made")
+    scores[T - last:], idx[T - last:] = _inputs(last, E, K, seed=6)
+    r = moe.moe_balance_loss(scores, idx, ALPHA, seq_start=_starts([0, T - last, T]))
+    grad = moe.moe_balance_loss_backward(scores, r.seq_count, K, ALPHA, seq_start=_starts([0, T - last, T]))
+    tail, tail_idx = scores[T - last:].clone(), idx[T - last:].clone()
+    one = moe.moe_balance_loss(tail, tail_idx, ALPHA)
+    want = moe.moe_balance_loss_backward(tail, one.seq_count, K, ALPHA)
+    torch.cuda.synchronize()
+    assert torch.equal(r.seq_count[1], one.seq_count[0]) and torch.equal(grad[T - last:], want)
+    # other chunks, so another order of the sums: 117 roundings as _check counts them, on both sides
+    assert ((r.loss[1] - one.loss[0]).abs() <= 2 * 117 * U * one.loss[0]).all()
+    assert int(r.seq_count[0].sum()) == K * (T - last) and int(r.expert_count.sum()) == K * T
+    f = r.seq_count[0].to(F8) * E / (K * (T - last))
+    s = scores[T - last - 50:T - last].to(F8)
+    p = s / s.sum(1, keepdim=True)
+    coef, fp = ALPHA / (T - last) * p * (1.0 - s), (p @ f)[:, None]
+    assert ((grad[T - last - 50:T - last].to(F8) - coef * (f - fp)).abs() <= 48 * U * coef * (f + fp)).all()
+
+
 def test_whole_batch_and_equal_lengths():
     """No starts: one sequence of all tokens.  Equal lengths: moe_seq_balance_loss but for the order of the sums."""
     dev()
@@ -304,6 +330,25 @@ def test_logits_large(T, d, E):
     a = _check_logits(dl, u, e)
     b = moe.moe_router_logits_backward(dl, u, e)
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_logits_past_32_bit_offsets():
+    dev()
+    T, d, E = 160001, 7168, 20
+    dl, u, e = _operands(T, d, E, seed=9)
+    du_in = _rand(_gen(1), T, d)
+    say("  inputs made")
+    du, de = moe.moe_router_logits_backward(dl, u, e, du_in=du_in)
+    torch.cuda.synchronize()
+    x = dl.to(F8)
+    for rows in (slice(0, 40), slice(149790, 149840), slice(T - 70, T)):      # 149797 rows of du are 2^32 bytes
+        ref, size = x[rows] @ e.to(F8) + du_in[rows].to(F8), x[rows].abs() @ e.to(F8).abs() + du_in[rows].to(F8).abs()
+        assert ((du[rows].to(F8) - ref).abs() <= (3 * E + 2) * U * size).all()
+    cols = slice(d - 130, d)
+    xt, uu = x.t().contiguous(), u[:, cols].to(F8)
+    assert ((de[:, cols].to(F8) - xt @ uu).abs() <= (3 * T + 2) * U * (xt.abs() @ uu.abs())).all()
+    # roundings of random sign
+    assert float((de[:, cols].to(F8) - xt @ uu).norm()) <= 1.5 * (3 * T) ** 0.5 * U * float((xt.abs() @ uu.abs()).norm())
 
 
 @pytest.mark.parametrize("T,d,E", [(300, 384, 61), (513, 256, 256), (64, 128, 16)])

@@ -112,3 +112,26 @@ def test_runs_at_other_sizes():
     r, g = block.step()
     torch.cuda.synchronize()
     assert all(torch.isfinite(t).all() for t in (r["out"], *g.values()))
+
+
+def test_two_steps_at_once():
+    """Forward and backward on two streams at the same time, each with its own scratch: one after the other's bits."""
+    dev()
+    blocks = [ts.Block(1500, 512, 16, 4, 256, seed=s) for s in (1, 2)]
+
+    def run(block):
+        r = block.forward()
+        g = block.backward(r)
+        return [r["out"], r["zq"], r["zs"], *r["balance"], *(g[k] for k in sorted(g))]
+
+    want = [run(b) for b in blocks]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(4):
+        got = [None, None]
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                got[k] = run(blocks[k])
+        torch.cuda.synchronize()
+        for k in (0, 1):
+            assert all(torch.equal(a, b) for a, b in zip(got[k], want[k])), (i, k)

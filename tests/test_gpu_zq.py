@@ -79,6 +79,23 @@ def test_product_many_tiles_and_repeats():
     assert torch.equal(a[0], z[0]) and torch.equal(a[1], z[1]) and torch.equal(a[2], q) and torch.equal(a[3], s)
 
 
+@pytest.mark.parametrize("M", [40, 300])
+def test_product_special_values(M):
+    """NaN, infinities, zeros and the largest and smallest values in z: the codes that the quantiser gives them."""
+    dev()
+    aq, a_s, off, bq, bs, _ = _operands([M], 512, 384)
+    a_s[3, 1], a_s[4, 0], a_s[5], a_s[6], a_s[7] = float("nan"), float("inf"), 3e38, 1e-38, 0.0
+    bs[0, 3, 2] = -float("inf")                       # gate and up columns 384 to 511, of every row
+    aq[8, 130], aq[9, 5], aq[10] = 0x7F, 0xFF, 0x80
+    hq, hs, zq, zs = moe.grouped_gemm_fp8_swiglu_zq(aq, a_s, off, M, bq, bs)
+    fq, fs, z = moe.grouped_gemm_fp8_blockscaled(aq, a_s, off, M, bq, bs, epi=moe.MOE_EPI_SWIGLU_QUANT_Z)
+    q, s = moe.fp8_quant_1x128(z)
+    torch.cuda.synchronize()
+    assert torch.isnan(z[3]).all() and torch.isinf(z[4, :384]).any() and torch.isnan(z[8, :384]).all() and torch.isfinite(z[11, :384]).all()
+    assert torch.equal(zs.view(torch.int32), s.view(torch.int32)) and torch.equal(zq, q)
+    assert torch.equal(hs.view(torch.int32), fs.view(torch.int32)) and torch.equal(hq, fq)
+
+
 def test_product_leaves_other_rows():
     """Rows behind the last group's are not written; no rows at all is a call that does nothing."""
     dev()
