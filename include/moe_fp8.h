@@ -189,7 +189,7 @@ int moe_balance_loss_backward(const float* scores, const int32_t* seq_count, con
  * depends on T, d and E alone; what is under the smallest normal FP32 number counts as
  * zero, and infinite values of u or the centroids may give NaN.  ws: scratch of
  * moe_router_logits_backward_workspace_bytes(T, d, E) bytes (no setup needed; may be
- * NULL when T = 0): 6 bytes for each logit, and partial sums of de.
+ * NULL when T = 0): at most 6 bytes for each logit, and partial sums of de.
  * Limits: 0 <= T <= 2^24, d % 128 == 0, d <= 65536, 1 <= E <= 256.
  */
 size_t moe_router_logits_backward_workspace_bytes(int64_t T, int d, int E);   /* 0 outside the limits */

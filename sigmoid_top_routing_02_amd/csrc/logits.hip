@@ -72,6 +72,26 @@ __device__ __forceinline__ v8bf column8(const char* p, int rows4) {
     return __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// The three parts of 8 values, [lo, mid, hi].
+__device__ __forceinline__ void split8(const float (&v)[8], v8bf (&w)[3]) {
+    v4i b[3];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // an infinity is its own first part; a NaN stays NaN through the second
+        const float hi = __uint_as_float(__float_as_uint(v[i]) & 0xFFFF0000u);
+        const float r = __builtin_fabsf(v[i]) == __builtin_inff() ? 0.0f : v[i] - hi;
+        const float mid = __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
+        const float part[3] = {r - mid, mid, hi};
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            const uint32_t x = __float_as_uint(part[p]) >> 16;
+            b[p][i / 2] = i % 2 ? b[p][i / 2] | (int)(x << 16) : (int)x;
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) w[p] = __builtin_bit_cast(v8bf, b[p]);
+}
+
 // The three planes of x (16384 x 256: 9 us, of HBM 42 MB), [chunk][plane][32 tokens][EP] bf16, each token's 16-byte
 // chunks permuted by swizzle<2 EP>; zeros past T and E.
 template <int EP>
@@ -90,27 +110,13 @@ __global__ __launch_bounds__(256) void logits_split_kernel(const float* __restri
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = t < T && c * 8 + i < E ? x[t * E + c * 8 + i] : 0.0f;
     }
-    uint32_t w[3][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        // an infinity is its own first part; a NaN stays NaN through the second
-        const float hi = __uint_as_float(__float_as_uint(v[i]) & 0xFFFF0000u);
-        const float r = __builtin_fabsf(v[i]) == __builtin_inff() ? 0.0f : v[i] - hi;
-        const float mid = __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
-        const float lo = r - mid;
-        const float part[3] = {lo, mid, hi};
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-            const uint32_t b = __float_as_uint(part[p]) >> 16;
-            w[p][i / 2] = i % 2 ? w[p][i / 2] | b << 16 : b;
-        }
-    }
+    v8bf w[3];
+    split8(v, w);
     const int64_t chunk = t / CHUNK;
     const int row = (int)(t % CHUNK);
 #pragma unroll
     for (int p = 0; p < 3; ++p)
-        *reinterpret_cast<uint4*>(planes + ((chunk * 3 + p) * CHUNK + row) * (EP * 2) + (c ^ swizzle<EP * 2>(row)) * 16) =
-            make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+        *reinterpret_cast<v8bf*>(planes + ((chunk * 3 + p) * CHUNK + row) * (EP * 2) + (c ^ swizzle<EP * 2>(row)) * 16) = w[p];
 }
 
 // Both products in one launch, blocks of four waves, two to a CU.
@@ -335,6 +341,122 @@ __global__ __launch_bounds__(256, 2) void logits_kernel(LogitsArgs a) {
     else du_block<EP, ADD, NT>(a, block - a.de_blocks, lds);
 }
 
+// Small calls: both products in one launch, without planes, parts or scratch.  A wave of
+// du takes 32 tokens by 64 columns over all experts; a block of de 32 experts by 64
+// columns, its eight waves every eighth 16 tokens, added up through LDS in order.  The
+// fragments come straight from global memory, and x is split where it is used.  Bound by
+// latency and by the launch: 64 x 512 x 8 5 us (three launches 10), 1031 x 640 x 61 12 (16),
+// 512 x 7168 x 64 13 (18), 1024 x 4096 x 256 26 (33).  Loads two steps ahead instead of one:
+// 12, 16 and more of the larger.
+constexpr int SMALL_WAVES = 8;
+struct SmallArgs {
+    const float* x;
+    const uint16_t* u;
+    const uint16_t* e;
+    int T, d, E;
+    int du_blocks;                      // the first blocks
+    const float* du_in;
+    const float* de_in;
+    float* du;
+    float* de;
+};
+
+typedef float v2f __attribute__((ext_vector_type(2)));
+
+// The products of 32 rows from row0 (DE: experts, else tokens) and the lane's columns col
+// and col + 1, over every `step`th 16 tokens (experts) from `first`.  Rows past the end
+// are out of the descriptors' ranges, which give zeros.
+template <bool DE, bool VEC>
+__device__ __forceinline__ void small_products(const SmallArgs& a, int row0, int col, int first, int step, v16f (&acc)[2]) {
+    const int lane = threadIdx.x & 63, half = lane >> 5, own = row0 + (lane & 31);
+    const int over = DE ? a.T : a.E;
+    const auto x_rsrc = make_rsrc(a.x, (uint32_t)a.T * (uint32_t)a.E * 4u);
+    const auto b_rsrc = make_rsrc(DE ? a.u : a.e, (uint32_t)over * (uint32_t)a.d * 2u);
+    const uint32_t x_row = DE ? (uint32_t)a.E * 4u : 4u, b_row = (uint32_t)a.d * 2u;
+    uint32_t x_at = DE ? (own < a.E ? (uint32_t)own * 4u : 0x80000000u) : (uint32_t)own * (uint32_t)a.E * 4u;
+    uint32_t b_at = (uint32_t)col * 2u;
+    x_at += (uint32_t)(first + 8 * half) * x_row;
+    b_at += (uint32_t)(first + 8 * half) * b_row;
+    float v[8];
+    uint32_t w[8];
+    auto load = [&]() {
+        if constexpr (VEC && !DE) {
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+                const v4f q = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(x_rsrc, x_at + j * 4, 0, 0));
+                v[j] = q.x; v[j + 1] = q.y; v[j + 2] = q.z; v[j + 3] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(x_rsrc, x_at + j * x_row, 0, 0));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = __builtin_amdgcn_raw_buffer_load_b32(b_rsrc, b_at + j * b_row, 0, 0);
+        x_at += (uint32_t)step * x_row;
+        b_at += (uint32_t)step * b_row;
+    };
+    load();
+    for (int k = first; k < over; k += step) {
+        if constexpr (!DE) {                          // past its last expert a row goes on with the next one
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = k + 8 * half + j < a.E ? v[j] : 0.0f;
+        }
+        v8bf x[3];
+        split8(v, x);
+        v4i even, odd;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            even[j] = (int)((w[2 * j] & 0xFFFFu) | w[2 * j + 1] << 16);
+            odd[j] = (int)(w[2 * j] >> 16 | (w[2 * j + 1] & 0xFFFF0000u));
+        }
+        load();                                       // past the end: zeros, from no memory
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[p], __builtin_bit_cast(v8bf, even), acc[0], 0, 0, 0);
+            acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[p], __builtin_bit_cast(v8bf, odd), acc[1], 0, 0, 0);
+        }
+    }
+}
+
+template <bool VEC>
+__global__ __launch_bounds__(64 * SMALL_WAVES) void logits_small_kernel(SmallArgs a) {
+    __shared__ v2f red[SMALL_WAVES][16][64];
+    const int lane = threadIdx.x & 63, half = lane >> 5, wave = (int)uni(threadIdx.x >> 6), columns = a.d / 64;
+    const bool is_de = (int)blockIdx.x >= a.du_blocks;
+    const int tile = is_de ? (int)blockIdx.x - a.du_blocks : (int)blockIdx.x * SMALL_WAVES + wave;
+    const int col = tile % columns * 64 + 2 * (lane & 31), row0 = tile / columns * 32;
+    // result i of 16: row 8 (i / 4) + 4 half + i % 4
+    auto put_row = [&](int i, v2f o, int rows, const float* in, float* out) {
+        const int row = row0 + 8 * (i / 4) + 4 * half + i % 4;
+        if (row >= rows) return;
+        const int64_t at = (int64_t)row * a.d + col;
+        if (in) o += *reinterpret_cast<const v2f*>(in + at);
+        *reinterpret_cast<v2f*>(out + at) = o;
+    };
+    v16f acc[2] = {};
+    if (!is_de) {
+        if (row0 >= a.T) return;
+        small_products<false, VEC>(a, row0, col, 0, 16, acc);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) put_row(i, v2f{acc[0][i], acc[1][i]}, a.T, a.du_in, a.du);
+        return;
+    }
+    const int parts = min((a.T + 15) / 16, SMALL_WAVES);
+    if (wave < parts) {
+        small_products<true, VEC>(a, row0, col, 16 * wave, 16 * SMALL_WAVES, acc);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) red[wave][i][lane] = v2f{acc[0][i], acc[1][i]};
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = wave; i < 16; i += SMALL_WAVES) {
+        v2f s = red[0][i][lane];
+        for (int k = 1; k < parts; ++k) s += red[k][i][lane];
+        put_row(i, s, a.E, a.de_in, a.de);
+    }
+}
+
 // de = de_in + the parts in order; n = E d values, a multiple of 4
 __global__ __launch_bounds__(256) void logits_sum_kernel(const float* __restrict__ part, int parts, int64_t n,
                                                          const float* in, float* out) {
@@ -345,6 +467,12 @@ __global__ __launch_bounds__(256) void logits_sum_kernel(const float* __restrict
     if (in) s += *reinterpret_cast<const v4f*>(in + at);
     *reinterpret_cast<v4f*>(out + at) = s;
 }
+
+// Both kinds of call timed on 34 sizes, us, small / large: 4096 x 1024 with 16, 64 and 256
+// experts 25 / 25, 26.5 / 26.5 and 33 / 42, 2048 x 2048 x 256 27 / 36, 512 x 7168 x 256
+// 25 / 32, 64 x 65536 x 8 12 / 18; past 2^22 1024 x 7168 x 64 25 / 24, 4096 x 2048 x 128
+// 53 / 44, 2048 x 7168 x 64 56 / 49; past 4096 tokens 8192 x 128 x 16 40 / 30.
+bool small_call(int64_t T, int d) { return T <= 4096 && T * d <= 1 << 22; }
 
 int padded_experts(int E) { return E <= 64 ? 64 : E <= 128 ? 128 : 256; }
 
@@ -392,12 +520,21 @@ void launch_all(const float* x, LogitsArgs& a, bool de, hipStream_t st) {
 }  // namespace
 
 size_t router_logits_backward_ws_bytes(int64_t T, int d, int E) {
-    return T == 0 ? 16 : plane_bytes(T, E) + (size_t)de_parts(T, d, E) * E * d * sizeof(float);
+    return T == 0 || small_call(T, d) ? 16 : plane_bytes(T, E) + (size_t)de_parts(T, d, E) * E * d * sizeof(float);
 }
 
 hipError_t launch_router_logits_backward(const float* dlogits, const uint16_t* u, const uint16_t* e, int64_t T, int d,
                                          int E, const float* du_in, const float* de_in, float* du, float* de, void* ws,
                                          hipStream_t st) {
+    if (T > 0 && small_call(T, d)) {
+        const int columns = d / 64, de_blocks = de ? (E + 31) / 32 * columns : 0;
+        const int du_blocks = du ? (int)(((T + 31) / 32 * columns + SMALL_WAVES - 1) / SMALL_WAVES) : 0;
+        const SmallArgs a{dlogits, u, e, (int)T, d, E, du_blocks, du_in, de_in, du, de};
+        hipLaunchKernelGGL(E % 4 ? logits_small_kernel<false> : logits_small_kernel<true>,
+                           dim3((unsigned)(du_blocks + de_blocks)), dim3(64 * SMALL_WAVES), 0,
+                           st, a);
+        return hipGetLastError();
+    }
     LogitsArgs a{};
     if (T > 0) {
         a.planes = static_cast<const char*>(ws);

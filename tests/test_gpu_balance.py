@@ -322,6 +322,22 @@ def test_logits_tokens(T):
         _check_logits(dl, u, e, du_in=_rand(_gen(1), T, d), de_in=_rand(_gen(2), E, d))
 
 
+@pytest.mark.parametrize("T", [4095, 4096, 4097, 4111, 4127, 4128, 4129, 4223, 4225, 5003])
+def test_logits_many_tokens(T):
+    """About the number of tokens from which on planes of x are written and the tokens split in parts."""
+    dev()
+    for E, d in ((1, 128), (8, 256), (61, 640), (64, 128), (65, 384), (128, 128), (129, 384), (256, 256), (200, 1280)):
+        say(f"  T={T} E={E} d={d}")
+        dl, u, e = _operands(T, d, E, seed=T)
+        _check_logits(dl, u, e, du_in=_rand(_gen(1), T, d), de_in=_rand(_gen(2), E, d))
+
+
+@pytest.mark.parametrize("T,d,E", [(33, 65536, 5), (584, 7168, 40), (586, 7168, 40), (2049, 2048, 30), (128, 32896, 3)])
+def test_logits_wide(T, d, E):
+    dev()
+    _check_logits(*_operands(T, d, E, seed=d))
+
+
 @pytest.mark.parametrize("T,d,E", [(4096, 7168, 256), (5003, 1152, 160), (300, 16384, 7), (20001, 256, 64), (70001, 128, 33)])
 def test_logits_large(T, d, E):
     dev()
@@ -351,7 +367,7 @@ def test_logits_past_32_bit_offsets():
     assert float((de[:, cols].to(F8) - xt @ uu).norm()) <= 1.5 * (3 * T) ** 0.5 * U * float((xt.abs() @ uu.abs()).norm())
 
 
-@pytest.mark.parametrize("T,d,E", [(300, 384, 61), (513, 256, 256), (64, 128, 16)])
+@pytest.mark.parametrize("T,d,E", [(300, 384, 61), (513, 256, 256), (64, 128, 16), (4300, 128, 61), (4300, 384, 200)])
 def test_logits_keep_all_bits(T, d, E):
     """One product to an output: the 32-bit logits come through with all their bits."""
     dev()
@@ -369,7 +385,7 @@ def test_logits_keep_all_bits(T, d, E):
     assert torch.equal(de, -2.0 * dl[row].t())
 
 
-@pytest.mark.parametrize("T,d,E", [(700, 256, 100), (3000, 128, 256)])
+@pytest.mark.parametrize("T,d,E", [(700, 256, 100), (3000, 128, 256), (4500, 128, 256), (9000, 256, 60)])
 def test_logits_whole_numbers(T, d, E):
     """Sums of whole numbers under 2^24 are exact in any order."""
     dev()
@@ -381,10 +397,11 @@ def test_logits_whole_numbers(T, d, E):
     assert torch.equal(du.to(F8), dl.to(F8) @ e.to(F8)) and torch.equal(de.to(F8), dl.to(F8).t().contiguous() @ u.to(F8))
 
 
-def test_logits_special_values():
+@pytest.mark.parametrize("T", [200, 4200])
+def test_logits_special_values(T):
     """NaN and infinite logits reach their row of du and their row of de, and nothing else."""
     dev()
-    T, d, E = 200, 256, 70
+    d, E = 256, 70
     dl, u, e = _operands(T, d, E)
     want = moe.moe_router_logits_backward(dl, u, e)
     bad = dl.clone()
@@ -404,7 +421,8 @@ def test_logits_special_values():
     assert (du.abs() <= 1e-36).all()
 
 
-def test_logits_no_tokens_one_output_and_in_place():
+@pytest.mark.parametrize("T", [300, 4300])
+def test_logits_no_tokens_one_output_and_in_place(T):
     dev()
     d, E = 256, 20
     dl, u, e = _operands(0, d, E)
@@ -412,8 +430,8 @@ def test_logits_no_tokens_one_output_and_in_place():
     du, de = moe.moe_router_logits_backward(dl, u, e)
     assert du.shape == (0, d) and (de == 0).all()
     assert torch.equal(moe.moe_router_logits_backward(dl, u, e, de_in=add)[1], add)
-    dl, u, e = _operands(300, d, E)
-    du_in = _rand(_gen(2), 300, d)
+    dl, u, e = _operands(T, d, E)
+    du_in = _rand(_gen(2), T, d)
     want = moe.moe_router_logits_backward(dl, u, e, du_in=du_in, de_in=add)
     only = moe.moe_router_logits_backward(dl, u, e, du_in=du_in, want_de=False)
     assert only[1] is None and torch.equal(only[0], want[0])
@@ -425,7 +443,8 @@ def test_logits_no_tokens_one_output_and_in_place():
     assert got[0] is a and got[1] is b and torch.equal(a, want[0]) and torch.equal(b, want[1])
 
 
-@pytest.mark.parametrize("T,d,E", [(1, 128, 1), (45, 256, 33), (97, 384, 70), (130, 128, 129), (161, 256, 200)])
+@pytest.mark.parametrize("T,d,E", [(1, 128, 1), (45, 256, 33), (97, 384, 70), (130, 128, 129), (161, 256, 200),
+                                   (4097, 128, 1), (4129, 256, 33), (4225, 384, 70), (4131, 128, 129), (4161, 256, 200)])
 def test_logits_operands_inside_a_buffer(T, d, E):
     """Nothing around the operands is read (there are NaN) and nothing around the outputs written."""
     dev()
@@ -468,9 +487,10 @@ def test_logits_against_differences():
         assert abs(ne - float((de.to(F8) * ve).sum())) <= 1e-6 * float((de.to(F8) * ve).abs().sum())
 
 
-def test_logits_on_another_stream_and_in_a_graph():
+@pytest.mark.parametrize("T", [700, 4700])
+def test_logits_on_another_stream_and_in_a_graph(T):
     dev()
-    T, d, E = 700, 384, 61
+    d, E = 384, 61
     dl, u, e = _operands(T, d, E)
     du_in, de_in = _rand(_gen(1), T, d), _rand(_gen(2), E, d)
 
