@@ -122,7 +122,7 @@ __global__ __launch_bounds__(256) void seq_balance_final_kernel(const BalancePar
 // its counts as record c + q: along the chunks and sequences that meet, c + q grows
 // at every step, so no two runs share a record.  The chunk's counts over its runs
 // are kept too.  A second launch adds up each sequence's records, and the chunks'
-// counts.  Every order is fixed by the sizes and the starts.
+// counts.  Small calls take one launch, a block to a sequence.  Every order is fixed by the sizes and the starts.
 
 constexpr int RUN_WAVES = 16;
 constexpr int RUN_CHUNKS = 256;     // at most: one block per CU
@@ -197,14 +197,58 @@ constexpr int AT_ONCE = 4;          // tokens whose loads go out together
 // four indexes at a time, and 16 lanes a token with 16 values each (half the
 // instructions) all leave it at that.
 
+template <int LPT> struct RunLds {
+    static constexpr int GROUPS = 64 * RUN_WAVES / LPT, WIDE = 4 * LPT;
+    int cnt[256];
+    float psum[GROUPS][WIDE];
+};
+
+// The sums of the shares p of the tokens [rb, re) of one sequence and their counts, by a
+// block of RUN_WAVES waves: thread = expert e < E has them afterwards.
+template <int LPT, bool VEC>
+__device__ __forceinline__ void run_sums(const float* __restrict__ s, const int32_t* __restrict__ idx, int rb, int re,
+                                         int E, int K, RunLds<LPT>& lds, float& sum, int& count) {
+    constexpr int GROUPS = RunLds<LPT>::GROUPS;
+    const int tid = threadIdx.x, l = tid % LPT, grp = tid / LPT;
+    if (tid < 256) lds.cnt[tid] = 0;
+    __syncthreads();
+    for (int64_t i = (int64_t)rb * K + tid; i < (int64_t)re * K; i += 64 * RUN_WAVES) {
+        const int e = idx[i];
+        if ((unsigned)e < (unsigned)E) atomicAdd(&lds.cnt[e], 1);          // integers: exact in any order
+    }
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int t = rb + grp; t < re; t += AT_ONCE * GROUPS) {
+        float v[AT_ONCE][4];
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k)
+            load_experts<LPT, VEC>(s + (int64_t)(t + k * GROUPS) * E, l, E, t + k * GROUPS < re, v[k]);
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) {
+            float p[4];
+            shares<LPT>(v[k], p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] += p[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) lds.psum[grp][expert_of<LPT, VEC>(l, j)] = acc[j];
+    __syncthreads();
+    if (tid < E) {
+        float p[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int g = 0; g < GROUPS; g += 4)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] += lds.psum[g + i][tid];
+        sum = (p[0] + p[1]) + (p[2] + p[3]);
+        count = lds.cnt[tid];
+    }
+}
+
 template <int LPT, bool VEC>
 __global__ __launch_bounds__(64 * RUN_WAVES) void balance_runs_kernel(
     const float* __restrict__ s, const int32_t* __restrict__ idx, const int32_t* __restrict__ start, int n_seq, int T,
     int E, int K, int chunk, BalanceRun* __restrict__ rec, int32_t* __restrict__ chunk_n) {
-    constexpr int GROUPS = 64 * RUN_WAVES / LPT, WIDE = 4 * LPT;
-    __shared__ int cnt[256];
-    __shared__ float psum[GROUPS][WIDE];
-    const int tid = threadIdx.x, l = tid % LPT, grp = tid / LPT;
+    __shared__ RunLds<LPT> lds;
+    const int tid = threadIdx.x;
     const int tb = blockIdx.x * chunk, te = min(T, tb + chunk);
     int all = 0;                                      // thread = expert: counts over the chunk's runs
     for (int q = seq_of<64>(start, n_seq, T, tb); q < n_seq; ++q) {
@@ -214,41 +258,58 @@ __global__ __launch_bounds__(64 * RUN_WAVES) void balance_runs_kernel(
             q = max(q, seq_of<64>(start, n_seq, T, rb) - 1);
             continue;
         }
-        if (tid < 256) cnt[tid] = 0;
-        __syncthreads();
-        for (int64_t i = (int64_t)rb * K + tid; i < (int64_t)re * K; i += 64 * RUN_WAVES) {
-            const int e = idx[i];
-            if ((unsigned)e < (unsigned)E) atomicAdd(&cnt[e], 1);          // integers: exact in any order
-        }
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int t = rb + grp; t < re; t += AT_ONCE * GROUPS) {
-            float v[AT_ONCE][4];
-#pragma unroll
-            for (int k = 0; k < AT_ONCE; ++k)
-                load_experts<LPT, VEC>(s + (int64_t)(t + k * GROUPS) * E, l, E, t + k * GROUPS < re, v[k]);
-#pragma unroll
-            for (int k = 0; k < AT_ONCE; ++k) {
-                float p[4];
-                shares<LPT>(v[k], p);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[j] += p[j];
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) psum[grp][expert_of<LPT, VEC>(l, j)] = acc[j];
-        __syncthreads();
+        float p = 0.0f;
+        int n = 0;
+        run_sums<LPT, VEC>(s, idx, rb, re, E, K, lds, p, n);
         if (tid < E) {
-            float p[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int g = 0; g < GROUPS; g += 4)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) p[i] += psum[g + i][tid];
-            rec[blockIdx.x + q].p[tid] = (p[0] + p[1]) + (p[2] + p[3]);
-            rec[blockIdx.x + q].n[tid] = cnt[tid];
-            all += cnt[tid];
+            rec[blockIdx.x + q].p[tid] = p;
+            rec[blockIdx.x + q].n[tid] = n;
+            all += n;
         }
         __syncthreads();
     }
     if (tid < E) chunk_n[blockIdx.x * 256 + tid] = all;
+}
+
+// A sequence's count and loss from the sums over its L tokens: thread = expert, four
+// waves.
+__device__ __forceinline__ void finish_sequence(int e, float p, int n, int q, int L, int E, int K, float alpha,
+                                                float (&wave_term)[4], float* loss, int32_t* seq_count) {
+    if (e < E) seq_count[(int64_t)q * E + e] = n;
+    const float len = (float)max(L, 1), f = (float)E * (float)n / ((float)K * len);
+    const float term = wave_sum(f * (p / len));
+    if ((e & 63) == 0) wave_term[e >> 6] = term;
+    __syncthreads();
+    if (e == 0) loss[q] = alpha * ((wave_term[0] + wave_term[1]) + (wave_term[2] + wave_term[3]));
+}
+
+// Small calls in one launch: a block goes through a whole sequence, and one counts over
+// all of them.
+template <int LPT, bool VEC>
+__global__ __launch_bounds__(64 * RUN_WAVES) void balance_small_kernel(
+    const float* __restrict__ s, const int32_t* __restrict__ idx, const int32_t* __restrict__ start, int n_seq, int T,
+    int E, int K, float alpha, float* __restrict__ loss, int32_t* __restrict__ seq_count,
+    int32_t* __restrict__ expert_count) {
+    __shared__ RunLds<LPT> lds;
+    __shared__ float wave_term[4];
+    const int tid = threadIdx.x, q = blockIdx.x;
+    if (q == n_seq) {
+        if (tid < 256) lds.cnt[tid] = 0;
+        __syncthreads();
+        const int b = seq_start_at(start, 0, n_seq, T) * K, end = seq_start_at(start, n_seq, n_seq, T) * K;
+        for (int i = b + tid; i < end; i += 64 * RUN_WAVES) {
+            const int e = idx[i];
+            if ((unsigned)e < (unsigned)E) atomicAdd(&lds.cnt[e], 1);
+        }
+        __syncthreads();
+        if (tid < E) expert_count[tid] = lds.cnt[tid];
+        return;
+    }
+    const int b = seq_start_at(start, q, n_seq, T), L = max(seq_start_at(start, q + 1, n_seq, T) - b, 0);
+    float p = 0.0f;
+    int n = 0;
+    if (L > 0) run_sums<LPT, VEC>(s, idx, b, b + L, E, K, lds, p, n);
+    if (tid < 256) finish_sequence(tid, p, n, q, L, E, K, alpha, wave_term, loss, seq_count);
 }
 
 // The sum of x(c) for c = c0 + part, c0 + part + 4, .. up to c1, in that order, 16 loads
@@ -298,13 +359,8 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const BalanceRun* __r
     if (part) return;
     p = (ps[0][e] + ps[1][e]) + (ps[2][e] + ps[3][e]);
     n = (ns[0][e] + ns[1][e]) + (ns[2][e] + ns[3][e]);
-    if (e < E) seq_count[(int64_t)q * E + e] = n;
-    const float len = (float)max(L, 1), f = (float)E * (float)n / ((float)K * len);
-    const float term = wave_sum(f * (p / len));      // four waves are left
     __shared__ float wave_term[4];
-    if ((e & 63) == 0) wave_term[e >> 6] = term;
-    __syncthreads();
-    if (e == 0) loss[q] = alpha * ((wave_term[0] + wave_term[1]) + (wave_term[2] + wave_term[3]));
+    finish_sequence(e, p, n, q, L, E, K, alpha, wave_term, loss, seq_count);
 }
 
 // LPT lanes go through EACH consecutive tokens: their sequence is looked for once and
@@ -375,6 +431,18 @@ int balance_chunk(int64_t T) {
 
 }  // namespace
 
+// One launch, or two: a block takes 16 tokens at a time (64 of up to 64 experts), 16 rounds
+// of which take as long as the second launch; the starts are not known here, so the
+// longest sequence is taken for all of a few tokens, or for twice to four times the mean
+// of a few more.  Kernels, us, one / two: 300 x 61 in 7 sequences 3.7 / 8.5, 1024 x 64 in
+// one 7.8 / 7.8, 2048 x 64 in one 13.0 / 7.9 and in 8 4.4 / 8.0, 512 x 256 in one 13.5 /
+// 8.4, in 4 5.3 / 7.6 and in 512 4.2 / 89, 1024 x 256 in 64 3.8 / 12.5, 2048 x 256 in 4
+// 13.6 / 8.7.
+bool small_call(int64_t T, int n_seq, int E) {
+    const int64_t few = E > 64 ? 256 : 1024;
+    return T <= few || (T <= 8 * few && T <= n_seq * (few / 2));
+}
+
 size_t balance_loss_ws_bytes(int64_t T, int n_seq) {
     const int64_t chunk = balance_chunk(T);
     const int64_t chunks = (T + chunk - 1) / chunk;
@@ -384,6 +452,13 @@ size_t balance_loss_ws_bytes(int64_t T, int n_seq) {
 hipError_t launch_balance_loss(const float* s, const int32_t* idx, const int32_t* start, int n_seq, int64_t T, int E,
                                int K, float alpha, float* loss, int32_t* seq_count, int32_t* expert_count, void* ws,
                                hipStream_t st) {
+    if (T > 0 && small_call(T, n_seq, E)) {
+        const auto small = E > 64 ? E % 4 ? balance_small_kernel<64, false> : balance_small_kernel<64, true>
+                                  : E % 4 ? balance_small_kernel<16, false> : balance_small_kernel<16, true>;
+        hipLaunchKernelGGL(small, dim3(n_seq + (expert_count ? 1 : 0)), dim3(64 * RUN_WAVES), 0, st, s, idx, start, n_seq,
+                           (int)T, E, K, alpha, loss, seq_count, expert_count);
+        return hipGetLastError();
+    }
     BalanceRun* rec = static_cast<BalanceRun*>(ws);
     const int chunk = balance_chunk(T), chunks = (int)((T + chunk - 1) / chunk);
     int32_t* chunk_n = reinterpret_cast<int32_t*>(rec + chunks + n_seq);
