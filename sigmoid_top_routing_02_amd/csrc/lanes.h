@@ -26,6 +26,15 @@ __device__ __forceinline__ float wave_sum(float s) {
     const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(s), __float_as_uint(s), false, false);
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
+// over each L = 16, 32 or 64 lanes
+template <int L>
+__device__ __forceinline__ float lanes_sum(float s) {
+    if constexpr (L == 64) return wave_sum(s);
+    s = sum16(s);
+    if constexpr (L == 16) return s;
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(s), __float_as_uint(s), false, false);
+    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
 __device__ __forceinline__ float max16(float m) {     // a NaN counts as less than anything
     float o = dpp<0xB1>(m);
     m = o > m ? o : m;

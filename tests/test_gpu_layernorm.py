@@ -89,6 +89,44 @@ def test_forward_widths(d):
         _check_forward(x, res, w, None if T == 3 else b, quant=d % 128 == 0)
 
 
+# every start of a row in its 16 bytes; lanes to a row 16, 32, 64 and a block, up to the last width of each; many turns
+SHIFTED = [(1, 1), (1, 7), (7, 1), (2, 3), (3, 5), (37, 9), (100, 57), (5000, 61), (9, 121), (9, 122), (2001, 127), (20011, 65),
+           (300, 129), (70, 249), (70, 250), (9001, 255), (70, 505), (70, 506), (3001, 511), (50, 1017), (50, 1018), (2500, 1023),
+           (30, 2041), (1203, 2047), (20, 8185), (20, 8186), (700, 8191), (9, 16377), (9, 16378), (600, 16383), (131072 + 5, 67)]
+
+
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", SHIFTED)
+def test_rows_of_no_multiple_of_8(T, d, xt):
+    """Forward and backward, the operands between NaN, the outputs between guards."""
+    dev()
+    say(f"  T={T} d={d} {xt}")
+    pad = 1024
+
+    def inside(t):
+        big = torch.full((t.numel() + 2 * pad,), float("nan"), dtype=t.dtype, device="cuda")
+        big[pad:pad + t.numel()] = t.reshape(-1)
+        return big, big[pad:pad + t.numel()].view(t.shape)
+
+    def guarded(want, call):
+        outs = [inside(torch.zeros_like(t)) for t in want]
+        call([view for _, view in outs])
+        torch.cuda.synchronize()
+        for (big, view), t in zip(outs, want):
+            assert torch.equal(view, t) and torch.isnan(big[:pad]).all() and torch.isnan(big[pad + t.numel():]).all()
+
+    x, res, w, b = _inputs(T, d, xt, xt, "f32", seed=T + d)
+    want = _check_forward(x, res, w, b, quant=False)
+    hx, hres, hw, hb = (inside(t)[1] for t in (x, res, w, b))
+    guarded((want.h, want.y, want.mean, want.rstd), lambda o: moe.moe_add_layernorm(
+        hx, hw, EPS, bias=hb, residual=hres, h_out=o[0], y=o[1], mean=o[2], rstd=o[3]))
+    _check_backward(T, d, xt, xt, "f32", xt, seed=T + d)
+    dy, dh = _inputs(T, d, xt, xt, "f32", seed=1)[:2]
+    grads = moe.moe_add_layernorm_backward(dy, x, w, want.mean, want.rstd, dh=dh)
+    hdy, hx, hw, hm, hr, hdh = (inside(t)[1] for t in (dy, x, w, want.mean, want.rstd, dh))
+    guarded(grads, lambda o: moe.moe_add_layernorm_backward(hdy, hx, hw, hm, hr, dh=hdh, dx=o[0], dw=o[1], db=o[2]))
+
+
 @pytest.mark.parametrize("xt", ["bf16", "f32"])
 @pytest.mark.parametrize("rt", [None, "bf16", "f32"])
 @pytest.mark.parametrize("wt", ["bf16", "f32"])
