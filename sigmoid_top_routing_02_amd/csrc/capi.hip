@@ -677,8 +677,8 @@ int moe_wgrad_operands(const float* dh, const float* topk_gate, const int32_t* s
                        const int32_t* kb_start, int G, int n_kb, int64_t T, int K, int d, int I,
                        int64_t shared_row0, uint8_t* dyT_q, float* dyT_scale, uint8_t* hT_q, float* hT_scale,
                        uint8_t* dzT_q, float* dzT_scale, uint8_t* xT_q, float* xT_scale, moe_stream_t stream) {
-    return wgrad_operands(__func__, dh, topk_gate, slot_row, row_token, z, nullptr, nullptr, dh_row, u_bf16, group_offset, kb_start, G, n_kb, T, K, d, I,
-                          shared_row0, dyT_q, dyT_scale, hT_q, hT_scale, dzT_q, dzT_scale, xT_q, xT_scale, stream);
+    return wgrad_operands(__func__, dh, topk_gate, slot_row, row_token, z, nullptr, nullptr, dh_row, u_bf16,
+                          group_offset, kb_start, G, n_kb, T, K, d, I, shared_row0, dyT_q, dyT_scale, hT_q, hT_scale, dzT_q, dzT_scale, xT_q, xT_scale, stream);
 }
 
 int moe_wgrad_operands_zq(const float* dh, const float* topk_gate, const int32_t* slot_row, const int32_t* row_token,
@@ -687,8 +687,8 @@ int moe_wgrad_operands_zq(const float* dh, const float* topk_gate, const int32_t
                        int64_t shared_row0, uint8_t* dyT_q, float* dyT_scale, uint8_t* hT_q, float* hT_scale,
                        uint8_t* dzT_q, float* dzT_scale, uint8_t* xT_q, float* xT_scale, moe_stream_t stream) {
     if (n_kb > 0) REQUIRE_PTR(z_q);
-    return wgrad_operands(__func__, dh, topk_gate, slot_row, row_token, nullptr, z_q, z_scale, dh_row, u_bf16, group_offset, kb_start, G, n_kb, T, K, d, I,
-                          shared_row0, dyT_q, dyT_scale, hT_q, hT_scale, dzT_q, dzT_scale, xT_q, xT_scale, stream);
+    return wgrad_operands(__func__, dh, topk_gate, slot_row, row_token, nullptr, z_q, z_scale, dh_row, u_bf16,
+                          group_offset, kb_start, G, n_kb, T, K, d, I, shared_row0, dyT_q, dyT_scale, hT_q, hT_scale, dzT_q, dzT_scale, xT_q, xT_scale, stream);
 }
 
 size_t moe_wgrad_workspace_bytes(int G, int d, int I) {

@@ -334,7 +334,8 @@ __global__ __launch_bounds__(MAXT, NV == 2 ? 4 : 1) void add_layernorm_kernel(Ad
 // leaves a thread no registers for them (4096 rows of 16384 bf16 values
 // with dh: 116 us, in registers that spill 183 to 250).
 template <int NV, bool VEC, int LPR, bool NT, bool BF, bool AHEAD, bool IN_LDS, int MAXT>
-__global__ __launch_bounds__(MAXT, VEC || IN_LDS ? 1 : LPR || !BF ? 4 : 5) void add_layernorm_backward_kernel(AddLayernormBackwardArgs a) {
+__global__ __launch_bounds__(MAXT, VEC || IN_LDS ? 1 : LPR || !BF ? 4 : 5) void add_layernorm_backward_kernel(
+    AddLayernormBackwardArgs a) {
     __shared__ v4f kept[IN_LDS ? NV * 4 * MAXT : 1];  // [v][dw, db][half of 8][thread]
     auto sums = [&](int v, int which, int half) -> v4f& { return kept[((v * 2 + which) * 2 + half) * MAXT + (int)threadIdx.x]; };
     __shared__ float part[2][2][16];
@@ -517,15 +518,17 @@ int backward_threads(int d) {
 }
 
 // As many blocks as the card holds (24 waves of 8 values a thread to a CU, 16 of those
-// with a shift or with sums in LDS), which keeps the partial rows few: 8192 rows of 7168 bf16 values with
-// dh on 256 / 512 blocks 110 / 115 us, 16384 of 5120 156 / 136.
+// with a shift or with sums in LDS), which keeps the partial rows few: 8192 rows of 7168
+// bf16 values with dh on 256 / 512 blocks 110 / 115 us, 16384 of 5120 156 / 136.
 // Narrow rows: 512 wide on 768 / 1024 blocks 89 / 94 us, in FP32 176 / 185; with a shift
 // the registers are held to what lets four waves on a SIMD (67 wide on 1024 blocks 176, 768
 // 196; in FP32 343 without that, 279 with), and of a block's rows in bf16 five (2055 wide
 // 195 -> 124).
 int backward_most(int d) {
     const int n = span(d), waves = (n + 511) / 512;
-    return n <= 512 ? (d % 8 ? 1024 : 768) : n <= backward_narrow(d) ? MOST_PARTIAL_ROWS : n <= 8192 ? 256 * ((d % 8 ? 16 : 24) / waves) : 256;
+    if (n <= 512) return d % 8 ? 1024 : 768;
+    if (n <= backward_narrow(d)) return MOST_PARTIAL_ROWS;
+    return n <= 8192 ? 256 * ((d % 8 ? 16 : 24) / waves) : 256;
 }
 
 // Functions of the sizes alone, so the bits of dw and db are too.  A multiple of 8 where
