@@ -164,8 +164,8 @@ int moe_seq_balance_loss(const float* scores, const int32_t* topk_idx, int64_t T
  * loss FP32 [n_seq], seq_count int32 [n_seq,E], expert_count int32 [E] or NULL;
  * dloss FP32 [n_seq], the gradient of each loss (NULL: ones); dlogits_in FP32 [T,E]
  * (NULL: zeros), dlogits FP32 [T,E], which may be dlogits_in itself.  ws: scratch of
- * moe_balance_loss_workspace_bytes(T, n_seq) bytes, no setup needed.  T = 0 gives
- * zeros.  Nothing is read back to the host, so both calls can be captured in a graph
+ * moe_balance_loss_workspace_bytes(T, n_seq) bytes, no setup needed; where that is 16
+ * (small calls) none is taken and ws may be NULL.  T = 0 gives zeros.  Nothing is read back to the host, so both calls can be captured in a graph
  * whose replays take other starts.
  * Limits: 0 <= T <= 2^30, 1 <= n_seq <= 2^20, 1 <= E <= 256, 1 <= K <= min(E, 16).
  */
@@ -188,8 +188,9 @@ int moe_balance_loss_backward(const float* scores, const int32_t* seq_count, con
  * as the sum of three bf16 that it is) and they are summed in FP32 in an order that
  * depends on T, d and E alone; what is under the smallest normal FP32 number counts as
  * zero, and infinite values of u or the centroids may give NaN.  ws: scratch of
- * moe_router_logits_backward_workspace_bytes(T, d, E) bytes (no setup needed; may be
- * NULL when T = 0): at most 6 bytes for each logit, and partial sums of de.
+ * moe_router_logits_backward_workspace_bytes(T, d, E) bytes (no setup needed): 6 bytes
+ * for each logit, and partial sums of de; where that is 16 (small calls) none is taken
+ * and ws may be NULL.
  * Limits: 0 <= T <= 2^24, d % 128 == 0, d <= 65536, 1 <= E <= 256.
  */
 size_t moe_router_logits_backward_workspace_bytes(int64_t T, int d, int E);   /* 0 outside the limits */

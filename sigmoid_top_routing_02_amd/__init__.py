@@ -912,7 +912,9 @@ BalanceLoss = namedtuple("BalanceLoss", "loss seq_count expert_count")
 
 
 def _scratch(ws, nbytes, dev):
-    """(tensor, address, bytes) of a call's scratch, allocated where none is given."""
+    """(tensor, address, bytes) of a call's scratch, allocated where one is needed and not given."""
+    if ws is None and nbytes == 16:                   # the call takes none
+        return None, None, 0
     if ws is None:
         ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
         return ws, ws.data_ptr(), max(nbytes, 16)

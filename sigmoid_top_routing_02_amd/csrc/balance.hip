@@ -444,6 +444,7 @@ bool small_call(int64_t T, int n_seq, int E) {
 }
 
 size_t balance_loss_ws_bytes(int64_t T, int n_seq) {
+    if (small_call(T, n_seq, 256)) return 16;         // whatever E: small with 256 experts is small with fewer
     const int64_t chunk = balance_chunk(T);
     const int64_t chunks = (T + chunk - 1) / chunk;
     return (size_t)(chunks + n_seq) * sizeof(BalanceRun) + (size_t)chunks * 256 * sizeof(int32_t);
@@ -452,7 +453,7 @@ size_t balance_loss_ws_bytes(int64_t T, int n_seq) {
 hipError_t launch_balance_loss(const float* s, const int32_t* idx, const int32_t* start, int n_seq, int64_t T, int E,
                                int K, float alpha, float* loss, int32_t* seq_count, int32_t* expert_count, void* ws,
                                hipStream_t st) {
-    if (T > 0 && small_call(T, n_seq, E)) {
+    if (small_call(T, n_seq, E)) {
         const auto small = E > 64 ? E % 4 ? balance_small_kernel<64, false> : balance_small_kernel<64, true>
                                   : E % 4 ? balance_small_kernel<16, false> : balance_small_kernel<16, true>;
         hipLaunchKernelGGL(small, dim3(n_seq + (expert_count ? 1 : 0)), dim3(64 * RUN_WAVES), 0, st, s, idx, start, n_seq,
@@ -464,9 +465,8 @@ hipError_t launch_balance_loss(const float* s, const int32_t* idx, const int32_t
     int32_t* chunk_n = reinterpret_cast<int32_t*>(rec + chunks + n_seq);
     const auto runs = E > 64 ? E % 4 ? balance_runs_kernel<64, false> : balance_runs_kernel<64, true>
                              : E % 4 ? balance_runs_kernel<16, false> : balance_runs_kernel<16, true>;
-    if (T > 0)
-        hipLaunchKernelGGL(runs, dim3(chunks), dim3(64 * RUN_WAVES), 0, st, s, idx, start, n_seq, (int)T, E, K, chunk, rec,
-                           chunk_n);
+    hipLaunchKernelGGL(runs, dim3(chunks), dim3(64 * RUN_WAVES), 0, st, s, idx, start, n_seq, (int)T, E, K, chunk, rec,
+                       chunk_n);
     hipLaunchKernelGGL(balance_sum_kernel, dim3(n_seq + (expert_count ? 1 : 0)), dim3(1024), 0, st, rec, chunk_n, start,
                        n_seq, (int)T, E, K, chunk, alpha, loss, seq_count, expert_count);
     return hipGetLastError();

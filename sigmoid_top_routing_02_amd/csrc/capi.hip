@@ -44,6 +44,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 inline hipStream_t S(moe_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
 
+constexpr size_t NO_SCRATCH = 16;      // what the workspace sizes are for calls that take none
 constexpr int64_t BALANCE_MAX_T = (int64_t)1 << 30;
 constexpr int BALANCE_MAX_SEQ = 1 << 20;
 constexpr int64_t LOGITS_MAX_T = (int64_t)1 << 24;
@@ -167,9 +168,11 @@ int moe_balance_loss(const float* scores, const int32_t* topk_idx, const int32_t
         REQUIRE_PTR(scores);
         REQUIRE_PTR(topk_idx);
     }
-    REQUIRE_PTR(ws);
-    REQUIRE(ws_bytes >= moe::balance_loss_ws_bytes(T, n_seq), MOE_ERR_WORKSPACE,
-            "moe_balance_loss: workspace of %zu bytes, %zu needed", ws_bytes, moe::balance_loss_ws_bytes(T, n_seq));
+    const size_t need = moe::balance_loss_ws_bytes(T, n_seq);
+    if (need > NO_SCRATCH) {
+        REQUIRE_PTR(ws);
+        REQUIRE(ws_bytes >= need, MOE_ERR_WORKSPACE, "moe_balance_loss: workspace of %zu bytes, %zu needed", ws_bytes, need);
+    }
     return hip_status(moe::launch_balance_loss(scores, topk_idx, seq_start, n_seq, T, E, K, alpha, loss, seq_count,
                                                expert_count, ws, S(stream)),
                       "balance loss launch");
@@ -218,10 +221,12 @@ int moe_router_logits_backward(const float* dlogits, const void* u_bf16, const v
     }
     if (T > 0) {
         REQUIRE_PTR(dlogits);
-        REQUIRE_PTR(ws);
-        REQUIRE(ws_bytes >= moe::router_logits_backward_ws_bytes(T, d, E), MOE_ERR_WORKSPACE,
-                "moe_router_logits_backward: workspace %zu < %zu bytes", ws_bytes,
-                moe::router_logits_backward_ws_bytes(T, d, E));
+        const size_t need = moe::router_logits_backward_ws_bytes(T, d, E);
+        if (need > NO_SCRATCH) {
+            REQUIRE_PTR(ws);
+            REQUIRE(ws_bytes >= need, MOE_ERR_WORKSPACE, "moe_router_logits_backward: workspace %zu < %zu bytes", ws_bytes,
+                    need);
+        }
     }
     if (T == 0 && !de) return MOE_OK;
     return hip_status(moe::launch_router_logits_backward(dlogits, static_cast<const uint16_t*>(u_bf16),

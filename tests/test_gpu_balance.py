@@ -539,7 +539,7 @@ def test_binding_refusals():
         lambda: moe.moe_balance_loss(scores, idx, ALPHA, seq_start=start[:1]),
         lambda: moe.moe_balance_loss(scores, idx, ALPHA, seq_start=start.cpu()),
         lambda: moe.moe_balance_loss(scores[:, ::2], idx, ALPHA),
-        lambda: moe.moe_balance_loss(scores, idx, ALPHA, ws=small),
+        lambda: moe.moe_balance_loss(scores.repeat(64, 1), idx.repeat(64, 1), ALPHA, ws=small),
         lambda: moe.moe_balance_loss(scores[:, :3].contiguous(), idx, ALPHA),           # K above E
         lambda: moe.moe_balance_loss(torch.zeros((4, 257), device="cuda"), idx[:4], ALPHA),
         lambda: moe.moe_balance_loss_backward(scores, r.seq_count, 0, ALPHA),
