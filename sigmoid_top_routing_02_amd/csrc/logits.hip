@@ -457,13 +457,37 @@ __global__ __launch_bounds__(64 * SMALL_WAVES) void logits_small_kernel(SmallArg
     }
 }
 
-// de = de_in + the parts in order; n = E d values, a multiple of 4
+// de = de_in + the parts; n = E d values, a multiple of 4.  SPLIT = 1: a thread adds up all
+// parts of its four values; 4: four waves every fourth part each, eight loads at a time,
+// for more than 8 parts (us, 1 / 4: 8689 x 256 x 94 in 69 parts 19 / 4, 8192 x 2048 x 128 in
+// 32 10 / 7, 16384 x 7168 x 256 in 4 7 / 13).
+template <int SPLIT>
 __global__ __launch_bounds__(256) void logits_sum_kernel(const float* __restrict__ part, int parts, int64_t n,
                                                          const float* in, float* out) {
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (at >= n) return;
+    constexpr int WIDE = 256 / SPLIT;
+    const int own = threadIdx.x % WIDE, first = threadIdx.x / WIDE;
+    const int64_t at = ((int64_t)blockIdx.x * WIDE + own) * 4;
     v4f s = {0.f, 0.f, 0.f, 0.f};
-    for (int p = 0; p < parts; ++p) s += *reinterpret_cast<const v4f*>(part + p * n + at);
+    if (at < n) {
+        for (int p = first; p < parts; p += 8 * SPLIT) {
+            v4f x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (SPLIT > 1 || p + i < parts)
+                    x[i] = *reinterpret_cast<const v4f*>(part + (int64_t)min(p + SPLIT * i, parts - 1) * n + at);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (p + SPLIT * i < parts) s += x[i];
+        }
+    }
+    if constexpr (SPLIT > 1) {
+        __shared__ v4f red[SPLIT][WIDE];
+        red[first][own] = s;
+        __syncthreads();
+        if (first) return;
+        s = (red[0][own] + red[1][own]) + (red[2][own] + red[3][own]);
+    }
+    if (at >= n) return;
     if (in) s += *reinterpret_cast<const v4f*>(in + at);
     *reinterpret_cast<v4f*>(out + at) = s;
 }
@@ -480,13 +504,13 @@ int64_t token_chunks(int64_t T) { return (T + CHUNK - 1) / CHUNK; }
 
 size_t plane_bytes(int64_t T, int E) { return (size_t)token_chunks(T) * 3 * CHUNK * padded_experts(E) * 2; }
 
-// 32-token chunks that a block of de takes: about one block to a CU, and four chunks at
-// least.
+// 32-token chunks that a block of de takes: about one block to a CU, and two chunks at
+// least (7680 x 128 x 1: 7 us, with four 9).
 int de_chunks(int64_t T, int d, int E) {
     const int64_t blocks = (int64_t)((d + 255) / 256) * (padded_experts(E) > 128 ? 2 : 1);
     const int64_t chunks = token_chunks(T), parts = 256 / blocks < 1 ? 1 : 256 / blocks;
     const int64_t each = (chunks + parts - 1) / parts;
-    return (int)(each < 4 ? 4 : each);
+    return (int)(each < 2 ? 2 : each);
 }
 
 int de_parts(int64_t T, int d, int E) {
@@ -550,8 +574,10 @@ hipError_t launch_router_logits_backward(const float* dlogits, const uint16_t* u
     }
     if (de) {
         const int64_t n = (int64_t)E * d;
-        hipLaunchKernelGGL(logits_sum_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, a.part, a.de_parts, n,
-                           de_in, de);
+        const bool split = a.de_parts > 8;
+        const int64_t wide = split ? 64 : 256;
+        hipLaunchKernelGGL(split ? logits_sum_kernel<4> : logits_sum_kernel<1>, dim3((unsigned)((n / 4 + wide - 1) / wide)),
+                           dim3(256), 0, st, a.part, a.de_parts, n, de_in, de);
     }
     return hipGetLastError();
 }
