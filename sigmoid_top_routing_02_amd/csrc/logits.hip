@@ -345,9 +345,10 @@ __global__ __launch_bounds__(256, 2) void logits_kernel(LogitsArgs a) {
 // du takes 32 tokens by 64 columns over all experts; a block of de 32 experts by 64
 // columns, its eight waves every eighth 16 tokens, added up through LDS in order.  The
 // fragments come straight from global memory, and x is split where it is used.  Bound by
-// latency and by the launch: 64 x 512 x 8 5 us (three launches 10), 1031 x 640 x 61 12 (16),
+// latency and by the launch: 64 x 512 x 8 5 us (three launches 10), 1031 x 640 x 61 10 (16),
 // 512 x 7168 x 64 13 (18), 1024 x 4096 x 256 26 (33).  Loads two steps ahead instead of one:
-// 12, 16 and more of the larger.
+// 512 x 7168 x 64 16.  x's rows of no multiple of 4 experts by single values: 65 x 896 x 221
+// 24, four at a time 13.
 constexpr int SMALL_WAVES = 8;
 struct SmallArgs {
     const float* x;
@@ -380,10 +381,11 @@ __device__ __forceinline__ void small_products(const SmallArgs& a, int row0, int
     float v[8];
     uint32_t w[8];
     auto load = [&]() {
-        if constexpr (VEC && !DE) {
+        if constexpr (VEC && !DE) {                   // four at a time, the tensor's last ones early where need be
+            const uint32_t last = ((uint32_t)a.T * (uint32_t)a.E - 4u) * 4u;
 #pragma unroll
             for (int j = 0; j < 8; j += 4) {
-                const v4f q = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(x_rsrc, x_at + j * 4, 0, 0));
+                const v4f q = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(x_rsrc, min(x_at + j * 4, last), 0, 0));
                 v[j] = q.x; v[j + 1] = q.y; v[j + 2] = q.z; v[j + 3] = q.w;
             }
         } else {
@@ -398,9 +400,22 @@ __device__ __forceinline__ void small_products(const SmallArgs& a, int row0, int
     };
     load();
     for (int k = first; k < over; k += step) {
-        if constexpr (!DE) {                          // past its last expert a row goes on with the next one
+        if constexpr (!DE) {
+            if (VEC && (a.T - row0 - 32) * a.E < 16) { // what was read early, by that many values
+                const int room = (a.T - min(own, a.T)) * a.E - k - 8 * half;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = k + 8 * half + j < a.E ? v[j] : 0.0f;
+                for (int j = 0; j < 8; j += 4) {
+                    const int early = 4 + j - room;
+#pragma unroll
+                    for (int s = 2; s > 0; s >>= 1)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[j + i] = early <= 0 || !(early & s) ? v[j + i] : i + s < 4 ? v[j + i + s] : 0.0f;
+                }
+            }
+            // past its last expert a row goes on with the next one, and past the last row is none
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = own < a.T && k + 8 * half + j < a.E ? v[j] : 0.0f;
         }
         v8bf x[3];
         split8(v, x);
@@ -528,7 +543,11 @@ void launch_all(const float* x, LogitsArgs& a, bool de, hipStream_t st) {
     if (a.du) {
         const int64_t along = (token_chunks(a.T) + 3) / 4;
         const int steps = a.d / 64;
-        int64_t split = (512 + along - 1) / along;
+        // two blocks to a CU in all, de's among them; of up to 64 experts du is most of it
+        // and waits for memory alone (256 / 512 blocks, us: 5000 x 1152 x 160 36 / 44, 8192 x
+        // 2048 x 128 63 / 76, 16384 x 7168 x 256 401 / 405, but 8988 x 6272 x 4 142 / 126)
+        const int64_t blocks = de && EP > 64 ? 256 : 512;
+        int64_t split = (blocks + along - 1) / along;
         split = split < steps ? split : steps;
         a.du_steps = (int)((steps + split - 1) / split);
         a.du_split = (steps + a.du_steps - 1) / a.du_steps;
@@ -554,7 +573,7 @@ hipError_t launch_router_logits_backward(const float* dlogits, const uint16_t* u
         const int columns = d / 64, de_blocks = de ? (E + 31) / 32 * columns : 0;
         const int du_blocks = du ? (int)(((T + 31) / 32 * columns + SMALL_WAVES - 1) / SMALL_WAVES) : 0;
         const SmallArgs a{dlogits, u, e, (int)T, d, E, du_blocks, du_in, de_in, du, de};
-        hipLaunchKernelGGL(E % 4 ? logits_small_kernel<false> : logits_small_kernel<true>,
+        hipLaunchKernelGGL(T * E < 4 ? logits_small_kernel<false> : logits_small_kernel<true>,
                            dim3((unsigned)(du_blocks + de_blocks)), dim3(64 * SMALL_WAVES), 0,
                            st, a);
         return hipGetLastError();
