@@ -434,10 +434,10 @@ int balance_chunk(int64_t T) {
 // One launch, or two: a block takes 16 tokens at a time (64 of up to 64 experts), 16 rounds
 // of which take as long as the second launch; the starts are not known here, so the
 // longest sequence is taken for all of a few tokens, or for twice the mean of up to four
-// times as many (1024 x 256 in one of many sequences costs 24 for 8.5).  Kernels, us, one / two: 300 x 61 in 7 sequences 3.7 / 8.5, 1024 x 64 in
-// one 7.8 / 7.8, 2048 x 64 in one 13.0 / 7.9 and in 8 4.4 / 8.0, 512 x 256 in one 13.5 /
-// 8.4, in 4 5.3 / 7.6 and in 512 4.2 / 89, 1024 x 256 in 64 3.8 / 12.5, 2048 x 256 in 4
-// 13.6 / 8.7.
+// times as many (1024 x 256 in one of many sequences costs 24 for 8.5).  Kernels, us, one /
+// two: 300 x 61 in 7 sequences 3.7 / 8.5, 1024 x 64 in one 7.8 / 7.8, 2048 x 64 in one 13.0
+// / 7.9 and in 8 4.4 / 8.0, 512 x 256 in one 13.5 / 8.4, in 4 5.3 / 7.6 and in 512 4.2 /
+// 89, 1024 x 256 in 64 3.8 / 12.5, 2048 x 256 in 4 13.6 / 8.7.
 bool small_call(int64_t T, int n_seq, int E) {
     const int64_t few = E > 64 ? 256 : 1024;
     return T <= few || (T <= 4 * few && T <= n_seq * (few / 2));
