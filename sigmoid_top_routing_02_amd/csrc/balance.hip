@@ -367,17 +367,19 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const BalanceRun* __r
 // followed from there, its f kept as long as it lasts.  Bound by HBM: 131072 x 256 in 96
 // sequences 45 us (5.9 TB/s), 16384 x 256 in 4 10, four dependent reads long before a
 // token's sequence is known (the starts held by lane where they are few: the same; 8
-// tokens a lane: 46).
-constexpr int EACH = 4;
+// tokens a lane: 46).  Tokens that would take 2^32 threads (2^28 of more than 64 experts,
+// 2^30 of fewer) go in several launches, by block0 (stepping by the grid instead: 131072 x
+// 256 3 us more).
+constexpr int EACH = BALANCE_EACH;
 
 template <int LPT, bool VEC, bool NT>
 __global__ __launch_bounds__(256) void balance_backward_kernel(
     const float* __restrict__ s, const int32_t* __restrict__ seq_count, const int32_t* __restrict__ start, int n_seq,
-    int T, int E, int K, float alpha, const float* __restrict__ dloss, const float* in, float* out) {
+    int T, int E, int K, float alpha, const float* __restrict__ dloss, const float* in, float* out, unsigned block0) {
     constexpr int GROUPS = 256 / LPT;
     typedef float v4f __attribute__((ext_vector_type(4)));
     const int l = threadIdx.x % LPT;
-    const int64_t first = ((int64_t)blockIdx.x * GROUPS + threadIdx.x / LPT) * EACH;
+    const int64_t first = ((int64_t)(block0 + blockIdx.x) * GROUPS + threadIdx.x / LPT) * EACH;
     if (first >= T) return;                           // whole groups of lanes
     const int t0 = (int)first, te = min(T, t0 + EACH);
     int q = -1, qb = 0, qe = 0;                       // the sequence that holds the last token looked at, or none yet
@@ -475,16 +477,18 @@ hipError_t launch_balance_loss(const float* s, const int32_t* idx, const int32_t
 hipError_t launch_balance_loss_backward(const float* s, const int32_t* seq_count, const int32_t* start, int n_seq,
                                         int64_t T, int E, int K, float alpha, const float* dloss, const float* in,
                                         float* out, hipStream_t st) {
-    const int lanes = E > 64 ? 64 : 16;
-    const int64_t each = (int64_t)EACH * 256 / lanes;
     const bool nt = streamed(T * E * 4);
     const auto kernel = E > 64 ? E % 4 ? nt ? balance_backward_kernel<64, false, true> : balance_backward_kernel<64, false, false>
                                        : nt ? balance_backward_kernel<64, true, true> : balance_backward_kernel<64, true, false>
                                : E % 4 ? nt ? balance_backward_kernel<16, false, true> : balance_backward_kernel<16, false, false>
                                        : nt ? balance_backward_kernel<16, true, true> : balance_backward_kernel<16, true, false>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((T + each - 1) / each)), dim3(256), 0, st, s, seq_count, start, n_seq, (int)T, E,
-                       K, alpha, dloss, in, out);
-    return hipGetLastError();
+    for (int64_t from = 0; from < T; from += balance_backward_tokens(E)) {
+        hipLaunchKernelGGL(kernel, dim3(balance_backward_blocks(T - from, E)), dim3(256), 0, st, s, seq_count, start, n_seq,
+                           (int)T, E, K, alpha, dloss, in, out, (unsigned)(from / balance_block_tokens(E)));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 size_t seq_balance_ws_bytes(int64_t n_seq, int L) {

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "launch.h"
+
 namespace moe {
 
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
@@ -24,12 +26,5 @@ __device__ __forceinline__ void put(T* p, T v) {
 // 7 MiB 21.2 / 20.2, 56 MiB 73.7 / 71.3, alone with 896 MiB 746 / 769, and with
 // rows of 512 values and 128 MiB 87 / 117.
 inline bool streamed(int64_t bytes) { return bytes > ((int64_t)64 << 20); }
-
-// Blocks of a launch that has work for `want` blocks: a launch is held under 2^32
-// threads, and kernels whose work may pass that go on in steps of the grid.
-inline unsigned launch_blocks(int64_t want, int threads) {
-    const int64_t most = 0xFFFFFFFFll / threads;
-    return (unsigned)(want < most ? want : most);
-}
 
 }  // namespace moe
