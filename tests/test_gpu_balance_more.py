@@ -45,3 +45,47 @@ def test_gradient_past_a_launch(T, E):
         part = grad[a:a + n]
         rows = n // B * B
         assert (part[:rows].view(-1, B, E) == first).all() and torch.equal(part[rows:], first[:n - rows]), a
+
+
+@pytest.mark.parametrize("T", [300, 4500])
+@pytest.mark.parametrize("E", [2, 16, 64, 65, 128, 191, 256])
+def test_shares_are_rounded_once(T, E):
+    """Scores of ten bits, so that a token's sum is exact, and sequences of one token with one expert each: with
+    alpha 1 the loss is E p of that expert, and the gradient p (1 - s) (f - E p), each rounded where FP32
+    arithmetic rounds it, from p rounded once."""
+    dev()
+    say(f"  T={T} E={E}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + E)
+    scores = torch.randint(1, 1024, (T, E), generator=g, device="cuda").float() / 1024
+    idx = torch.randint(0, E, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    start = torch.arange(T + 1, dtype=torch.int32, device="cuda")
+    r = moe.moe_balance_loss(scores, idx, 1.0, seq_start=start)
+    grad = moe.moe_balance_loss_backward(scores, r.seq_count, 1, 1.0, seq_start=start)
+    torch.cuda.synchronize()
+    p = (scores.to(F8) / scores.to(F8).sum(1, keepdim=True)).float()      # 53 bits and then 24 round as 24 at once
+    want = E * p.gather(1, idx.long())                                     # a product of FP32: one rounding
+    assert torch.equal(r.loss, want[:, 0])
+    f = torch.zeros((T, E), device="cuda").scatter_(1, idx.long(), float(E))
+    assert torch.equal(grad, (p * (1.0 - scores)) * (f - want))
+
+
+def test_shares_of_tiny_and_uneven_scores():
+    """Sums down to the smallest number, shares down to 2^-60: relative to the 64-bit ones, the sum's roundings
+    (8 of them for 128 experts) and one of the quotient."""
+    dev()
+    T, E = 512, 128
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    scores = torch.rand((T, E), generator=g, device="cuda") + 0.5
+    scores[:, 1:] *= torch.exp2(-60.0 * torch.rand((T, E - 1), generator=g, device="cuda"))
+    scores *= torch.exp2(-torch.arange(T, device="cuda") * (60.0 / T))[:, None]
+    scores[::8] = torch.rand((T // 8, E), generator=g, device="cuda") * 2.0 ** -100
+    scores[5], scores[7] = 2.0 ** -149, 0.0
+    idx = torch.randint(0, E, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    start = torch.arange(T + 1, dtype=torch.int32, device="cuda")
+    loss = moe.moe_balance_loss(scores, idx, 1.0, seq_start=start).loss
+    torch.cuda.synchronize()
+    s = scores.to(F8)
+    want = E * (s / s.sum(1, keepdim=True)).nan_to_num().gather(1, idx.long())[:, 0]
+    assert ((loss.to(F8) - want).abs() <= 9 * U * want).all() and loss[7] == 0 and loss[5] == 1
