@@ -206,10 +206,11 @@ __device__ __forceinline__ void quant_nt8(const float (&v)[8], int part, uint8_t
     if (part == 0) *sp = sc;
 }
 
-__global__ __launch_bounds__(256) void swiglu_backward_zq_kernel(const uint8_t* __restrict__ z_q,
-                                                                 const float* __restrict__ z_s,
+// (dz_q may be z_q and dz_s z_s: a lane's loads of a tile are before its stores to it, and
+// the scale is stored by one of the lanes that loaded it together.)
+__global__ __launch_bounds__(256) void swiglu_backward_zq_kernel(const uint8_t* z_q, const float* z_s,
                                                                  const float* __restrict__ dh_row, int64_t R, int I,
-                                                                 uint8_t* __restrict__ dz_q, float* __restrict__ dz_s) {
+                                                                 uint8_t* dz_q, float* dz_s) {
     const int nb = I / 128;
     const int64_t total = R * nb * 16;
     for (int64_t gi = (int64_t)blockIdx.x * 256 + threadIdx.x; gi - threadIdx.x < total;
