@@ -568,17 +568,17 @@ def moe_wgrad_zq(dh, topk_gate, slot_row, row_token, z_q, z_scale, dh_row, u, gr
     [R, 2I/128]; the operands come from moe_wgrad_operands_zq."""
     if z_q.dim() != 2:
         raise MoEError(f"z_q: shape {tuple(z_q.shape)}, expected two dimensions")
-    R, I2 = z_q.shape
-    _want(z_q, torch.uint8, (R, I2), "z_q")
-    _want(z_scale, torch.float32, (R, I2 // 128), "z_scale")
-    _want(dh_row, torch.float32, (R, I2 // 2), "dh_row")
-    T, d = dh.shape
-    K = topk_gate.shape[1]
-    _want(dh, torch.float32, (T, d), "dh")
-    _want(u, torch.bfloat16, (T, d), "u")
-    _want(topk_gate, torch.float32, (T, K), "topk_gate")
-    _want(slot_row, torch.int32, (T, K), "slot_row")
-    _want(row_token, torch.int32, (R,), "row_token")
+    if dh.dim() != 2 or topk_gate.dim() != 2:
+        raise MoEError(f"dh: {tuple(dh.shape)}, topk_gate: {tuple(topk_gate.shape)}, expected [T, d] and [T, K]")
+    (R, I2), (T, d), K = z_q.shape, dh.shape, topk_gate.shape[1]
+    dev = _current(z_q, "z_q")
+    for t, dtype, shape, name in (
+            (z_q, torch.uint8, (R, I2), "z_q"), (z_scale, torch.float32, (R, I2 // 128), "z_scale"),
+            (dh_row, torch.float32, (R, I2 // 2), "dh_row"), (dh, torch.float32, (T, d), "dh"),
+            (u, torch.bfloat16, (T, d), "u"), (topk_gate, torch.float32, (T, K), "topk_gate"),
+            (slot_row, torch.int32, (T, K), "slot_row"), (row_token, torch.int32, (R,), "row_token"),
+            (group_offset, torch.int32, group_offset.shape, "group_offset")):
+        _in(t, dtype, shape, name, dev)
     return _wgrad(dh, topk_gate, slot_row, row_token, z_q, z_scale, dh_row, u, group_offset, shared_row0)
 
 
