@@ -424,7 +424,7 @@ __global__ __launch_bounds__(MAXT, VEC || IN_LDS ? 1 : LPR || !BF ? 4 : 5) void 
             s0 = lanes_sum<LPR>(s0);
             s1 = lanes_sum<LPR>(s1);
         } else {
-            row_sum2<false>(s0, s1, part[flip]);
+            row_sum2(s0, s1, part[flip]);
         }
         const float c0 = s0 / (float)d, c1 = s1 / (float)d;
 #pragma unroll

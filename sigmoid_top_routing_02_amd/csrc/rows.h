@@ -139,12 +139,10 @@ __device__ __forceinline__ float row_sum(float s, float (*part)[16], int flip) {
     return s;
 }
 
-// Two such sums at once, the waves' by wave_sum.
-template <bool WAVE_ROW>
+// Two such sums at once over a block's row, the waves' by wave_sum.
 __device__ __forceinline__ void row_sum2(float& a, float& b, float (*part)[16]) {
     a = wave_sum(a);
     b = wave_sum(b);
-    if constexpr (WAVE_ROW) return;
     if ((threadIdx.x & 63) == 0) {
         part[0][threadIdx.x >> 6] = a;
         part[1][threadIdx.x >> 6] = b;
