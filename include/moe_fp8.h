@@ -153,6 +153,7 @@ int moe_seq_balance_loss(const float* scores, const int32_t* topk_idx, int64_t T
  *   expert_count[i] = sum_q seq_count[q,i]   (what moe_bias_update takes)
  *   dlogits[t,i] = dlogits_in[t,i] + dloss[q] * alpha / L_q * p[t,i] * (1 - scores[t,i])
  *                  * (f[q,i] - sum_j f[q,j] p[t,j])
+ * (exactly dlogits_in where a sequence's experts are chosen equally often).
  * The counts are held fixed in the gradient, as the choice of the experts is
  * elsewhere.  Tokens before seq_start[0] and from seq_start[n_seq] on (padding) are
  * in no sequence: not counted, and dlogits = dlogits_in there.  moe_seq_balance_loss

@@ -20,6 +20,8 @@
 // order).  The chunk's partial P and counts go to the workspace.  Pass 2: one
 // block per sequence adds the chunks in order and reduces the E terms by a
 // fixed tree.
+#include <limits.h>
+
 #include "kernels.h"
 #include "lanes.h"
 #include "streaming.h"
@@ -380,6 +382,10 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const BalanceRun* __r
 // tokens a lane: 46).  Tokens that would take 2^32 threads (2^28 of more than 64 experts,
 // 2^30 of fewer) go in several launches, by block0 (stepping by the grid instead: 131072 x
 // 256 3 us more).
+//
+// f is taken from the sequence's least one on, f_i = E (n_i - min n) / (K L), which leaves
+// f_i - sum_j f_j p_j as it is (sum p = 1) and holds its error to what the f are apart: use
+// that is even gives zeros.
 constexpr int EACH = BALANCE_EACH;
 
 template <int LPT, bool VEC, bool NT>
@@ -411,11 +417,16 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(
                 qe = q < n_seq ? seq_start_at(start, q + 1, n_seq, T) : T;
                 const float len = (float)max(qe - qb, 1), per = (float)E / ((float)K * len);
                 coef = q < n_seq ? (dloss ? dloss[q] : 1.0f) * alpha / len : 0.0f;
+                int n[4], least = INT_MAX;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int e = expert_of<LPT, VEC>(l, j);
-                    f[j] = q < n_seq && e < E ? per * (float)seq_count[(int64_t)q * E + e] : 0.0f;
+                    n[j] = q < n_seq && e < E ? seq_count[(int64_t)q * E + e] : INT_MAX;
+                    least = min(least, n[j]);
                 }
+                least = lanes_min<LPT>(least);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = n[j] == INT_MAX ? 0.0f : per * (float)(n[j] - least);
             }
             float p[4], o[4];
             shares<LPT>(v[k], p);

@@ -46,6 +46,23 @@ __device__ __forceinline__ float max16(float m) {     // a NaN counts as less th
     return o > m ? o : m;
 }
 
+// the least over each L = 16 or 64 lanes
+template <int L>
+__device__ __forceinline__ int lanes_min(int m) {
+    auto with = [&](int o) { m = o < m ? o : m; };
+    with(__builtin_amdgcn_update_dpp(m, m, 0xB1, 0xf, 0xf, false));       // the lanes of sum16
+    with(__builtin_amdgcn_update_dpp(m, m, 0x4E, 0xf, 0xf, false));
+    with(__builtin_amdgcn_update_dpp(m, m, 0x141, 0xf, 0xf, false));
+    with(__builtin_amdgcn_update_dpp(m, m, 0x140, 0xf, 0xf, false));
+    if constexpr (L == 64) {
+        const auto a = __builtin_amdgcn_permlane16_swap((unsigned)m, (unsigned)m, false, false);
+        m = (int)a[0] < (int)a[1] ? (int)a[0] : (int)a[1];
+        const auto b = __builtin_amdgcn_permlane32_swap((unsigned)m, (unsigned)m, false, false);
+        m = (int)b[0] < (int)b[1] ? (int)b[0] : (int)b[1];
+    }
+    return m;
+}
+
 // the largest of lanes l, l ^ 16, l ^ 32 and l ^ 48 (of no NaN)
 __device__ __forceinline__ float max_of_rows(float m) {
     const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);

@@ -89,3 +89,33 @@ def test_shares_of_tiny_and_uneven_scores():
     s = scores.to(F8)
     want = E * (s / s.sum(1, keepdim=True)).nan_to_num().gather(1, idx.long())[:, 0]
     assert ((loss.to(F8) - want).abs() <= 9 * U * want).all() and loss[7] == 0 and loss[5] == 1
+
+
+@pytest.mark.parametrize("E,K", [(2, 2), (5, 5), (8, 8), (12, 3), (64, 4), (65, 5), (96, 8), (256, 16)])
+def test_gradient_of_even_use(E, K):
+    """Experts chosen equally often (all of them, or in turn) have the same f, and f - sum f p is 0 as sum p = 1:
+    the gradient is the one added to, bit for bit.  Where one expert is chosen a little more often, the gradient's
+    error goes by how far the f are apart, not by their size (48 roundings, as in the other tests)."""
+    dev()
+    say(f"  E={E} K={K}")
+    L = E * 7
+    starts = [0, E, E + L, E + L, 2 * E + 2 * L]
+    T = starts[-1] + 3
+    g = torch.Generator(device="cuda")
+    g.manual_seed(E)
+    scores = torch.sigmoid(2.0 * torch.randn((T, E), generator=g, device="cuda"))
+    idx = ((torch.arange(T, device="cuda")[:, None] * K + torch.arange(K, device="cuda")) % E).to(torch.int32)
+    start = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    r = moe.moe_balance_loss(scores, idx, 1.0, seq_start=start)
+    assert (r.seq_count == torch.tensor([[K], [7 * K], [0], [8 * K]], dtype=torch.int32, device="cuda")).all()
+    add = torch.randn((T, E), generator=g, device="cuda")
+    assert (moe.moe_balance_loss_backward(scores, r.seq_count, K, 1.0, seq_start=start) == 0).all()
+    assert torch.equal(moe.moe_balance_loss_backward(scores, r.seq_count, K, 1.0, seq_start=start, dlogits_in=add), add)
+    n = 1000000 + torch.randint(0, 3, (1, E), generator=g, device="cuda", dtype=torch.int32)
+    grad = moe.moe_balance_loss_backward(scores, n, K, 1.0)
+    torch.cuda.synchronize()
+    s = scores.to(F8)
+    f = (n - n.min()).to(F8) * E / (K * T)
+    p = s / s.sum(1, keepdim=True)
+    coef, fp = p * (1.0 - s) / T, (f * p).sum(1, keepdim=True)
+    assert ((grad.to(F8) - coef * (f - fp)).abs() <= 48 * U * coef * (f + fp)).all()
