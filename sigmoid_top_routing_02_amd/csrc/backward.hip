@@ -181,8 +181,11 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(const float* __res
 // element is loaded and stored past the caches, a thread takes one group (a grid of
 // 65536 blocks that came round: 446 us against 429, plain loads and stores of z and dz
 // 429 against 414), and quantising is kept to few instructions (with clamps and LDS
-// shuffles 503 us against 446).  16 values a lane, whose loads of dh lie 64 bytes
-// apart, 608 us; 4 a lane 465.  147456 x 2048: 414 us, 5.9 TB/s (from FP32 z 850).
+// shuffles 503 us against 446).  The sigmoid is the FP32 form's, by the hardware's exp2
+// and reciprocal, so that both give the same codes: of 6.0e8 codes 843 to 868 are not those
+// of 64 bits, where a division and a rounded exponential leave 846 to 882.  16 values a
+// lane, whose loads of dh lie 64 bytes apart, 608 us; 4 a lane 465.  147456 x 2048: 398 to
+// 414 us, 5.9 TB/s (from FP32 z 850).
 typedef uint32_t bwd_v2u __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ void decode8(const uint8_t* p, float s, float (&v)[8]) {
     const bwd_v2u c = __builtin_nontemporal_load(reinterpret_cast<const bwd_v2u*>(p));

@@ -205,7 +205,7 @@ __device__ __forceinline__ void shares(const float (&v)[4], float (&p)[4]) {
 constexpr int AT_ONCE = 4;          // tokens whose loads go out together
 
 // Bound by the latency of HBM reads: 131072 x 256 with 8 experts a token in 96 sequences
-// 31 us (4.4 TB/s), 16384 x 256 in 4 7.  The next four tokens' loads ahead of the sums,
+// 30 us (4.6 TB/s), 16384 x 256 in 4 7.  The next four tokens' loads ahead of the sums,
 // four indexes at a time, and 16 lanes a token with 16 values each (half the
 // instructions) all leave it at that.
 
@@ -377,7 +377,7 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const BalanceRun* __r
 
 // LPT lanes go through EACH consecutive tokens: their sequence is looked for once and
 // followed from there, its f kept as long as it lasts.  Bound by HBM: 131072 x 256 in 96
-// sequences 45 us (5.9 TB/s), 16384 x 256 in 4 10, four dependent reads long before a
+// sequences 44 us (6.1 TB/s), 16384 x 256 in 4 10, four dependent reads long before a
 // token's sequence is known (the starts held by lane where they are few: the same; 8
 // tokens a lane: 46).  Tokens that would take 2^32 threads (2^28 of more than 64 experts,
 // 2^30 of fewer) go in several launches, by block0 (stepping by the grid instead: 131072 x
@@ -460,7 +460,9 @@ int balance_chunk(int64_t T) {
 // times as many (1024 x 256 in one of many sequences costs 24 for 8.5).  Kernels, us, one /
 // two: 300 x 61 in 7 sequences 3.7 / 8.5, 1024 x 64 in one 7.8 / 7.8, 2048 x 64 in one 13.0
 // / 7.9 and in 8 4.4 / 8.0, 512 x 256 in one 13.5 / 8.4, in 4 5.3 / 7.6 and in 512 4.2 /
-// 89, 1024 x 256 in 64 3.8 / 12.5, 2048 x 256 in 4 13.6 / 8.7.
+// 89, 1024 x 256 in 64 3.8 / 12.5, 2048 x 256 in 4 13.6 / 8.7.  Past the limit many short
+// sequences, which a block goes through one after the other, cost most: 1000 x 256 in 512
+// 4.6, 1100 46, 3000 in 500 24, 4097 in as many 105.
 bool small_call(int64_t T, int n_seq, int E) {
     const int64_t few = E > 64 ? 256 : 1024;
     return T <= few || (T <= 4 * few && T <= n_seq * (few / 2));

@@ -328,11 +328,13 @@ __device__ __forceinline__ void de_block(const LogitsArgs& a, int block, char* l
 
 // de's blocks go first, one to a CU, and du's beside them: while du waits for memory, de
 // multiplies.  16384 x 7168 x 256, added in: 360 GFLOP of products (three for each of the
-// FP32 ones) and 1.2 GB, 370 to 400 us with the split (9) and the sum (8), the matrix units
-// busy 61% of the cycles at the 1.5 GHz that the power leaves them: 0.97 PFLOP/s, where a
-// plain bf16 product reaches 1.26 to 1.43.  du and de each in a launch of its own: 404.  On
-// one box, 401 as here: de's blocks after du's 443, eight of each in turn 434, twice the
-// parts of de 408.
+// FP32 ones) and 1.2 GB, 360 to 400 us with the split (9) and the sum (8): 0.97 PFLOP/s,
+// where a plain bf16 product reaches 1.26 to 1.43.  The matrix units' cycles
+// take 143 us at 2.4 GHz and 190 at the 1.81 read while calls follow each other (the plain
+// product's clock: 1.92), of 345: power is a part of what bounds it, waits are more.  It
+// reads 1043 MiB of 700, as the columns' blocks lie across the XCDs and each XCD reads
+// all planes.  du and de each in a launch of its own: 404.  On one box, 401 as here: de's
+// blocks after du's 443, eight of each in turn 434, twice the parts of de 408.
 template <int EP, bool ADD, bool NT>
 __global__ __launch_bounds__(256, 2) void logits_kernel(LogitsArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[LDS_BYTES];

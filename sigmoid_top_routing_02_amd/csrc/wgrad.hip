@@ -63,8 +63,10 @@ __device__ __forceinline__ float row_weight(const WgradSrc& s, int64_t r, int64_
 
 // z's 4 values at column `at` of row r, from FP32 or (ZQ) from 8 bits: of the 147456
 // rows of a 16384-token layer with I = 2048 the operand h^T takes 394 us from 8 bits and
-// 517 from FP32, dz^T 893 and 1104 (of dz^T's sources dh, read by the blocks of both
-// halves, is the larger part by then).
+// 517 from FP32, dz^T 893 and 1104.  Their bytes would take 145 and 385 at 6.3 TB/s:
+// the blocks of dz^T's gate and up halves each read both of z's and dh, and h^T's time is
+// not its bytes at all (its columns' maxima come one after the other from LDS, and two
+// blocks fit a CU; not timed apart).
 template <bool ZQ> struct Z4 {
     float4 v;
     __device__ __forceinline__ void load(const WgradSrc& s, int64_t r, int at) {
